@@ -5,125 +5,20 @@
 // preserve caller device/stream ownership, 64-bit addressing), graph-capture
 // rejection (PR 5282, Scope), launch planning and stream-ordered scratch.
 #include "mqa_fp4_topk.h"
+#include "mqa_host.h"
 #include "mqa_launch.h"
 
 #include <hip/hip_runtime.h>
 
-#include <cstring>
 #include <mutex>
 
 namespace {
 
 using mqa::PathArgs;
+using namespace mqa::host;
 
-constexpr int kMaxDevices = 64;
 constexpr int kRowsPerCta = 8;       // must match the kernels' row tile
 constexpr int kMaxAutoSplits = 64;
-
-struct DeviceInfo {
-  bool probed = false;
-  bool gfx950 = false;
-  int cus = 0;
-  bool pool_ready = false;
-};
-
-std::mutex g_mu;
-DeviceInfo g_dev[kMaxDevices];
-
-// Probes (once) whether `dev` is a gfx950 and how many CUs it has.
-int32_t device_info(int dev, DeviceInfo* out) {
-  if (dev < 0 || dev >= kMaxDevices) return MQA_ERR_DEVICE;
-  std::lock_guard<std::mutex> lk(g_mu);
-  DeviceInfo& d = g_dev[dev];
-  if (!d.probed) {
-    hipDeviceProp_t prop;
-    if (hipGetDeviceProperties(&prop, dev) != hipSuccess) {
-      (void)hipGetLastError();
-      return MQA_ERR_HIP;
-    }
-    d.gfx950 = std::strncmp(prop.gcnArchName, "gfx950", 6) == 0;
-    d.cus = prop.multiProcessorCount;
-    d.probed = true;
-  }
-  if (!d.pool_ready && d.gfx950) {
-    // keep freed scratch in the device's default pool instead of returning it
-    hipMemPool_t pool;
-    if (hipDeviceGetDefaultMemPool(&pool, dev) == hipSuccess) {
-      uint64_t thr = ~0ull;
-      (void)hipMemPoolSetAttribute(pool, hipMemPoolAttrReleaseThreshold, &thr);
-    }
-    (void)hipGetLastError();
-    d.pool_ready = true;
-  }
-  *out = d;
-  return d.gfx950 ? MQA_OK : MQA_ERR_DEVICE;
-}
-
-// Restores the caller's current device on scope exit.
-struct DeviceGuard {
-  int saved = -1;
-  bool changed = false;
-  int32_t enter(int dev) {
-    if (hipGetDevice(&saved) != hipSuccess) {
-      (void)hipGetLastError();
-      return MQA_ERR_HIP;
-    }
-    if (saved != dev) {
-      if (hipSetDevice(dev) != hipSuccess) {
-        (void)hipGetLastError();
-        return MQA_ERR_HIP;
-      }
-      changed = true;
-    }
-    return MQA_OK;
-  }
-  ~DeviceGuard() {
-    if (changed) (void)hipSetDevice(saved);
-  }
-};
-
-int32_t stream_device(hipStream_t st, int* dev) {
-  const bool ok = (st == nullptr ? hipGetDevice(dev) : hipStreamGetDevice(st, dev)) == hipSuccess;
-  if (!ok) (void)hipGetLastError();   // reported through the return code only
-  return ok ? MQA_OK : st == nullptr ? MQA_ERR_HIP : MQA_ERR_DEVICE;
-}
-
-// A non-null pointer must be device (or managed) memory of device `dev`.
-int32_t check_ptr_device(const void* p, int dev) {
-  if (p == nullptr) return MQA_OK;
-  hipPointerAttribute_t attr;
-  std::memset(&attr, 0, sizeof(attr));
-  if (hipPointerGetAttributes(&attr, p) != hipSuccess) {
-    (void)hipGetLastError();
-    return MQA_ERR_DEVICE;
-  }
-  if (attr.type != hipMemoryTypeDevice && attr.type != hipMemoryTypeManaged) return MQA_ERR_DEVICE;
-  if (attr.device != dev) return MQA_ERR_DEVICE;
-  return MQA_OK;
-}
-
-struct PtrSpec {
-  const void* p;
-  bool required;
-  uintptr_t align;
-};
-
-// Host-only pointer checks (no HIP call): presence and alignment.
-int32_t check_ptrs_host(const PtrSpec* specs, int n) {
-  for (int i = 0; i < n; ++i)
-    if (specs[i].required && specs[i].p == nullptr) return MQA_ERR_NULL_POINTER;
-  for (int i = 0; i < n; ++i)
-    if (specs[i].p && reinterpret_cast<uintptr_t>(specs[i].p) % specs[i].align) return MQA_ERR_MISALIGNED;
-  return MQA_OK;
-}
-
-int32_t check_ptrs_device(const PtrSpec* specs, int n, int dev) {
-  for (int i = 0; i < n; ++i) {
-    const int32_t rc = check_ptr_device(specs[i].p, dev);
-    if (rc != MQA_OK) return rc;
-  }
-  return MQA_OK;
-}
 
 int32_t check_sizes(int64_t Q, int64_t P_phys, int64_t P_log) {
   if (Q < 0 || P_phys < 0 || P_log < 0) return MQA_ERR_BAD_SIZE;
@@ -131,15 +26,6 @@ int32_t check_sizes(int64_t Q, int64_t P_phys, int64_t P_log) {
   if (P_log > (0x7FFFFFFFll - 512) / 64) return MQA_ERR_BAD_SIZE; // positions in int32
   if (P_phys > 0x7FFFFFFFll / 64) return MQA_ERR_BAD_SIZE;        // slots in int32
   return MQA_OK;
-}
-
-int32_t check_capture(hipStream_t st) {
-  hipStreamCaptureStatus cs = hipStreamCaptureStatusNone;
-  if (hipStreamIsCapturing(st, &cs) != hipSuccess) {
-    (void)hipGetLastError();
-    return MQA_ERR_HIP;
-  }
-  return cs == hipStreamCaptureStatusNone ? MQA_OK : MQA_ERR_CAPTURING;
 }
 
 // Context splits per row tile: enough CTAs for `per_cu` of them per CU.
@@ -199,26 +85,6 @@ FusedScratch fused_scratch_layout(int64_t Q, int32_t K) {
   return s;
 }
 
-// Common entry checks; on success the guard holds the tensors' device.
-// Order: host-only checks first (testable without a GPU), then device checks.
-int32_t enter(hipStream_t st, const PtrSpec* specs, int nspecs, DeviceGuard& guard, DeviceInfo* info,
-              bool allow_capture = false) {
-  int32_t rc = check_ptrs_host(specs, nspecs);
-  if (rc != MQA_OK) return rc;
-  int dev = -1;
-  rc = stream_device(st, &dev);
-  if (rc != MQA_OK) return rc;
-  if (!allow_capture) {
-    rc = check_capture(st);
-    if (rc != MQA_OK) return rc;
-  }
-  rc = device_info(dev, info);
-  if (rc != MQA_OK) return rc;
-  rc = check_ptrs_device(specs, nspecs, dev);
-  if (rc != MQA_OK) return rc;
-  return guard.enter(dev);
-}
-
 // Stream-ordered scratch for one call.
 struct Scratch {
   void* p = nullptr;
@@ -243,12 +109,6 @@ thread_local void* const* t_stage_events = nullptr;
 
 void record_stage(int i, hipStream_t st) {
   if (t_stage_events) (void)hipEventRecord(static_cast<hipEvent_t>(t_stage_events[i]), st);
-}
-
-int32_t hip_rc(hipError_t e) {
-  if (e == hipSuccess) return MQA_OK;
-  (void)hipGetLastError();
-  return MQA_ERR_HIP;
 }
 
 // Scratch of the allocation-free entry point: one fixed array per device, held
@@ -695,6 +555,7 @@ const char* mqa_fp4_error_string(int32_t code) {
     case MQA_ERR_CAPTURING: return "stream is capturing a graph (not supported)";
     case MQA_ERR_HIP: return "HIP runtime error";
     case MQA_ERR_BAD_FLAGS: return "unknown flag bits";
+    case MQA_ERR_UNSUPPORTED: return "unsupported type or head dimension";
     default: return "unknown error";
   }
 }
