@@ -20,7 +20,7 @@ MQA_OK = 0
 ERRORS = {
     -1: "MQA_ERR_UNSUPPORTED_K", -2: "MQA_ERR_NULL_POINTER", -3: "MQA_ERR_MISALIGNED",
     -4: "MQA_ERR_BAD_SIZE", -5: "MQA_ERR_DEVICE", -6: "MQA_ERR_CAPTURING", -7: "MQA_ERR_HIP",
-    -8: "MQA_ERR_BAD_FLAGS",
+    -8: "MQA_ERR_BAD_FLAGS", -9: "MQA_ERR_UNSUPPORTED",
 }
 ROW_BAD_WINDOW, ROW_BAD_PAGE, ROW_UNDERFILL, ROW_SELECTOR = -1, -2, -3, -4
 STATUS_BAD_WINDOW, STATUS_BAD_PAGE, STATUS_UNDERFILL, STATUS_SELECTOR = 1, 2, 4, 8
@@ -29,6 +29,25 @@ FLAG_NO_PREFILTER = 0x100
 FLAG_FORCE_UNDERFILL = 0x200
 FLAG_NO_FALLBACK = 0x400
 STATIC_SCRATCH_BYTES = 64 << 20          # MQA_STATIC_SCRATCH_BYTES
+KV_MAX_ARRAYS = 8                        # MQA_KV_MAX_ARRAYS
+
+
+class _KvCache(ctypes.Structure):        # mqa_kv_cache
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_stride", ctypes.c_int64 * 3),
+                ("v_stride", ctypes.c_int64 * 3), ("num_phys_pages", ctypes.c_int64),
+                ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("type", ctypes.c_int32),
+                ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float)]
+
+
+class _KvQuery(ctypes.Structure):        # mqa_kv_query
+    _fields_ = [("q", ctypes.c_void_p), ("row_stride", ctypes.c_int64), ("num_rows", ctypes.c_int64),
+                ("num_heads", ctypes.c_int32), ("type", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class _KvArray(ctypes.Structure):        # mqa_kv_array
+    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("src_stride", ctypes.c_int64 * 3),
+                ("dst_stride", ctypes.c_int64 * 3), ("row_bytes", ctypes.c_int64),
+                ("rows_per_position", ctypes.c_int64)]
 
 
 class MQAError(RuntimeError):
@@ -77,6 +96,20 @@ def lib() -> ctypes.CDLL:
         L.mqa_fp4_decode_workspace_bytes.argtypes = [i64, i32, i32, i32]
         L.mqa_fp4_decode_workspace_bytes.restype = i64
         L.mqa_fp4_cache_write.argtypes = [P, i64, P, P, i64, i64, P, P, P]
+        L.mqa_kv_attention_decode.argtypes = [P, P, P, i64, i64, P, P, P, P, P, P, i64, P]
+        L.mqa_kv_attention_decode_workspace_bytes.argtypes = [i64, i32, i32, i32]
+        L.mqa_kv_attention_selected.argtypes = [P, P, P, P, i64, P, P, P, i64, P]
+        L.mqa_kv_attention_selected_workspace_bytes.argtypes = [i64, i64, i32, i32, i32]
+        L.mqa_kv_weights_accumulate.argtypes = [P, P, P, P, i64, i64, P, P, P, P, i64, P]
+        L.mqa_kv_evict_select.argtypes = [P, i64, P, i64, i64, i64, i64, P, P, P, P, i64, P]
+        L.mqa_kv_evict_workspace_bytes.argtypes = [i64, i64]
+        L.mqa_kv_compact.argtypes = [P, P, i64, i64, P, i64, i64, P, i64, i64, P, i32, P]
+        for name in ("mqa_kv_attention_decode_workspace_bytes", "mqa_kv_attention_selected_workspace_bytes",
+                     "mqa_kv_evict_workspace_bytes"):
+            getattr(L, name).restype = i64
+        for name in ("mqa_kv_attention_decode", "mqa_kv_attention_selected", "mqa_kv_weights_accumulate",
+                     "mqa_kv_evict_select", "mqa_kv_compact"):
+            getattr(L, name).restype = i32
         for name in ("mqa_fp4_topk_prefill", "mqa_fp4_topk_prefill_ex", "mqa_fp4_topk_prefill_static",
                      "mqa_fp4_dense_topk_prefill",
                      "mqa_fp4_dense_logits", "mqa_fp4_logits_topk", "mqa_fp4_supported_k",
@@ -375,3 +408,254 @@ def mqa_fp4_set_stage_events(events) -> None:
     else:
         _rc(lib().mqa_fp4_set_stage_events(ctypes.cast(events, ctypes.c_void_p), len(events)),
             "mqa_fp4_set_stage_events")
+
+
+# --- key-value cache operators (include/mqa_kv_cache.h) ------------------------------
+
+def _kv_types():
+    import torch
+    return {torch.bfloat16: 0, torch.float16: 1, torch.float8_e4m3fn: 2}
+
+
+def _kv_query(q, scale):
+    import torch
+    if not isinstance(q, torch.Tensor):
+        raise TypeError("q must be a torch.Tensor")
+    if q.dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError(f"q must be bfloat16 or float16, got {q.dtype}")
+    if q.dim() != 3:
+        raise ValueError(f"q must be [Q, H, D], got {tuple(q.shape)}")
+    Q, H, D = q.shape
+    if Q > 0 and ((D > 1 and q.stride(2) != 1) or (H > 1 and q.stride(1) != D)):
+        raise ValueError("the heads of one row of q must be contiguous")
+    return _KvQuery(q.data_ptr(), q.stride(0) if Q > 1 else H * D, Q, H, _kv_types()[q.dtype],
+                    D ** -0.5 if scale is None else float(scale))
+
+
+def _kv_pages(t, name, q):
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != q.dtype and t.dtype != torch.float8_e4m3fn:
+        raise TypeError(f"{name} must be {q.dtype} or float8_e4m3fn, got {t.dtype}")
+    if t.dim() != 4 or t.shape[1] != 64 or t.shape[3] != q.shape[2]:
+        raise ValueError(f"{name} must be [P, 64, Hkv, {q.shape[2]}], got {tuple(t.shape)}")
+    if t.shape[2] < 1 or q.shape[1] % t.shape[2]:
+        raise ValueError(f"{name}: {q.shape[1]} query heads over {t.shape[2]} key heads")
+    if t.numel() and t.stride(3) != 1:
+        raise ValueError(f"{name}: the elements of one head must be contiguous")
+
+
+def _kv_cache(q, k_pages, v_pages, k_scale, v_scale):
+    _kv_pages(k_pages, "k_pages", q)
+    c = _KvCache(k=k_pages.data_ptr(), num_phys_pages=k_pages.shape[0], num_kv_heads=k_pages.shape[2],
+                 head_dim=k_pages.shape[3], type=_kv_types()[k_pages.dtype], k_scale=float(k_scale),
+                 v_scale=float(v_scale))
+    c.k_stride[:] = k_pages.stride()[:3]
+    if v_pages is not None:
+        _kv_pages(v_pages, "v_pages", q)
+        if v_pages.shape != k_pages.shape or v_pages.dtype != k_pages.dtype:
+            raise ValueError("k_pages and v_pages must have one shape and type")
+        c.v = v_pages.data_ptr()
+        c.v_stride[:] = v_pages.stride()[:3]
+    return c
+
+
+def _kv_windows(q, block_table, seq_of_row, row_start, row_end):
+    import torch
+    _check(block_table, "block_table", torch.int32, 2)
+    for t, n in ((seq_of_row, "seq_of_row"), (row_start, "row_start"), (row_end, "row_end")):
+        _check(t, n, torch.int32, 1)
+        if t.shape[0] != q.shape[0]:
+            raise ValueError(f"{n} must be [{q.shape[0]}]")
+
+
+def _kv_outputs(q, out, lse, workspace):
+    import torch
+    _check(out, "out", q.dtype, 3)
+    _check(lse, "lse", torch.float32, 2)
+    _check(workspace, "workspace", torch.uint8)
+    if out is None or out.shape != q.shape:
+        raise ValueError(f"out must be {tuple(q.shape)}")
+    if lse is not None and lse.shape != q.shape[:2]:
+        raise ValueError(f"lse must be {tuple(q.shape[:2])}")
+
+
+def _kv_same_device(first, *others):
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"tensors on {first.device} and {t.device}")
+
+
+def mqa_kv_attention_decode(q, k_pages, v_pages, block_table, seq_of_row, row_start, row_end, out, workspace,
+                            lse=None, scale=None, k_scale=1.0, v_scale=1.0, stream=None):
+    """Attention of new tokens over a paged key-value cache: q [Q, H, D] (bfloat16 or float16; the row
+    stride is free), k_pages and v_pages [P, 64, Hkv, D] of q's type or float8_e4m3fn (page, position and
+    head strides are free), windows and block table as in mqa_fp4_topk_decode, out [Q, H, D], lse float32
+    [Q, H] or None, scale 1/sqrt(D) if None, workspace uint8 of at least
+    mqa_kv_attention_decode_workspace_bytes(Q, H, Hkv, D) bytes. Allocates nothing on the device and does
+    not synchronise (capturable)."""
+    query, cache = _kv_query(q, scale), _kv_cache(q, k_pages, v_pages, k_scale, v_scale)
+    _kv_windows(q, block_table, seq_of_row, row_start, row_end)
+    _kv_outputs(q, out, lse, workspace)
+    _kv_same_device(q, k_pages, v_pages, block_table, seq_of_row, row_start, row_end, out, lse, workspace)
+    rc = lib().mqa_kv_attention_decode(
+        ctypes.byref(query), ctypes.byref(cache), _ptr(block_table), block_table.shape[0], block_table.shape[1],
+        _ptr(seq_of_row), _ptr(row_start), _ptr(row_end), _ptr(out), _ptr(lse), _ptr(workspace),
+        0 if workspace is None else workspace.numel(), _stream(stream, q.device))
+    _rc(rc, "mqa_kv_attention_decode")
+
+
+def mqa_kv_attention_decode_workspace_bytes(num_rows: int, num_heads: int, num_kv_heads: int, head_dim: int) -> int:
+    r = int(lib().mqa_kv_attention_decode_workspace_bytes(int(num_rows), int(num_heads), int(num_kv_heads),
+                                                          int(head_dim)))
+    if r < 0:
+        raise MQAError(r, "mqa_kv_attention_decode_workspace_bytes")
+    return r
+
+
+def mqa_kv_attention_selected(q, k_pages, v_pages, slots, count, out, workspace=None, lse=None, scale=None,
+                              k_scale=1.0, v_scale=1.0, stream=None):
+    """Attention over a list of cache slots per row (the indexer's out_slot and out_count): slots int32
+    [Q, K], count int32 [Q]; the other arguments as in mqa_kv_attention_decode, workspace of at least
+    mqa_kv_attention_selected_workspace_bytes(Q, K, H, Hkv, D) bytes (None where that is 0). Capturable."""
+    import torch
+    query, cache = _kv_query(q, scale), _kv_cache(q, k_pages, v_pages, k_scale, v_scale)
+    _check(slots, "slots", torch.int32, 2)
+    _check(count, "count", torch.int32, 1)
+    if slots.shape[0] != q.shape[0] or count.shape[0] != q.shape[0]:
+        raise ValueError(f"slots and count must have {q.shape[0]} rows")
+    _kv_outputs(q, out, lse, workspace)
+    _kv_same_device(q, k_pages, v_pages, slots, count, out, lse, workspace)
+    rc = lib().mqa_kv_attention_selected(
+        ctypes.byref(query), ctypes.byref(cache), _ptr(slots), _ptr(count), slots.shape[1], _ptr(out), _ptr(lse),
+        _ptr(workspace), 0 if workspace is None else workspace.numel(), _stream(stream, q.device))
+    _rc(rc, "mqa_kv_attention_selected")
+
+
+def mqa_kv_attention_selected_workspace_bytes(num_rows: int, K: int, num_heads: int, num_kv_heads: int,
+                                              head_dim: int) -> int:
+    r = int(lib().mqa_kv_attention_selected_workspace_bytes(int(num_rows), int(K), int(num_heads),
+                                                            int(num_kv_heads), int(head_dim)))
+    if r < 0:
+        raise MQAError(r, "mqa_kv_attention_selected_workspace_bytes")
+    return r
+
+
+def mqa_kv_weights_accumulate(q, lse, k_pages, block_table, seq_of_row, row_start, row_end, acc, scale=None,
+                              k_scale=1.0, stream=None):
+    """Adds every position's attention weight, summed over its sequence's rows and heads, to acc float32
+    [n_seq, at least 64 * max_pages] (logical positions; the row stride is free); lse float32 [Q, H] as the
+    attention returned it for the same rows. Capturable."""
+    import torch
+    query, cache = _kv_query(q, scale), _kv_cache(q, k_pages, None, k_scale, 1.0)
+    _kv_windows(q, block_table, seq_of_row, row_start, row_end)
+    _check(lse, "lse", torch.float32, 2)
+    if lse is None or lse.shape != q.shape[:2]:
+        raise ValueError(f"lse must be {tuple(q.shape[:2])}")
+    stride = _kv_sums(acc, "acc", block_table.shape[0], 64 * block_table.shape[1])
+    _kv_same_device(q, lse, k_pages, block_table, seq_of_row, row_start, row_end, acc)
+    rc = lib().mqa_kv_weights_accumulate(
+        ctypes.byref(query), _ptr(lse), ctypes.byref(cache), _ptr(block_table), block_table.shape[0],
+        block_table.shape[1], _ptr(seq_of_row), _ptr(row_start), _ptr(row_end), _ptr(acc), stride,
+        _stream(stream, q.device))
+    _rc(rc, "mqa_kv_weights_accumulate")
+
+
+def _kv_sums(acc, name, n_seq, positions):
+    """Checks accumulated weights [n_seq, >= positions] and returns their row stride."""
+    import torch
+    if not isinstance(acc, torch.Tensor) or acc.dtype != torch.float32:
+        raise TypeError(f"{name} must be a float32 tensor")
+    if acc.dim() != 2 or acc.shape[0] != n_seq or acc.shape[1] < positions:
+        raise ValueError(f"{name} must be [{n_seq}, at least {positions}], got {tuple(acc.shape)}")
+    if acc.shape[1] > 1 and acc.stride(1) != 1:
+        raise ValueError(f"the positions of one sequence must be contiguous in {name}")
+    stride = acc.stride(0) if n_seq > 1 else acc.shape[1]
+    if stride < acc.shape[1]:
+        raise ValueError(f"the rows of {name} overlap")
+    return stride
+
+
+def mqa_kv_evict_select(acc, seq_len, budget, recent, keep, kept, workspace=None, kept_acc=None, stream=None):
+    """Chooses what a budget keeps of every sequence: its last `recent` positions and the budget - recent
+    earlier ones with the largest acc (float32 [n_seq, max_len]; seq_len int32 [n_seq]). Fills keep int32
+    [n_seq, budget] (rising, padded with -1), kept int32 [n_seq] and, if given, kept_acc float32 [n_seq,
+    budget]. workspace: at least mqa_kv_evict_workspace_bytes(n_seq, max_len) bytes. Capturable."""
+    import torch
+    _check(seq_len, "seq_len", torch.int32, 1)
+    _check(keep, "keep", torch.int32, 2)
+    _check(kept, "kept", torch.int32, 1)
+    _check(kept_acc, "kept_acc", torch.float32, 2)
+    _check(workspace, "workspace", torch.uint8)
+    n_seq = seq_len.shape[0]
+    stride = _kv_sums(acc, "acc", n_seq, 0)
+    if tuple(keep.shape) != (n_seq, int(budget)) or kept.shape[0] != n_seq:
+        raise ValueError(f"keep must be [{n_seq}, {int(budget)}] and kept [{n_seq}]")
+    if kept_acc is not None and kept_acc.shape != keep.shape:
+        raise ValueError(f"kept_acc must be {tuple(keep.shape)}")
+    _kv_same_device(acc, seq_len, keep, kept, kept_acc, workspace)
+    rc = lib().mqa_kv_evict_select(
+        _ptr(acc), stride, _ptr(seq_len), n_seq, acc.shape[1], int(budget), int(recent), _ptr(keep), _ptr(kept),
+        _ptr(kept_acc), _ptr(workspace), 0 if workspace is None else workspace.numel(), _stream(stream, acc.device))
+    _rc(rc, "mqa_kv_evict_select")
+
+
+def mqa_kv_evict_workspace_bytes(num_seqs: int, max_len: int) -> int:
+    r = int(lib().mqa_kv_evict_workspace_bytes(int(num_seqs), int(max_len)))
+    if r < 0:
+        raise MQAError(r, "mqa_kv_evict_workspace_bytes")
+    return r
+
+
+def _kv_array(pair, n):
+    import torch
+    src, dst = pair
+    for t, side in ((src, "source"), (dst, "destination")):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"array {n}: its {side} must be a torch.Tensor")
+        if t.dim() not in (2, 3, 4) or t.shape[1] != 64:
+            raise ValueError(f"array {n}: its {side} must be [P, 64], [P, 64, X] or [P, 64, Y, X]")
+    if src.dtype != dst.dtype or src.shape[1:] != dst.shape[1:]:
+        raise ValueError(f"array {n}: source and destination differ in type or shape")
+    size = src.element_size()
+    tail = tuple(src.shape[2:])
+    rows, width = (tail[0], tail[1]) if len(tail) == 2 else (1, tail[0] if tail else 1)
+    if rows < 1 or width < 1:
+        raise ValueError(f"array {n} has no elements per position")
+    a = _KvArray(src=src.data_ptr(), dst=dst.data_ptr(), row_bytes=width * size, rows_per_position=rows)
+    for t, strides, side in ((src, a.src_stride, "source"), (dst, a.dst_stride, "destination")):
+        if width > 1 and t.numel() and t.stride(-1) != 1:
+            raise ValueError(f"array {n}: the last dimension of its {side} must be contiguous")
+        strides[:] = [t.stride(0) * size, t.stride(1) * size,
+                      t.stride(2) * size if len(tail) == 2 and rows > 1 else width * size]
+    return a
+
+
+def mqa_kv_compact(keep, kept, src_table, dst_table, arrays, stream=None):
+    """Moves the kept positions (keep int32 [n_seq, budget], kept int32 [n_seq]) of paged arrays from
+    src_table's pages to the first positions of dst_table's. arrays: up to KV_MAX_ARRAYS pairs (source,
+    destination) of tensors [P, 64], [P, 64, X] or [P, 64, Y, X] (keys, values, the indexer's codes and
+    scales, ...), whole 4-byte words per position; source and destination may be one pool, with
+    destination pages that the call does not read. Capturable."""
+    import torch
+    _check(keep, "keep", torch.int32, 2)
+    _check(kept, "kept", torch.int32, 1)
+    _check(src_table, "src_table", torch.int32, 2)
+    _check(dst_table, "dst_table", torch.int32, 2)
+    n_seq = keep.shape[0]
+    if kept.shape[0] != n_seq or src_table.shape[0] != n_seq or dst_table.shape[0] != n_seq:
+        raise ValueError(f"kept, src_table and dst_table must have {n_seq} rows")
+    arrays = list(arrays)
+    if len(arrays) > KV_MAX_ARRAYS:
+        raise ValueError(f"at most {KV_MAX_ARRAYS} arrays, got {len(arrays)}")
+    made = (_KvArray * max(1, len(arrays)))(*[_kv_array(pair, i) for i, pair in enumerate(arrays)])
+    p_src = min((src.shape[0] for src, _ in arrays), default=0)
+    p_dst = min((dst.shape[0] for _, dst in arrays), default=0)
+    for src, dst in arrays:
+        _kv_same_device(keep, src, dst)
+    _kv_same_device(keep, kept, src_table, dst_table)
+    rc = lib().mqa_kv_compact(
+        _ptr(keep), _ptr(kept), n_seq, keep.shape[1], _ptr(src_table), src_table.shape[1], p_src, _ptr(dst_table),
+        dst_table.shape[1], p_dst, made, len(arrays), _stream(stream, keep.device))
+    _rc(rc, "mqa_kv_compact")

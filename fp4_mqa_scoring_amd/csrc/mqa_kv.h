@@ -1,0 +1,98 @@
+// Internal declarations of the key-value cache operators: what the host side
+// (mqa_kv_api.hip) hands to the kernels' launchers.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace mqa {
+
+// One call of an attention over the cache. Strides in bytes.
+struct KvAttnArgs {
+  const char* q;
+  int64_t q_row;
+  int64_t Q;
+  const char* k;
+  const char* v;
+  int64_t k_page, k_pos, k_head;
+  int64_t v_page, v_pos, v_head;
+  int64_t P_phys;
+  int32_t H, Hkv, D;
+  int32_t G;                 // query heads per key head
+  int32_t q_type, kv_type;   // MQA_KV_*
+  float c;                   // |scale * k_scale| * log2(e)
+  uint32_t q_flip;           // 0x80008000 where scale * k_scale is negative, else 0
+  float score_scale;         // scale * k_scale (weights)
+  float v_scale;
+  void* out;
+  float* lse;
+  // windows (decode, weights)
+  const int32_t* table;
+  int64_t n_seq, max_pages;
+  const int32_t *seq_of_row, *row_start, *row_end;
+  // lists (selected)
+  const int32_t *slots, *count;
+  int64_t K;
+  int32_t splits;
+  // workspace
+  int64_t* prefix;           // [Q + 1] window pages of the rows before each row (decode)
+  float* part_o;             // [slots of partial sums, heads, D]
+  float2* part_ml;           // [slots of partial sums, heads] maximum (log2 domain) and sum
+  int32_t* status;
+};
+
+// Query heads that one wave carries, in tiles of 16: as many as the group has,
+// up to 64 (32 for D = 256, whose sums need twice the registers).
+constexpr int kv_q_tiles(int D, int G) { return G <= 16 ? 1 : D == 256 ? 2 : 4; }
+constexpr int kv_q_groups(int D, int G) { return (G + 16 * kv_q_tiles(D, G) - 1) / (16 * kv_q_tiles(D, G)); }
+constexpr int kv_group_rows(int D, int G) { return G < 16 * kv_q_tiles(D, G) ? G : 16 * kv_q_tiles(D, G); }
+
+// Workgroups of the decode form: what a 256-CU device holds at once.
+constexpr int kv_decode_groups(int D, int G) { return G <= 16 && D < 256 ? 768 : 256; }
+constexpr int kKvWeightGroups = 1024; // workgroups of the accumulated weights
+constexpr int kKvPlanRows = 1024;     // rows up to which every workgroup plans for itself
+constexpr int kKvSelBlock = 1024;     // slots staged at once by the selected form
+
+int32_t kv_selected_splits(int64_t Q, int64_t K, int D, int G, int Hkv);
+
+hipError_t launch_kv_decode(const KvAttnArgs& a, hipStream_t st);
+hipError_t launch_kv_selected(const KvAttnArgs& a, hipStream_t st);
+
+// acc[seq * acc_stride + p] += the rows' weights (a.lse is read, out unused).
+hipError_t launch_kv_weights(const KvAttnArgs& a, const float* lse, float* acc, int64_t acc_stride, hipStream_t st);
+
+struct KvEvictArgs {
+  const float* acc;
+  int64_t acc_stride;
+  const int32_t* seq_len;
+  int64_t n_seq, max_len, budget, recent;
+  int32_t* keep;
+  int32_t* kept;
+  float* kept_acc;
+  int32_t* status;
+};
+hipError_t launch_kv_evict_select(const KvEvictArgs& a, hipStream_t st);
+
+constexpr int kKvMaxArrays = 8;
+struct KvCompactArray {
+  const char* src;
+  char* dst;
+  int64_t src_page, src_pos, src_row, dst_page, dst_pos, dst_row;   // byte strides
+  int64_t units;       // pieces of 16 (or 4) bytes per row
+  int64_t rows;        // rows per position
+  int32_t wide;        // 16-byte pieces
+};
+struct KvCompactArgs {
+  const int32_t *keep, *kept;
+  int64_t n_seq, budget;
+  const int32_t* src_table;
+  int64_t src_pages, P_src;
+  const int32_t* dst_table;
+  int64_t dst_pages, P_dst;
+  int32_t n_arrays;
+  KvCompactArray arrays[kKvMaxArrays];
+  int32_t* status;
+};
+hipError_t launch_kv_compact(const KvCompactArgs& a, hipStream_t st);
+
+}  // namespace mqa
