@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 from . import synth  # noqa: F401  (seeded input generator)
 
@@ -30,24 +31,6 @@ FLAG_FORCE_UNDERFILL = 0x200
 FLAG_NO_FALLBACK = 0x400
 STATIC_SCRATCH_BYTES = 64 << 20          # MQA_STATIC_SCRATCH_BYTES
 KV_MAX_ARRAYS = 8                        # MQA_KV_MAX_ARRAYS
-
-
-class _KvCache(ctypes.Structure):        # mqa_kv_cache
-    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_stride", ctypes.c_int64 * 3),
-                ("v_stride", ctypes.c_int64 * 3), ("num_phys_pages", ctypes.c_int64),
-                ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("type", ctypes.c_int32),
-                ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float)]
-
-
-class _KvQuery(ctypes.Structure):        # mqa_kv_query
-    _fields_ = [("q", ctypes.c_void_p), ("row_stride", ctypes.c_int64), ("num_rows", ctypes.c_int64),
-                ("num_heads", ctypes.c_int32), ("type", ctypes.c_int32), ("scale", ctypes.c_float)]
-
-
-class _KvArray(ctypes.Structure):        # mqa_kv_array
-    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("src_stride", ctypes.c_int64 * 3),
-                ("dst_stride", ctypes.c_int64 * 3), ("row_bytes", ctypes.c_int64),
-                ("rows_per_position", ctypes.c_int64)]
 
 
 class MQAError(RuntimeError):
@@ -411,80 +394,134 @@ def mqa_fp4_set_stage_events(events) -> None:
 
 
 # --- key-value cache operators (include/mqa_kv_cache.h) ------------------------------
+#
+# The decode step of a small batch takes the device about ten microseconds, so these
+# calls are kept short on the host: the header's structures are packed as bytes (a
+# ctypes structure of this size costs 4 us to fill) and the current stream is read as a handle.
 
-def _kv_types():
-    import torch
-    return {torch.bfloat16: 0, torch.float16: 1, torch.float8_e4m3fn: 2}
+_KV_CACHE = struct.Struct("@PP3q3qqiiiff4x")    # mqa_kv_cache
+_KV_QUERY = struct.Struct("@Pqqiif4x")          # mqa_kv_query
+_KV_ARRAY = struct.Struct("@PP3q3qqq")          # mqa_kv_array
+_kv_const = None
+
+
+def _kv():
+    """(torch, its 16-bit and 8-bit types -> MQA_KV_*, the reader of a device's current stream handle)."""
+    global _kv_const
+    if _kv_const is None:
+        import torch
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is None:
+            raw = lambda index: torch.cuda.current_stream(index).cuda_stream  # noqa: E731
+        _kv_const = (torch, {torch.bfloat16: 0, torch.float16: 1, torch.float8_e4m3fn: 2}, raw)
+    return _kv_const
+
+
+def _kv_stream(stream, device):
+    if stream is None and device.index is not None:
+        return _kv()[2](device.index)
+    return _stream(stream, device)
+
+
+# Devices are checked by the library: every pointer must be memory of the stream's device.
+
+def _kv_check(t, name, dtype, shape):
+    """t is a contiguous tensor of this type and shape; its address."""
+    try:
+        if t.dtype == dtype and t.shape == shape and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        raise TypeError(f"{name} must be a torch.Tensor") from None
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _kv_table(t, name, rows):
+    """t is a contiguous int32 table [rows (or any), X]; its address and sizes."""
+    try:
+        n, width = t.shape
+    except (AttributeError, ValueError):
+        raise (ValueError if hasattr(t, "shape") else TypeError)(f"{name} must be a tensor of two dimensions") from None
+    return _kv_check(t, name, _kv()[0].int32, (n if rows is None else rows, width)), n, width
+
+
+def _kv_workspace(t):
+    """Address and bytes of a workspace (None: none)."""
+    if t is None:
+        return None, 0
+    return _kv_check(t, "workspace", _kv()[0].uint8, getattr(t, "shape", None)), t.numel()
+
+
+def _f32(x):
+    """x as a 32-bit number; beyond their range an infinity, which the library refuses."""
+    x = float(x)
+    return x if -3.4e38 < x < 3.4e38 else ctypes.c_float(x).value
 
 
 def _kv_query(q, scale):
-    import torch
+    """mqa_kv_query of q, and q's shape."""
+    torch, types, _ = _kv()
     if not isinstance(q, torch.Tensor):
         raise TypeError("q must be a torch.Tensor")
-    if q.dtype not in (torch.bfloat16, torch.float16):
-        raise TypeError(f"q must be bfloat16 or float16, got {q.dtype}")
-    if q.dim() != 3:
-        raise ValueError(f"q must be [Q, H, D], got {tuple(q.shape)}")
-    Q, H, D = q.shape
-    if Q > 0 and ((D > 1 and q.stride(2) != 1) or (H > 1 and q.stride(1) != D)):
+    kind, shape = q.dtype, q.shape
+    if kind != torch.bfloat16 and kind != torch.float16:
+        raise TypeError(f"q must be bfloat16 or float16, got {kind}")
+    if len(shape) != 3:
+        raise ValueError(f"q must be [Q, H, D], got {list(shape)}")
+    Q, H, D = shape
+    row, head, element = q.stride()
+    if Q > 0 and ((D > 1 and element != 1) or (H > 1 and head != D)):
         raise ValueError("the heads of one row of q must be contiguous")
-    return _KvQuery(q.data_ptr(), q.stride(0) if Q > 1 else H * D, Q, H, _kv_types()[q.dtype],
-                    D ** -0.5 if scale is None else float(scale))
-
-
-def _kv_pages(t, name, q):
-    import torch
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != q.dtype and t.dtype != torch.float8_e4m3fn:
-        raise TypeError(f"{name} must be {q.dtype} or float8_e4m3fn, got {t.dtype}")
-    if t.dim() != 4 or t.shape[1] != 64 or t.shape[3] != q.shape[2]:
-        raise ValueError(f"{name} must be [P, 64, Hkv, {q.shape[2]}], got {tuple(t.shape)}")
-    if t.shape[2] < 1 or q.shape[1] % t.shape[2]:
-        raise ValueError(f"{name}: {q.shape[1]} query heads over {t.shape[2]} key heads")
-    if t.numel() and t.stride(3) != 1:
-        raise ValueError(f"{name}: the elements of one head must be contiguous")
+    return _KV_QUERY.pack(q.data_ptr(), row if Q > 1 else H * D, Q, H, types[kind],
+                          (D ** -0.5 if D else 0.0) if scale is None else _f32(scale)), shape
 
 
 def _kv_cache(q, k_pages, v_pages, k_scale, v_scale):
-    _kv_pages(k_pages, "k_pages", q)
-    c = _KvCache(k=k_pages.data_ptr(), num_phys_pages=k_pages.shape[0], num_kv_heads=k_pages.shape[2],
-                 head_dim=k_pages.shape[3], type=_kv_types()[k_pages.dtype], k_scale=float(k_scale),
-                 v_scale=float(v_scale))
-    c.k_stride[:] = k_pages.stride()[:3]
+    """mqa_kv_cache of the pages (v_pages None: keys only) for q."""
+    torch, types, _ = _kv()
+    if not isinstance(k_pages, torch.Tensor):
+        raise TypeError("k_pages must be a torch.Tensor")
+    kind, shape = k_pages.dtype, k_pages.shape
+    _, H, D = q.shape
+    if kind != q.dtype and kind != torch.float8_e4m3fn:
+        raise TypeError(f"k_pages must be {q.dtype} or float8_e4m3fn, got {kind}")
+    if len(shape) != 4 or shape[1] != 64 or shape[3] != D:
+        raise ValueError(f"k_pages must be [P, 64, Hkv, {D}], got {list(shape)}")
+    P, _, heads, _ = shape
+    if heads < 1 or H % heads:
+        raise ValueError(f"k_pages: {H} query heads over {heads} key heads")
+    page, pos, head, element = k_pages.stride()
+    if element != 1 and k_pages.numel():
+        raise ValueError("k_pages: the elements of one head must be contiguous")
+    v = (0, 0, 0)
+    v_ptr = 0
     if v_pages is not None:
-        _kv_pages(v_pages, "v_pages", q)
-        if v_pages.shape != k_pages.shape or v_pages.dtype != k_pages.dtype:
+        if not isinstance(v_pages, torch.Tensor):
+            raise TypeError("v_pages must be a torch.Tensor")
+        if v_pages.dtype != kind or v_pages.shape != shape:
             raise ValueError("k_pages and v_pages must have one shape and type")
-        c.v = v_pages.data_ptr()
-        c.v_stride[:] = v_pages.stride()[:3]
-    return c
+        *v, element = v_pages.stride()
+        if element != 1 and v_pages.numel():
+            raise ValueError("v_pages: the elements of one head must be contiguous")
+        v_ptr = v_pages.data_ptr()
+    return _KV_CACHE.pack(k_pages.data_ptr(), v_ptr, page, pos, head, *v, P, heads, D, types[kind], _f32(k_scale),
+                          _f32(v_scale))
 
 
-def _kv_windows(q, block_table, seq_of_row, row_start, row_end):
-    import torch
-    _check(block_table, "block_table", torch.int32, 2)
-    for t, n in ((seq_of_row, "seq_of_row"), (row_start, "row_start"), (row_end, "row_end")):
-        _check(t, n, torch.int32, 1)
-        if t.shape[0] != q.shape[0]:
-            raise ValueError(f"{n} must be [{q.shape[0]}]")
+def _kv_windows(rows, block_table, seq_of_row, row_start, row_end):
+    """Addresses of the table and the windows, with the table's sizes, in the order of the C calls."""
+    i32 = _kv()[0].int32
+    return (*_kv_table(block_table, "block_table", None), _kv_check(seq_of_row, "seq_of_row", i32, rows),
+            _kv_check(row_start, "row_start", i32, rows), _kv_check(row_end, "row_end", i32, rows))
 
 
-def _kv_outputs(q, out, lse, workspace):
-    import torch
-    _check(out, "out", q.dtype, 3)
-    _check(lse, "lse", torch.float32, 2)
-    _check(workspace, "workspace", torch.uint8)
-    if out is None or out.shape != q.shape:
-        raise ValueError(f"out must be {tuple(q.shape)}")
-    if lse is not None and lse.shape != q.shape[:2]:
-        raise ValueError(f"lse must be {tuple(q.shape[:2])}")
-
-
-def _kv_same_device(first, *others):
-    for t in others:
-        if t is not None and t.device != first.device:
-            raise ValueError(f"tensors on {first.device} and {t.device}")
+def _kv_outputs(q, shape, out, lse):
+    """Addresses of out and lse (None: none)."""
+    return (_kv_check(out, "out", q.dtype, shape),
+            None if lse is None else _kv_check(lse, "lse", _kv()[0].float32, shape[:2]))
 
 
 def mqa_kv_attention_decode(q, k_pages, v_pages, block_table, seq_of_row, row_start, row_end, out, workspace,
@@ -495,14 +532,11 @@ def mqa_kv_attention_decode(q, k_pages, v_pages, block_table, seq_of_row, row_st
     [Q, H] or None, scale 1/sqrt(D) if None, workspace uint8 of at least
     mqa_kv_attention_decode_workspace_bytes(Q, H, Hkv, D) bytes. Allocates nothing on the device and does
     not synchronise (capturable)."""
-    query, cache = _kv_query(q, scale), _kv_cache(q, k_pages, v_pages, k_scale, v_scale)
-    _kv_windows(q, block_table, seq_of_row, row_start, row_end)
-    _kv_outputs(q, out, lse, workspace)
-    _kv_same_device(q, k_pages, v_pages, block_table, seq_of_row, row_start, row_end, out, lse, workspace)
+    query, shape = _kv_query(q, scale)
     rc = lib().mqa_kv_attention_decode(
-        ctypes.byref(query), ctypes.byref(cache), _ptr(block_table), block_table.shape[0], block_table.shape[1],
-        _ptr(seq_of_row), _ptr(row_start), _ptr(row_end), _ptr(out), _ptr(lse), _ptr(workspace),
-        0 if workspace is None else workspace.numel(), _stream(stream, q.device))
+        query, _kv_cache(q, k_pages, v_pages, k_scale, v_scale),
+        *_kv_windows(shape[:1], block_table, seq_of_row, row_start, row_end), *_kv_outputs(q, shape, out, lse),
+        *_kv_workspace(workspace), _kv_stream(stream, q.device))
     _rc(rc, "mqa_kv_attention_decode")
 
 
@@ -519,17 +553,12 @@ def mqa_kv_attention_selected(q, k_pages, v_pages, slots, count, out, workspace=
     """Attention over a list of cache slots per row (the indexer's out_slot and out_count): slots int32
     [Q, K], count int32 [Q]; the other arguments as in mqa_kv_attention_decode, workspace of at least
     mqa_kv_attention_selected_workspace_bytes(Q, K, H, Hkv, D) bytes (None where that is 0). Capturable."""
-    import torch
-    query, cache = _kv_query(q, scale), _kv_cache(q, k_pages, v_pages, k_scale, v_scale)
-    _check(slots, "slots", torch.int32, 2)
-    _check(count, "count", torch.int32, 1)
-    if slots.shape[0] != q.shape[0] or count.shape[0] != q.shape[0]:
-        raise ValueError(f"slots and count must have {q.shape[0]} rows")
-    _kv_outputs(q, out, lse, workspace)
-    _kv_same_device(q, k_pages, v_pages, slots, count, out, lse, workspace)
+    query, shape = _kv_query(q, scale)
+    cache = _kv_cache(q, k_pages, v_pages, k_scale, v_scale)
+    lists, _, K = _kv_table(slots, "slots", shape[0])
     rc = lib().mqa_kv_attention_selected(
-        ctypes.byref(query), ctypes.byref(cache), _ptr(slots), _ptr(count), slots.shape[1], _ptr(out), _ptr(lse),
-        _ptr(workspace), 0 if workspace is None else workspace.numel(), _stream(stream, q.device))
+        query, cache, lists, _kv_check(count, "count", _kv()[0].int32, shape[:1]), K, *_kv_outputs(q, shape, out, lse),
+        *_kv_workspace(workspace), _kv_stream(stream, q.device))
     _rc(rc, "mqa_kv_attention_selected")
 
 
@@ -547,28 +576,23 @@ def mqa_kv_weights_accumulate(q, lse, k_pages, block_table, seq_of_row, row_star
     """Adds every position's attention weight, summed over its sequence's rows and heads, to acc float32
     [n_seq, at least 64 * max_pages] (logical positions; the row stride is free); lse float32 [Q, H] as the
     attention returned it for the same rows. Capturable."""
-    import torch
-    query, cache = _kv_query(q, scale), _kv_cache(q, k_pages, None, k_scale, 1.0)
-    _kv_windows(q, block_table, seq_of_row, row_start, row_end)
-    _check(lse, "lse", torch.float32, 2)
-    if lse is None or lse.shape != q.shape[:2]:
-        raise ValueError(f"lse must be {tuple(q.shape[:2])}")
-    stride = _kv_sums(acc, "acc", block_table.shape[0], 64 * block_table.shape[1])
-    _kv_same_device(q, lse, k_pages, block_table, seq_of_row, row_start, row_end, acc)
+    query, shape = _kv_query(q, scale)
+    cache = _kv_cache(q, k_pages, None, k_scale, 1.0)
+    windows = _kv_windows(shape[:1], block_table, seq_of_row, row_start, row_end)
+    stride = _kv_sums(acc, "acc", windows[1], 64 * windows[2])
     rc = lib().mqa_kv_weights_accumulate(
-        ctypes.byref(query), _ptr(lse), ctypes.byref(cache), _ptr(block_table), block_table.shape[0],
-        block_table.shape[1], _ptr(seq_of_row), _ptr(row_start), _ptr(row_end), _ptr(acc), stride,
-        _stream(stream, q.device))
+        query, _kv_check(lse, "lse", _kv()[0].float32, shape[:2]), cache, *windows, acc.data_ptr(), stride,
+        _kv_stream(stream, q.device))
     _rc(rc, "mqa_kv_weights_accumulate")
 
 
 def _kv_sums(acc, name, n_seq, positions):
     """Checks accumulated weights [n_seq, >= positions] and returns their row stride."""
-    import torch
+    torch = _kv()[0]
     if not isinstance(acc, torch.Tensor) or acc.dtype != torch.float32:
         raise TypeError(f"{name} must be a float32 tensor")
     if acc.dim() != 2 or acc.shape[0] != n_seq or acc.shape[1] < positions:
-        raise ValueError(f"{name} must be [{n_seq}, at least {positions}], got {tuple(acc.shape)}")
+        raise ValueError(f"{name} must be [{n_seq}, at least {positions}], got {list(acc.shape)}")
     if acc.shape[1] > 1 and acc.stride(1) != 1:
         raise ValueError(f"the positions of one sequence must be contiguous in {name}")
     stride = acc.stride(0) if n_seq > 1 else acc.shape[1]
@@ -582,22 +606,17 @@ def mqa_kv_evict_select(acc, seq_len, budget, recent, keep, kept, workspace=None
     earlier ones with the largest acc (float32 [n_seq, max_len]; seq_len int32 [n_seq]). Fills keep int32
     [n_seq, budget] (rising, padded with -1), kept int32 [n_seq] and, if given, kept_acc float32 [n_seq,
     budget]. workspace: at least mqa_kv_evict_workspace_bytes(n_seq, max_len) bytes. Capturable."""
-    import torch
-    _check(seq_len, "seq_len", torch.int32, 1)
-    _check(keep, "keep", torch.int32, 2)
-    _check(kept, "kept", torch.int32, 1)
-    _check(kept_acc, "kept_acc", torch.float32, 2)
-    _check(workspace, "workspace", torch.uint8)
-    n_seq = seq_len.shape[0]
-    stride = _kv_sums(acc, "acc", n_seq, 0)
-    if tuple(keep.shape) != (n_seq, int(budget)) or kept.shape[0] != n_seq:
-        raise ValueError(f"keep must be [{n_seq}, {int(budget)}] and kept [{n_seq}]")
-    if kept_acc is not None and kept_acc.shape != keep.shape:
-        raise ValueError(f"kept_acc must be {tuple(keep.shape)}")
-    _kv_same_device(acc, seq_len, keep, kept, kept_acc, workspace)
+    torch = _kv()[0]
+    if not isinstance(seq_len, torch.Tensor) or seq_len.dim() != 1:
+        raise TypeError("seq_len must be a tensor of one dimension")
+    n = seq_len.shape[0]
+    stride = _kv_sums(acc, "acc", n, 0)
+    shape = (n, int(budget))
     rc = lib().mqa_kv_evict_select(
-        _ptr(acc), stride, _ptr(seq_len), n_seq, acc.shape[1], int(budget), int(recent), _ptr(keep), _ptr(kept),
-        _ptr(kept_acc), _ptr(workspace), 0 if workspace is None else workspace.numel(), _stream(stream, acc.device))
+        acc.data_ptr(), stride, _kv_check(seq_len, "seq_len", torch.int32, (n,)), n, acc.shape[1], shape[1], int(recent),
+        _kv_check(keep, "keep", torch.int32, shape), _kv_check(kept, "kept", torch.int32, (n,)),
+        None if kept_acc is None else _kv_check(kept_acc, "kept_acc", torch.float32, shape),
+        *_kv_workspace(workspace), _kv_stream(stream, acc.device))
     _rc(rc, "mqa_kv_evict_select")
 
 
@@ -608,28 +627,26 @@ def mqa_kv_evict_workspace_bytes(num_seqs: int, max_len: int) -> int:
     return r
 
 
-def _kv_array(pair, n):
-    import torch
-    src, dst = pair
-    for t, side in ((src, "source"), (dst, "destination")):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"array {n}: its {side} must be a torch.Tensor")
-        if t.dim() not in (2, 3, 4) or t.shape[1] != 64:
-            raise ValueError(f"array {n}: its {side} must be [P, 64], [P, 64, X] or [P, 64, Y, X]")
-    if src.dtype != dst.dtype or src.shape[1:] != dst.shape[1:]:
+def _kv_array(src, dst, n):
+    """mqa_kv_array of one pair of paged tensors."""
+    torch = _kv()[0]
+    if not isinstance(src, torch.Tensor) or not isinstance(dst, torch.Tensor):
+        raise TypeError(f"array {n} must be a pair of tensors")
+    shape, size = src.shape, src.element_size()
+    if not 2 <= len(shape) <= 4 or shape[1] != 64:
+        raise ValueError(f"array {n} must be [P, 64], [P, 64, X] or [P, 64, Y, X], got {list(shape)}")
+    if src.dtype != dst.dtype or shape[1:] != dst.shape[1:]:
         raise ValueError(f"array {n}: source and destination differ in type or shape")
-    size = src.element_size()
-    tail = tuple(src.shape[2:])
-    rows, width = (tail[0], tail[1]) if len(tail) == 2 else (1, tail[0] if tail else 1)
+    rows, width = (shape[2], shape[3]) if len(shape) == 4 else (1, shape[2] if len(shape) == 3 else 1)
     if rows < 1 or width < 1:
         raise ValueError(f"array {n} has no elements per position")
-    a = _KvArray(src=src.data_ptr(), dst=dst.data_ptr(), row_bytes=width * size, rows_per_position=rows)
-    for t, strides, side in ((src, a.src_stride, "source"), (dst, a.dst_stride, "destination")):
-        if width > 1 and t.numel() and t.stride(-1) != 1:
-            raise ValueError(f"array {n}: the last dimension of its {side} must be contiguous")
-        strides[:] = [t.stride(0) * size, t.stride(1) * size,
-                      t.stride(2) * size if len(tail) == 2 and rows > 1 else width * size]
-    return a
+    strides = []
+    for t in (src, dst):
+        stride = t.stride()
+        if width > 1 and stride[-1] != 1 and t.numel():
+            raise ValueError(f"array {n}: the last dimension must be contiguous")
+        strides += [stride[0] * size, stride[1] * size, stride[2] * size if rows > 1 else width * size]
+    return _KV_ARRAY.pack(src.data_ptr(), dst.data_ptr(), *strides, width * size, rows)
 
 
 def mqa_kv_compact(keep, kept, src_table, dst_table, arrays, stream=None):
@@ -638,24 +655,16 @@ def mqa_kv_compact(keep, kept, src_table, dst_table, arrays, stream=None):
     destination) of tensors [P, 64], [P, 64, X] or [P, 64, Y, X] (keys, values, the indexer's codes and
     scales, ...), whole 4-byte words per position; source and destination may be one pool, with
     destination pages that the call does not read. Capturable."""
-    import torch
-    _check(keep, "keep", torch.int32, 2)
-    _check(kept, "kept", torch.int32, 1)
-    _check(src_table, "src_table", torch.int32, 2)
-    _check(dst_table, "dst_table", torch.int32, 2)
-    n_seq = keep.shape[0]
-    if kept.shape[0] != n_seq or src_table.shape[0] != n_seq or dst_table.shape[0] != n_seq:
-        raise ValueError(f"kept, src_table and dst_table must have {n_seq} rows")
+    i32 = _kv()[0].int32
+    keep_at, n, budget = _kv_table(keep, "keep", None)
     arrays = list(arrays)
     if len(arrays) > KV_MAX_ARRAYS:
         raise ValueError(f"at most {KV_MAX_ARRAYS} arrays, got {len(arrays)}")
-    made = (_KvArray * max(1, len(arrays)))(*[_kv_array(pair, i) for i, pair in enumerate(arrays)])
-    p_src = min((src.shape[0] for src, _ in arrays), default=0)
-    p_dst = min((dst.shape[0] for _, dst in arrays), default=0)
-    for src, dst in arrays:
-        _kv_same_device(keep, src, dst)
-    _kv_same_device(keep, kept, src_table, dst_table)
+    made = b"".join([_kv_array(src, dst, i) for i, (src, dst) in enumerate(arrays)])
+    src_at, _, src_pages = _kv_table(src_table, "src_table", n)
+    dst_at, _, dst_pages = _kv_table(dst_table, "dst_table", n)
     rc = lib().mqa_kv_compact(
-        _ptr(keep), _ptr(kept), n_seq, keep.shape[1], _ptr(src_table), src_table.shape[1], p_src, _ptr(dst_table),
-        dst_table.shape[1], p_dst, made, len(arrays), _stream(stream, keep.device))
+        keep_at, _kv_check(kept, "kept", i32, (n,)), n, budget, src_at, src_pages,
+        min([src.shape[0] for src, _ in arrays], default=0), dst_at, dst_pages,
+        min([dst.shape[0] for _, dst in arrays], default=0), made, len(arrays), _kv_stream(stream, keep.device))
     _rc(rc, "mqa_kv_compact")

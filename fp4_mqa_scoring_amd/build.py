@@ -1,9 +1,11 @@
 """Builds the HIP library libmqa_fp4.so in-tree for gfx950 (hipcc, no GPU needed)."""
 from __future__ import annotations
 
+import concurrent.futures
 import os
 import shutil
 import subprocess
+import tempfile
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -29,12 +31,22 @@ def hipcc() -> str:
     raise RuntimeError("hipcc not found")
 
 
-def _build_one(lib: str, sources, verbose: bool) -> None:
-    tmp = lib + ".tmp%d" % os.getpid()
-    cmd = [hipcc(), *HIPCC_FLAGS, "-I", os.path.join(ROOT, "include"), *sources, "-o", tmp]
+def _run(cmd, verbose: bool) -> None:
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
+
+
+def _build_one(lib: str, sources, verbose: bool) -> None:
+    """Compiles the sources side by side, then links them."""
+    tmp = lib + ".tmp%d" % os.getpid()
+    with tempfile.TemporaryDirectory() as where:
+        objects = [os.path.join(where, os.path.basename(f) + ".o") for f in sources]
+        with concurrent.futures.ThreadPoolExecutor(min(8, os.cpu_count() or 1)) as pool:
+            flags = [f for f in HIPCC_FLAGS if f != "-shared"]
+            list(pool.map(lambda fo: _run([hipcc(), *flags, "-I", os.path.join(ROOT, "include"), "-c", fo[0], "-o", fo[1]],
+                                          verbose), zip(sources, objects)))
+        _run([hipcc(), *HIPCC_FLAGS, *objects, "-o", tmp], verbose)
     os.replace(tmp, lib)
 
 

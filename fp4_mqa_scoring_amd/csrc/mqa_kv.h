@@ -41,14 +41,14 @@ struct KvAttnArgs {
   int32_t* status;
 };
 
-// Query heads that one wave carries, in tiles of 16: as many as the group has,
-// up to 64 (32 for D = 256, whose sums need twice the registers).
-constexpr int kv_q_tiles(int D, int G) { return G <= 16 ? 1 : D == 256 ? 2 : 4; }
-constexpr int kv_q_groups(int D, int G) { return (G + 16 * kv_q_tiles(D, G) - 1) / (16 * kv_q_tiles(D, G)); }
-constexpr int kv_group_rows(int D, int G) { return G < 16 * kv_q_tiles(D, G) ? G : 16 * kv_q_tiles(D, G); }
+// Query heads that a workgroup carries for one row, in tiles of 16: as many as the
+// group has, up to four tiles (two where D = 256, whose sums need twice the registers).
+constexpr int kv_tiles(int D, int G) { return G <= 16 ? 1 : G <= 32 || D == 256 ? 2 : 4; }
+constexpr int kv_head_groups(int D, int G) { return (G + 16 * kv_tiles(D, G) - 1) / (16 * kv_tiles(D, G)); }
+constexpr int kv_group_rows(int D, int G) { return G < 16 * kv_tiles(D, G) ? G : 16 * kv_tiles(D, G); }
 
-// Workgroups of the decode form: what a 256-CU device holds at once.
-constexpr int kv_decode_groups(int D, int G) { return G <= 16 && D < 256 ? 768 : 256; }
+// Workgroups of the decode form: what 256 compute units hold at once.
+constexpr int kKvDecodeGroups = 512;
 constexpr int kKvWeightGroups = 1024; // workgroups of the accumulated weights
 constexpr int kKvPlanRows = 1024;     // rows up to which every workgroup plans for itself
 constexpr int kKvSelBlock = 1024;     // slots staged at once by the selected form

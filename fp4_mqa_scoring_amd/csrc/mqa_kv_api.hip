@@ -35,7 +35,7 @@ int32_t check_heads(int64_t num_rows, int32_t H, int32_t Hkv, int32_t D) {
 int32_t cache_strides(const int64_t* stride, const mqa_kv_cache& c, int64_t* page, int64_t* pos, int64_t* head) {
   const int64_t bytes = element_bytes(c.type), D = c.head_dim;
   for (int i = 0; i < 3; ++i) {
-    if (stride[i] < 0 || stride[i] > (1ll << 40)) return MQA_ERR_BAD_SIZE;
+    if (stride[i] < 0 || stride[i] >= (1ll << 35)) return MQA_ERR_BAD_SIZE;
     if (stride[i] * bytes % 16) return MQA_ERR_MISALIGNED;
   }
   // one page's extent, and every product of a stride in the kernels, fits
@@ -106,8 +106,8 @@ struct PartialLayout {
 };
 
 // Workspace: page prefix of the rows, then (maximum, sum) and weighted values of `slots` partial results.
-PartialLayout partial_layout(int64_t prefix_rows, int64_t slots, int32_t D, int32_t G) {
-  const int64_t heads = slots * mqa::kv_group_rows(D, G);
+PartialLayout partial_layout(int64_t prefix_rows, int64_t slots, int32_t D, int32_t group_rows) {
+  const int64_t heads = slots * group_rows;
   PartialLayout l;
   l.prefix = 0;
   l.ml = align_up(prefix_rows * static_cast<int64_t>(sizeof(int64_t)));
@@ -117,11 +117,11 @@ PartialLayout partial_layout(int64_t prefix_rows, int64_t slots, int32_t D, int3
 }
 
 PartialLayout decode_layout(int64_t Q, int32_t D, int32_t G) {
-  return partial_layout(Q + 1, 2 * mqa::kv_decode_groups(D, G), D, G);
+  return partial_layout(Q + 1, 2 * mqa::kKvDecodeGroups, D, mqa::kv_group_rows(D, G));
 }
 
 PartialLayout selected_layout(int64_t Q, int32_t D, int32_t G, int32_t Hkv, int32_t splits) {
-  return partial_layout(0, splits > 1 ? Q * Hkv * mqa::kv_q_groups(D, G) * splits : 0, D, G);
+  return partial_layout(0, splits > 1 ? Q * Hkv * mqa::kv_head_groups(D, G) * splits : 0, D, mqa::kv_group_rows(D, G));
 }
 
 void place(KvAttnArgs* a, const PartialLayout& l, void* workspace) {

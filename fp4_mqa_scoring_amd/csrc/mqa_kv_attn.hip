@@ -34,11 +34,18 @@ namespace {
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef float v2f __attribute__((ext_vector_type(2)));
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 typedef uint32_t v2u __attribute__((ext_vector_type(2)));
+
+template <bool FIRST, class A, class B>
+struct Pick { typedef A type; };
+template <class A, class B>
+struct Pick<false, A, B> { typedef B type; };
 
 constexpr int kThreads = 256;
 constexpr int kWaves = 4;
@@ -49,6 +56,10 @@ struct Bf16 {
   static __device__ __forceinline__ v4f mfma(v4u a, v4u b, v4f c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c,
                                                    0, 0, 0);
+  }
+  static __device__ __forceinline__ v4f mfma(v2u a, v2u b, v4f c) {
+    return __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(__builtin_bit_cast(s16x4, a), __builtin_bit_cast(s16x4, b), c, 0,
+                                                     0, 0);
   }
   static __device__ __forceinline__ uint32_t pack(float x, float y) {   // round to nearest even
     const v2f f = {x, y};
@@ -64,6 +75,10 @@ struct Fp16 {
   static __device__ __forceinline__ v4f mfma(v4u a, v4u b, v4f c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0,
                                                   0, 0);
+  }
+  static __device__ __forceinline__ v4f mfma(v2u a, v2u b, v4f c) {
+    return __builtin_amdgcn_mfma_f32_16x16x16f16(__builtin_bit_cast(f16x4, a), __builtin_bit_cast(f16x4, b), c, 0, 0,
+                                                 0);
   }
   static __device__ __forceinline__ uint32_t pack(float x, float y) {
     const v2f f = {x, y};
@@ -92,19 +107,36 @@ __device__ __forceinline__ float groups_sum(float x) {
   return __uint_as_float(s[0]) + __uint_as_float(s[1]);
 }
 
+// Passes matrix results on once they can be read, for a branch that overwrites a part of
+// them under a mask: behind such a branch this compiler has left out the wait for the
+// parts that it does not overwrite. A 16x16x32 product takes eight wait states.
+__device__ __forceinline__ void settle(v4f (&s)[1][1]) { __asm__ __volatile__("s_nop 7" : "+v"(s[0][0])); }
+__device__ __forceinline__ void settle(v4f (&s)[1][2]) {
+  __asm__ __volatile__("s_nop 7" : "+v"(s[0][0]), "+v"(s[0][1]));
+}
+__device__ __forceinline__ void settle(v4f (&s)[2][2]) {
+  __asm__ __volatile__("s_nop 7" : "+v"(s[0][0]), "+v"(s[0][1]), "+v"(s[1][0]), "+v"(s[1][1]));
+}
+
 // The registers and steps of one wave: NQ tiles of 16 query heads of one row and
-// key head, 32 positions at a time.
-template <class T, bool E4M3, int D, int NQ>
+// key head, POS (16 or 32) positions at a time.
+template <class T, bool E4M3, int D, int NQ, int POS = 32, bool QL = false>
 struct Wave {
+  static constexpr int kPositions = POS;
   static constexpr int kBytes = E4M3 ? 1 : 2;
   static constexpr int kChunks = D / 32;                 // matrix steps over the dims
   static constexpr int kLoads = D * kBytes / 64;         // 16-byte key loads per lane and position
   static constexpr int kDims = D / 16;                   // dims of a position that a lane's values hold
   static constexpr int kWords = kDims * kBytes / 4;      // and their registers
+  static constexpr int kTiles = POS / 16;                // matrix tiles of positions
+  static constexpr int kMine = POS / 4;                  // positions whose weights and values this lane holds
+  static constexpr bool kShared = QL;                    // the queries lie in LDS
+  typedef typename Pick<POS == 32, v4u, v2u>::type P;    // weights of kMine positions, packed
 
-  v4u q[NQ][kChunks];
-  v4u k[2][kLoads];
-  uint32_t v[8][kWords];
+  v4u q[kShared ? 1 : NQ][kShared ? 1 : kChunks];
+  const v4u* q_lds;
+  v4u k[kTiles][kLoads];
+  uint32_t v[kMine][kWords];
   v4f o[NQ][kDims];
   float m[NQ];   // running maximum in the log2 domain, equal in the four lane groups
   float l[NQ];   // this lane's part of the sum
@@ -126,29 +158,44 @@ struct Wave {
     }
   }
 
-  // Query heads [0, rows) at `p`, one after another; the dims of a step are those
-  // that the key loads put there.
-  __device__ __forceinline__ void load_q(const char* p, int rows, uint32_t flip) {
+  // Which of the POS positions this lane's j-th one is.
+  __device__ __forceinline__ int mine(int j) const { return 16 * (j >> 2) + 4 * grp + (j & 3); }
+
+  // This lane's part of step c of query tile n: of heads [0, rows) at `p`, one after
+  // another, the dims that the keys' pieces hold there.
+  __device__ __forceinline__ v4u query(const char* p, int n, int c, int rows, uint32_t flip) const {
+    const int h = 16 * n + col;
+    const int dim = E4M3 ? 64 * (c >> 1) + 16 * grp + 8 * (c & 1) : 32 * c + 8 * grp;
+    v4u x = {0, 0, 0, 0};
+    if (h < rows) x = *reinterpret_cast<const v4u*>(p + (static_cast<int64_t>(h) * D + dim) * 2);
+    return x ^ v4u{flip, flip, flip, flip};
+  }
+
+  // Loads the queries: into registers, or by the whole workgroup into `lds`
+  // (NQ * kChunks * 64 of it; a barrier must follow, and one precede).
+  __device__ __forceinline__ void load_q(const char* p, int rows, uint32_t flip, v4u* lds) {
+    if constexpr (kShared) {
+      q_lds = lds + lane;
 #pragma unroll
-    for (int n = 0; n < NQ; ++n) {
-      const int h = 16 * n + col;
-#pragma unroll
-      for (int c = 0; c < kChunks; ++c) {
-        const int dim = E4M3 ? 64 * (c >> 1) + 16 * grp + 8 * (c & 1) : 32 * c + 8 * grp;
-        v4u x = {0, 0, 0, 0};
-        if (h < rows) x = *reinterpret_cast<const v4u*>(p + (static_cast<int64_t>(h) * D + dim) * 2);
-        q[n][c] = x ^ v4u{flip, flip, flip, flip};
+      for (int i = 0; i < NQ * kChunks; i += kWaves) {
+        const int x = i + (threadIdx.x >> 6);
+        lds[64 * x + lane] = query(p, x / kChunks, x % kChunks, rows, flip);
       }
+    } else {
+#pragma unroll
+      for (int n = 0; n < NQ; ++n)
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) q[n][c] = query(p, n, c, rows, flip);
     }
   }
 
-  // Position a * 16 + col of the tile is at `p`.
+  // Position a * 16 + col is at `p`.
   __device__ __forceinline__ void load_k(int a, const char* p) {
 #pragma unroll
     for (int c = 0; c < kLoads; ++c) k[a][c] = *reinterpret_cast<const v4u*>(p + 64 * c + 16 * grp);
   }
 
-  // Position 16 (j / 4) + 4 grp + j % 4 of the tile is at `p`.
+  // Position mine(j) is at `p`.
   __device__ __forceinline__ void load_v(int j, const char* p) {
     const char* at = p + col * (kWords * 4);
     if constexpr (kWords == 1) {
@@ -161,50 +208,72 @@ struct Wave {
 #pragma unroll
       for (int e = 0; e < kWords; e += 4) {
         const v4u x = *reinterpret_cast<const v4u*>(at + 4 * e);
-        v[j][e] = x.x;
-        v[j][e + 1] = x.y;
-        v[j][e + 2] = x.z;
-        v[j][e + 3] = x.w;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[j][e + i] = x[i];
       }
     }
   }
 
-  __device__ __forceinline__ void scores(v4f (&s)[NQ][2]) {
+  __device__ __forceinline__ void scores(v4f (&s)[NQ][kTiles]) {
+    const v4u* queries = q_lds;
+    if constexpr (kShared) __asm__ __volatile__("" : "+v"(queries));   // read anew for every tile, not kept in registers
 #pragma unroll
-    for (int a = 0; a < 2; ++a) {
+    for (int n = 0; n < NQ; ++n)
 #pragma unroll
-      for (int n = 0; n < NQ; ++n) s[n][a] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+      for (int a = 0; a < kTiles; ++a) s[n][a] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int c = 0; c < kChunks; ++c) {
-        v4u x;
+    for (int c = 0; c < kChunks; ++c) {
+      v4u x[kTiles];
+#pragma unroll
+      for (int a = 0; a < kTiles; ++a) {
         if constexpr (E4M3) {
           const uint32_t w0 = k[a][c >> 1][2 * (c & 1)], w1 = k[a][c >> 1][2 * (c & 1) + 1];
-          x = v4u{T::template from_e4m3<false>(w0), T::template from_e4m3<true>(w0),
-                  T::template from_e4m3<false>(w1), T::template from_e4m3<true>(w1)};
+          x[a] = v4u{T::template from_e4m3<false>(w0), T::template from_e4m3<true>(w0),
+                     T::template from_e4m3<false>(w1), T::template from_e4m3<true>(w1)};
         } else {
-          x = k[a][c];
+          x[a] = k[a][c];
         }
+      }
 #pragma unroll
-        for (int n = 0; n < NQ; ++n) s[n][a] = T::mfma(x, q[n][c], s[n][a]);
+      for (int n = 0; n < NQ; ++n) {
+        v4u y;
+        if constexpr (kShared) y = queries[(n * kChunks + c) * 64];
+        else y = q[n][c];
+#pragma unroll
+        for (int a = 0; a < kTiles; ++a) s[n][a] = T::mfma(x[a], y, s[n][a]);
       }
     }
+  }
+
+  // The largest of this lane's scores.
+  static __device__ __forceinline__ float highest(const v4f (&s)[kTiles]) {
+    float x = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3]));
+#pragma unroll
+    for (int a = 1; a < kTiles; ++a) x = fmaxf(x, fmaxf(fmaxf(s[a][0], s[a][1]), fmaxf(s[a][2], s[a][3])));
+    return x;
   }
 
   // Scores to weights; `inside` bit j says whether this lane's j-th position counts
-  // (all ones: every one). Returns the weights packed as the second product's operand.
-  __device__ __forceinline__ void weights(v4f (&s)[NQ][2], float c, bool edge, uint32_t inside, v4u (&p)[NQ]) {
+  // (looked at where `edge`). Returns the weights packed as the second product's operand.
+  __device__ __forceinline__ void weights(v4f (&s)[NQ][kTiles], float c, bool edge, uint32_t inside, P (&p)[NQ]) {
     float top[NQ];
+    if (edge) {
+      settle(s);
+#pragma unroll
+      for (int n = 0; n < NQ; ++n) {
+#pragma unroll
+        for (int j = 0; j < kMine; ++j)
+          if (!(inside >> j & 1)) s[n][j >> 2][j & 3] = -__builtin_inff();
+        top[n] = highest(s[n]);
+      }
+    } else {
+#pragma unroll
+      for (int n = 0; n < NQ; ++n) top[n] = highest(s[n]);
+    }
     bool rise = false;
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
-      if (edge) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (!(inside >> j & 1)) s[n][j >> 2][j & 3] = -__builtin_inff();
-      }
-      float x = fmaxf(fmaxf(fmaxf(s[n][0][0], s[n][0][1]), fmaxf(s[n][0][2], s[n][0][3])),
-                      fmaxf(fmaxf(s[n][1][0], s[n][1][1]), fmaxf(s[n][1][2], s[n][1][3])));
-      top[n] = groups_max(x) * c;
+      top[n] = groups_max(top[n]) * c;
       rise |= top[n] > m[n];
     }
     if (__any(rise)) {   // rare after the first tiles
@@ -221,18 +290,21 @@ struct Wave {
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
       const float ref = m[n] == -__builtin_inff() ? 0.0f : m[n];
-      float w[8];
+      float w[kMine];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
+      for (int j = 0; j < kMine; ++j) {
         w[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n][j >> 2][j & 3], c, -ref));
         if (edge) w[j] = (inside >> j & 1) ? w[j] : 0.0f;
       }
-      l[n] += ((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7]));
-      p[n] = v4u{T::pack(w[0], w[1]), T::pack(w[2], w[3]), T::pack(w[4], w[5]), T::pack(w[6], w[7])};
+      float sum = (w[0] + w[1]) + (w[2] + w[3]);
+      if constexpr (POS == 32) sum += (w[4] + w[5]) + (w[6] + w[7]);
+      l[n] += sum;
+#pragma unroll
+      for (int j = 0; j < kMine / 2; ++j) p[n][j] = T::pack(w[2 * j], w[2 * j + 1]);
     }
   }
 
-  // Register e of dims pair e of position j, in the query's type.
+  // Dims 2 e and 2 e + 1 of this lane's position j, in the query's type.
   __device__ __forceinline__ uint32_t dims_pair(int j, int e) {
     if constexpr (E4M3) {
       return (e & 1) ? T::template from_e4m3<true>(v[j][e >> 1]) : T::template from_e4m3<false>(v[j][e >> 1]);
@@ -244,20 +316,20 @@ struct Wave {
   // Values outside the window are whatever the cache holds there, NaN perhaps.
   __device__ __forceinline__ void clear_outside(uint32_t inside) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
+    for (int j = 0; j < kMine; ++j)
 #pragma unroll
       for (int e = 0; e < kWords; ++e) v[j][e] = (inside >> j & 1) ? v[j][e] : 0u;
   }
 
-  __device__ __forceinline__ void add_values(const v4u (&p)[NQ]) {
+  __device__ __forceinline__ void add_values(const P (&p)[NQ]) {
 #pragma unroll
     for (int e = 0; e < kDims / 2; ++e) {
-      uint32_t w[8];
+      uint32_t w[kMine];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) w[j] = dims_pair(j, e);
-      v4u even, odd;
+      for (int j = 0; j < kMine; ++j) w[j] = dims_pair(j, e);
+      P even, odd;
 #pragma unroll
-      for (int jj = 0; jj < 4; ++jj) {
+      for (int jj = 0; jj < kMine / 2; ++jj) {
         even[jj] = __builtin_amdgcn_perm(w[2 * jj + 1], w[2 * jj], 0x05040100u);   // low halves
         odd[jj] = __builtin_amdgcn_perm(w[2 * jj + 1], w[2 * jj], 0x07060302u);    // high halves
       }
@@ -270,71 +342,465 @@ struct Wave {
   }
 };
 
-// Joins the four waves' results in LDS and writes the heads' outputs, or their
-// partial sums where part_o is not null. `bad`: this wave met an invalid page.
-template <class T, int D, int NQ>
+// --- up to 16 heads: keys and values in registers ---------------------------------
+//
+// The four waves of a workgroup take every fourth tile of 32 positions. The next
+// tile's keys are loaded into the registers that the first product has just read,
+// its values into those that the second has.
+
+// Joins the four waves' results in LDS and writes the heads' outputs, or their partial
+// sums where part_o is not null. `bad`: an invalid page or slot was met.
+template <class T, int D>
 struct Merge {
-  static constexpr int kPitch = D + 4;
+  static constexpr int kPart = D < 128 ? D : 128;   // dims of a head at a time, so that LDS holds two workgroups or more
+  static constexpr int kPitch = kPart + 4;
   float o[kWaves][16][kPitch];
-  float2 ml[kWaves][NQ * 16];
-  float2 fin[NQ * 16];
+  float2 ml[kWaves][16];
+  float2 fin[16];
 
   template <class W>
   __device__ __forceinline__ void run(W& w, bool bad, int rows, float v_scale, char* out, float* lse, float* part_o,
                                       float2* part_ml) {
     const int wave = threadIdx.x >> 6;
     __syncthreads();   // the previous use of this memory is over
-#pragma unroll
-    for (int n = 0; n < NQ; ++n) {
-      const float sum = groups_sum(w.l[n]);
-      if (w.grp == 0) ml[wave][16 * n + w.col] = make_float2(w.m[n], bad ? __builtin_nanf("") : sum);
-    }
+    const float mine = groups_sum(w.l[0]);
+    if (w.grp == 0) ml[wave][w.col] = make_float2(w.m[0], bad ? __builtin_nanf("") : mine);
     __syncthreads();
-    float f[NQ];
+    float2 x[kWaves];
+    float top = -__builtin_inff(), total = 0.0f;
 #pragma unroll
-    for (int n = 0; n < NQ; ++n) {
-      float2 x[kWaves];
-      float top = -__builtin_inff(), sum = 0.0f;
-#pragma unroll
-      for (int i = 0; i < kWaves; ++i) {
-        x[i] = ml[i][16 * n + w.col];
-        top = fmaxf(top, x[i].x);
-      }
-      const float ref = top == -__builtin_inff() ? 0.0f : top;
-#pragma unroll
-      for (int i = 0; i < kWaves; ++i) sum += x[i].y * __builtin_amdgcn_exp2f(x[i].x - ref);
-      f[n] = __builtin_amdgcn_exp2f(w.m[n] - ref);
-      if (wave == 0 && w.grp == 0) fin[16 * n + w.col] = make_float2(top, sum);
+    for (int i = 0; i < kWaves; ++i) {
+      x[i] = ml[i][w.col];
+      top = fmaxf(top, x[i].x);
     }
+    const float ref = top == -__builtin_inff() ? 0.0f : top;
 #pragma unroll
-    for (int n = 0; n < NQ; ++n) {
-      if (n > 0) __syncthreads();
+    for (int i = 0; i < kWaves; ++i) total += x[i].y * __builtin_amdgcn_exp2f(x[i].x - ref);
+    const float f = __builtin_amdgcn_exp2f(w.m[0] - ref);
+    if (wave == 0 && w.grp == 0) fin[w.col] = make_float2(top, total);
+    constexpr int kT = kPart / 16;   // matrix tiles of a part
+#pragma unroll
+    for (int t0 = 0; t0 < W::kDims; t0 += kT) {
+      if (t0 > 0) __syncthreads();
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int t = 0; t < W::kDims; t += 4) {
-          float* at = &o[wave][w.col][(4 * w.grp + i) * W::kDims + t];
-          *reinterpret_cast<v4f*>(at) = v4f{w.o[n][t][i] * f[n], w.o[n][t + 1][i] * f[n], w.o[n][t + 2][i] * f[n],
-                                            w.o[n][t + 3][i] * f[n]};
-        }
+        for (int t = 0; t < kT; t += 4)
+          *reinterpret_cast<v4f*>(&o[wave][w.col][(4 * w.grp + i) * kT + t]) =
+              v4f{w.o[0][t0 + t][i] * f, w.o[0][t0 + t + 1][i] * f, w.o[0][t0 + t + 2][i] * f,
+                  w.o[0][t0 + t + 3][i] * f};
       __syncthreads();
-      for (int x = threadIdx.x; x < 16 * D / 4; x += kThreads) {
-        const int h = x / (D / 4), d = 4 * (x % (D / 4)), head = 16 * n + h;
+      for (int e = threadIdx.x; e < 16 * kPart / 4; e += kThreads) {
+        const int head = e / (kPart / 4), at = 4 * (e % (kPart / 4));
+        const int d = at / kT * W::kDims + t0 + at % kT;
         if (head >= rows) continue;
-        v4f sum = *reinterpret_cast<const v4f*>(&o[0][h][d]);
+        v4f sum = *reinterpret_cast<const v4f*>(&o[0][head][at]);
 #pragma unroll
-        for (int i = 1; i < kWaves; ++i) sum += *reinterpret_cast<const v4f*>(&o[i][h][d]);
-        const float2 e = fin[head];
+        for (int i = 1; i < kWaves; ++i) sum += *reinterpret_cast<const v4f*>(&o[i][head][at]);
+        const float2 e2 = fin[head];
         if (part_o != nullptr) {
           *reinterpret_cast<v4f*>(part_o + static_cast<int64_t>(head) * D + d) = sum;
-          if (d == 0) part_ml[head] = e;
+          if (d == 0) part_ml[head] = e2;
         } else {
-          const float inv = v_scale / e.y;
+          const float inv = v_scale / e2.y;
           const v2u y = {T::pack(sum[0] * inv, sum[1] * inv), T::pack(sum[2] * inv, sum[3] * inv)};
           *reinterpret_cast<v2u*>(out + (static_cast<int64_t>(head) * D + d) * 2) = y;
-          if (d == 0 && lse != nullptr) lse[head] = (e.x + __builtin_amdgcn_logf(e.y)) * kLn2;
+          if (d == 0 && lse != nullptr) lse[head] = (e2.x + __builtin_amdgcn_logf(e2.y)) * kLn2;
         }
       }
+    }
+  }
+};
+
+// This wave's tiles t, t + kWaves, ... below t_hi; range(t, &lo, &hi) gives the positions of a tile that count.
+template <class W, class KEYS, class VALUES, class RANGE>
+__device__ __forceinline__ void run_tiles(W& w, int t, int t_hi, float c, KEYS&& load_keys, VALUES&& load_values,
+                                          RANGE&& range) {
+  if (t >= t_hi) return;
+  load_keys(t);
+  load_values(t);
+  while (true) {
+    const int tn = t + kWaves;
+    const bool more = tn < t_hi;
+    int lo, hi;
+    range(t, &lo, &hi);
+    const bool edge = lo > 0 || hi < W::kPositions;
+    uint32_t inside = 0xFFu;
+    if (edge) {
+      inside = 0;
+#pragma unroll
+      for (int j = 0; j < W::kMine; ++j) inside |= (w.mine(j) >= lo && w.mine(j) < hi ? 1u : 0u) << j;
+    }
+    v4f s[1][W::kTiles];
+    typename W::P p[1];
+    w.scores(s);
+    if (more) load_keys(tn);
+    w.weights(s, c, edge, inside, p);
+    if (edge) w.clear_outside(inside);
+    w.add_values(p);
+    if (!more) break;
+    load_values(tn);
+    t = tn;
+  }
+}
+
+// Positions of a register tile: 32, or 16 where D = 256 in 16 bits would need more registers than
+// two waves per SIMD leave.
+constexpr int register_tile(int D, bool e4m3) { return D == 256 && !e4m3 ? 16 : 32; }
+
+// --- more heads: positions staged in LDS ------------------------------------------
+//
+// Two waves (a half) carry the first heads, two the others; each takes half of a stage
+// of kStagePos positions (a page, or half of one). Asynchronous copies (memory to LDS, no
+// registers) write the stages, kStages in turn, so that every byte crosses from the caches
+// once, in whole rows, whatever the number of heads.
+//
+// The compiler would wait for every copy in flight before an LDS read that it
+// cannot prove apart from them; the reads are inline assembly for that reason, each
+// block with its own wait, and the copies are waited for by count before the
+// barrier that hands a stage over. Keys lie with the 16-byte pieces of a row permuted by
+// its position (piece ^ swizzle), which the copies' source addresses do, so that
+// the rows that one read takes fall on different banks.
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+  return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((const __attribute__((address_space(3))) void*)p));
+}
+
+template <int OFF>
+__device__ __forceinline__ void read4(uint32_t at, uint32_t at2, v4u& a, v4u& b, v4u& c, v4u& d) {
+  __asm__ __volatile__(
+      "ds_read_b128 %0, %4 offset:%6\n\tds_read_b128 %1, %5 offset:%6\n\t"
+      "ds_read_b128 %2, %4 offset:%7\n\tds_read_b128 %3, %5 offset:%7\n\ts_waitcnt lgkmcnt(0)"
+      : "=&v"(a), "=&v"(b), "=&v"(c), "=&v"(d)
+      : "v"(at), "v"(at2), "n"(OFF), "n"(OFF + 128)
+      : "memory");
+}
+
+template <class T, bool E4M3, int D, int NQ>
+struct Ring {
+  static constexpr int kParts = 2;
+  static constexpr int kPos = D < 256 ? 32 : 16;             // positions of a wave
+  typedef Wave<T, E4M3, D, NQ, kPos> W;
+  static constexpr int kStagePos = kParts * kPos;
+  static constexpr int kRow = D * W::kBytes;                 // bytes of one position
+  static constexpr int kImage = kStagePos * kRow;            // of a stage's keys, or values
+  static constexpr int kStages = kImage >= 16384 ? 2 : 4;
+  static constexpr int kCopies = kImage / 1024 / kWaves;     // 1 KiB copies per wave, of keys and of values each
+  static constexpr int kCopyRows = 1024 / kRow;
+  static constexpr int kPieces = kRow / 16;
+  static constexpr int kHeads = 2 * 16 * NQ;
+  char stage[kStages][2][kImage];
+  float2 ml[2][kParts][16 * NQ];
+
+  static __device__ __forceinline__ int swizzle(int row) { return kRow >= 128 ? row & 7 : row >> 1 & 3; }
+
+  // Position of the stage that this lane fetches in copy c of its wave.
+  static __device__ __forceinline__ int copy_row(int wave, int c, int lane) {
+    return (wave * kCopies + c) * kCopyRows + lane / kPieces;
+  }
+
+  __device__ __forceinline__ void copy(int s, int kv, int wave, int c, const char* src) {
+    __builtin_amdgcn_global_load_lds(src, &stage[s][kv][(wave * kCopies + c) * 1024], 16, 0, 0);
+  }
+
+  // Waits until at most `left` (0, 1 or 2) later stages of this wave's copies are in flight, then for the
+  // other waves.
+  static __device__ __forceinline__ void hand_over(int left) {
+    constexpr int kPer = 2 * kCopies;
+    if (kStages > 2 && left >= 2) __asm__ __volatile__("s_waitcnt vmcnt(%0)" ::"n"(2 * kPer) : "memory");
+    else if (kStages > 2 && left == 1) __asm__ __volatile__("s_waitcnt vmcnt(%0)" ::"n"(kPer) : "memory");
+    else __asm__ __volatile__("s_waitcnt vmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    __asm__ __volatile__("" ::: "memory");
+  }
+
+  // A word of LDS, by hand as the stages' reads are.
+  static __device__ __forceinline__ int read_word(uint32_t at) {
+    int x;
+    __asm__ __volatile__("ds_read_b32 %0, %1\n\ts_waitcnt lgkmcnt(0)" : "=&v"(x) : "v"(at) : "memory");
+    return x;
+  }
+
+  // The piece of a row that a lane fetches for its place in LDS.
+  static __device__ __forceinline__ int source_piece(int kv, int row, int lane) {
+    return kv == 0 ? lane % kPieces ^ swizzle(row) : lane % kPieces;
+  }
+
+  // This wave's copies of stage i: positions from `base` on of the page whose keys are at kp and
+  // values at vp; [lo, hi) of the page are inside the window, the lanes of others read the nearest one inside.
+  __device__ __forceinline__ void copy_page(const KvAttnArgs& a, const char* kp, const char* vp, int i, int wave,
+                                            int lane, int base, int lo, int hi) {
+#pragma unroll
+    for (int c = 0; c < kCopies; ++c) {
+      const int row = copy_row(wave, c, lane);
+      const int pos = min(max(base + row, lo), hi - 1);
+      copy(i % kStages, 0, wave, c,
+           kp + static_cast<uint32_t>(pos * static_cast<int>(a.k_pos)) + 16 * source_piece(0, row, lane));
+      copy(i % kStages, 1, wave, c,
+           vp + static_cast<uint32_t>(pos * static_cast<int>(a.v_pos)) + 16 * source_piece(1, row, lane));
+    }
+  }
+
+  // The same of stage i of a list of `len` slots in LDS (the last one again behind its end). Strides
+  // are multiples of 16 bytes, a page's below 2^36: their products take one 32-bit multiplication.
+  __device__ __forceinline__ void copy_list(const KvAttnArgs& a, const char* kb, const char* vb, int i, int wave,
+                                            int lane, uint32_t list, int len) {
+    const uint32_t k_page = static_cast<uint32_t>(a.k_page >> 4), v_page = static_cast<uint32_t>(a.v_page >> 4);
+    const uint32_t k_pos = static_cast<uint32_t>(a.k_pos >> 4), v_pos = static_cast<uint32_t>(a.v_pos >> 4);
+    int slot[kCopies];
+#pragma unroll
+    for (int c = 0; c < kCopies; ++c)
+      slot[c] = read_word(list + 4 * min(kStagePos * i + copy_row(wave, c, lane), len - 1));
+#pragma unroll
+    for (int c = 0; c < kCopies; ++c) {
+      const int row = copy_row(wave, c, lane);
+      const uint32_t page = static_cast<uint32_t>(slot[c]) >> 6, pos = static_cast<uint32_t>(slot[c]) & 63;
+      const uint64_t k_off = static_cast<uint64_t>(page) * k_page + pos * k_pos;
+      const uint64_t v_off = static_cast<uint64_t>(page) * v_page + pos * v_pos;
+      copy(i % kStages, 0, wave, c, kb + (k_off << 4) + 16 * source_piece(0, row, lane));
+      copy(i % kStages, 1, wave, c, vb + (v_off << 4) + 16 * source_piece(1, row, lane));
+    }
+  }
+
+  // Keys of positions kPos part + 16 a + col into w.k.
+  __device__ __forceinline__ void read_keys(W& w, int s, int part) {
+    const int z = swizzle(w.col);
+    const uint32_t row = lds_address(&stage[s][0][0]) + (kPos * part + w.col) * kRow + 16 * (w.grp ^ (z & 3));
+    const uint32_t even = row + 64 * (z >> 2), odd = row + 64 * (1 - (z >> 2));
+    if constexpr (kRow == 512) {
+      static_assert(W::kTiles == 1, "16 positions per wave");
+      read4<0>(even, odd, w.k[0][0], w.k[0][1], w.k[0][2], w.k[0][3]);
+      read4<256>(even, odd, w.k[0][4], w.k[0][5], w.k[0][6], w.k[0][7]);
+    } else if constexpr (kRow == 256) {
+      if constexpr (W::kTiles == 1) {
+        read4<0>(even, odd, w.k[0][0], w.k[0][1], w.k[0][2], w.k[0][3]);
+      } else {
+        __asm__ __volatile__(
+            "ds_read_b128 %0, %8\n\tds_read_b128 %1, %9\n\t"
+            "ds_read_b128 %2, %8 offset:128\n\tds_read_b128 %3, %9 offset:128\n\t"
+            "ds_read_b128 %4, %8 offset:4096\n\tds_read_b128 %5, %9 offset:4096\n\t"
+            "ds_read_b128 %6, %8 offset:4224\n\tds_read_b128 %7, %9 offset:4224\n\ts_waitcnt lgkmcnt(0)"
+            : "=&v"(w.k[0][0]), "=&v"(w.k[0][1]), "=&v"(w.k[0][2]), "=&v"(w.k[0][3]), "=&v"(w.k[1][0]),
+              "=&v"(w.k[1][1]), "=&v"(w.k[1][2]), "=&v"(w.k[1][3])
+            : "v"(even), "v"(odd)
+            : "memory");
+      }
+    } else if constexpr (kRow == 128) {
+      static_assert(W::kTiles == 2, "D < 256");
+      __asm__ __volatile__(
+          "ds_read_b128 %0, %4\n\tds_read_b128 %1, %5\n\t"
+          "ds_read_b128 %2, %4 offset:2048\n\tds_read_b128 %3, %5 offset:2048\n\ts_waitcnt lgkmcnt(0)"
+          : "=&v"(w.k[0][0]), "=&v"(w.k[0][1]), "=&v"(w.k[1][0]), "=&v"(w.k[1][1])
+          : "v"(even), "v"(odd)
+          : "memory");
+    } else {
+      __asm__ __volatile__("ds_read_b128 %0, %2\n\tds_read_b128 %1, %2 offset:1024\n\ts_waitcnt lgkmcnt(0)"
+                           : "=&v"(w.k[0][0]), "=&v"(w.k[1][0])
+                           : "v"(row)
+                           : "memory");
+    }
+  }
+
+  // Values of this lane's positions into w.v.
+  __device__ __forceinline__ void read_values(W& w, int s, int part) {
+    const uint32_t at = lds_address(&stage[s][1][0]) + (kPos * part + 4 * w.grp) * kRow + w.col * (kRow / 16);
+    if constexpr (kRow == 512) {
+      v4u x[8];
+      __asm__ __volatile__(
+          "ds_read_b128 %0, %8\n\tds_read_b128 %1, %8 offset:16\n\t"
+          "ds_read_b128 %2, %8 offset:512\n\tds_read_b128 %3, %8 offset:528\n\t"
+          "ds_read_b128 %4, %8 offset:1024\n\tds_read_b128 %5, %8 offset:1040\n\t"
+          "ds_read_b128 %6, %8 offset:1536\n\tds_read_b128 %7, %8 offset:1552\n\ts_waitcnt lgkmcnt(0)"
+          : "=&v"(x[0]), "=&v"(x[1]), "=&v"(x[2]), "=&v"(x[3]), "=&v"(x[4]), "=&v"(x[5]), "=&v"(x[6]), "=&v"(x[7])
+          : "v"(at)
+          : "memory");
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w.v[j / 2][4 * (j & 1) + e] = x[j][e];
+    } else if constexpr (kRow == 256 && W::kTiles == 1) {
+      v4u x[4];
+      __asm__ __volatile__(
+          "ds_read_b128 %0, %4\n\tds_read_b128 %1, %4 offset:256\n\t"
+          "ds_read_b128 %2, %4 offset:512\n\tds_read_b128 %3, %4 offset:768\n\ts_waitcnt lgkmcnt(0)"
+          : "=&v"(x[0]), "=&v"(x[1]), "=&v"(x[2]), "=&v"(x[3])
+          : "v"(at)
+          : "memory");
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w.v[j][e] = x[j][e];
+    } else if constexpr (kRow == 256) {
+      v4u x[8];
+      __asm__ __volatile__(
+          "ds_read_b128 %0, %8\n\tds_read_b128 %1, %8 offset:256\n\t"
+          "ds_read_b128 %2, %8 offset:512\n\tds_read_b128 %3, %8 offset:768\n\t"
+          "ds_read_b128 %4, %8 offset:4096\n\tds_read_b128 %5, %8 offset:4352\n\t"
+          "ds_read_b128 %6, %8 offset:4608\n\tds_read_b128 %7, %8 offset:4864\n\ts_waitcnt lgkmcnt(0)"
+          : "=&v"(x[0]), "=&v"(x[1]), "=&v"(x[2]), "=&v"(x[3]), "=&v"(x[4]), "=&v"(x[5]), "=&v"(x[6]), "=&v"(x[7])
+          : "v"(at)
+          : "memory");
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w.v[j][e] = x[j][e];
+    } else if constexpr (kRow == 128) {
+      v2u x[8];
+      __asm__ __volatile__(
+          "ds_read_b64 %0, %8\n\tds_read_b64 %1, %8 offset:128\n\t"
+          "ds_read_b64 %2, %8 offset:256\n\tds_read_b64 %3, %8 offset:384\n\t"
+          "ds_read_b64 %4, %8 offset:2048\n\tds_read_b64 %5, %8 offset:2176\n\t"
+          "ds_read_b64 %6, %8 offset:2304\n\tds_read_b64 %7, %8 offset:2432\n\ts_waitcnt lgkmcnt(0)"
+          : "=&v"(x[0]), "=&v"(x[1]), "=&v"(x[2]), "=&v"(x[3]), "=&v"(x[4]), "=&v"(x[5]), "=&v"(x[6]), "=&v"(x[7])
+          : "v"(at)
+          : "memory");
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) w.v[j][e] = x[j][e];
+    } else {
+      static_assert(kRow == 64 && W::kTiles == 2, "D = 64 in 8 bits");
+      __asm__ __volatile__(
+          "ds_read_b32 %0, %8\n\tds_read_b32 %1, %8 offset:64\n\t"
+          "ds_read_b32 %2, %8 offset:128\n\tds_read_b32 %3, %8 offset:192\n\t"
+          "ds_read_b32 %4, %8 offset:1024\n\tds_read_b32 %5, %8 offset:1088\n\t"
+          "ds_read_b32 %6, %8 offset:1152\n\tds_read_b32 %7, %8 offset:1216\n\ts_waitcnt lgkmcnt(0)"
+          : "=&v"(w.v[0][0]), "=&v"(w.v[1][0]), "=&v"(w.v[2][0]), "=&v"(w.v[3][0]), "=&v"(w.v[4][0]),
+            "=&v"(w.v[5][0]), "=&v"(w.v[6][0]), "=&v"(w.v[7][0])
+          : "v"(at)
+          : "memory");
+    }
+  }
+
+  // Runs the n stages of one segment or list. fetch(i) issues this wave's copies of
+  // stage i; range(i, &lo, &hi) gives the positions of the stage that count.
+  template <class FETCH, class RANGE>
+  __device__ __forceinline__ void run(W& w, int n, int part, float c, FETCH&& fetch, RANGE&& range) {
+    // no other load or store of this wave is in flight when the copies are counted
+    __asm__ __volatile__("s_waitcnt vmcnt(0)" ::: "memory");
+    constexpr int kAhead = kStages - 1;
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (i < n) {
+        fetch(i);
+        __asm__ __volatile__("" ::: "memory");   // a stage's copies are counted before the next one's
+      }
+    for (int i = 0; i < n; ++i) {
+      hand_over(min(n - 1 - i, kAhead - 1));
+      if (i + kAhead < n) {
+        fetch(i + kAhead);
+        __asm__ __volatile__("" ::: "memory");
+      }
+      int lo, hi;
+      range(i, &lo, &hi);
+      lo -= kPos * part;
+      hi -= kPos * part;
+      if (lo >= kPos || hi <= 0) continue;
+      const bool edge = lo > 0 || hi < kPos;
+      uint32_t inside = 0xFFu;
+      if (edge) {
+        inside = 0;
+#pragma unroll
+        for (int j = 0; j < W::kMine; ++j) inside |= (w.mine(j) >= lo && w.mine(j) < hi ? 1u : 0u) << j;
+      }
+      v4f x[NQ][W::kTiles];
+      typename W::P p[NQ];
+      read_keys(w, i % kStages, part);
+      w.scores(x);
+      w.weights(x, c, edge, inside, p);
+      read_values(w, i % kStages, part);
+      if (edge) w.clear_outside(inside);
+      w.add_values(p);
+    }
+  }
+
+  // Joins a half's waves and writes its heads' outputs, or their partial sums where
+  // part_o is not null. `bad`: an invalid page or slot was met. The stages' memory
+  // carries the sums; either wave adds and writes half of them.
+  __device__ __forceinline__ void finish(W& w, int half, int part, bool bad, int rows, float v_scale, char* out,
+                                         float* lse, float* part_o, float2* part_ml) {
+    constexpr int kShare = NQ * W::kDims / kParts;   // dim tiles that each wave joins
+    v4f* space = reinterpret_cast<v4f*>(&stage[0][0][0]) + half * kParts * (NQ * W::kDims) * 64 + w.lane;
+    static_assert(sizeof(stage) >= sizeof(v4f) * 2 * kParts * NQ * W::kDims * 64, "the stages hold all sums");
+    __syncthreads();   // every read of the stages is over
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+      const float sum = groups_sum(w.l[n]);
+      if (w.grp == 0) ml[half][part][16 * n + w.col] = make_float2(w.m[n], bad ? __builtin_nanf("") : sum);
+    }
+    __syncthreads();
+    float f[NQ], top[NQ], sum[NQ];
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+      float2 x[kParts];
+      top[n] = -__builtin_inff();
+#pragma unroll
+      for (int i = 0; i < kParts; ++i) {
+        x[i] = ml[half][i][16 * n + w.col];
+        top[n] = fmaxf(top[n], x[i].x);
+      }
+      const float ref = top[n] == -__builtin_inff() ? 0.0f : top[n];
+      sum[n] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kParts; ++i) sum[n] += x[i].y * __builtin_amdgcn_exp2f(x[i].x - ref);
+      f[n] = __builtin_amdgcn_exp2f(w.m[n] - ref);
+    }
+#pragma unroll
+    for (int x = 0; x < NQ * W::kDims; ++x) space[(part * NQ * W::kDims + x) * 64] = w.o[x / W::kDims][x % W::kDims] * f[x / W::kDims];
+    __syncthreads();
+    v4f got[kShare];   // tiles part * kShare .. of (query tile, dim tile) pairs: one query tile, neighbouring dims
+#pragma unroll
+    for (int x = 0; x < kShare; ++x) {
+      got[x] = space[(part * kShare + x) * 64];
+#pragma unroll
+      for (int i = 1; i < kParts; ++i) got[x] += space[(i * NQ * W::kDims + part * kShare + x) * 64];
+    }
+    const int n = part * kShare / W::kDims, t0 = part * kShare % W::kDims, head = 16 * n + w.col;
+    float inv = 0.0f, my_top = 0.0f, my_sum = 0.0f;
+#pragma unroll
+    for (int x = 0; x < NQ; ++x)
+      if (x == n) {
+        my_top = top[x];
+        my_sum = sum[x];
+      }
+    inv = v_scale / my_sum;
+    if (head < rows) {
+      const int64_t at = static_cast<int64_t>(head) * D + 4 * w.grp * W::kDims + t0;
+      if (part_o != nullptr) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          store_dims<float>(part_o + at + i * W::kDims, got, i, 1.0f);
+        if (w.grp == 0 && t0 == 0) part_ml[head] = make_float2(my_top, my_sum);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) store_dims<T>(reinterpret_cast<uint16_t*>(out) + at + i * W::kDims, got, i, inv);
+        if (w.grp == 0 && t0 == 0 && lse != nullptr) lse[head] = (my_top + __builtin_amdgcn_logf(my_sum)) * kLn2;
+      }
+    }
+    __syncthreads();   // the stages may be filled again
+  }
+
+  // Element i of each of the tiles, neighbouring dims, to `to`.
+  template <class OUT, class PTR>
+  static __device__ __forceinline__ void store_dims(PTR* to, const v4f (&x)[NQ * W::kDims / kParts], int i, float by) {
+    constexpr int kShare = NQ * W::kDims / kParts;
+    if constexpr (sizeof(PTR) == 4) {
+      if constexpr (kShare >= 4) {
+#pragma unroll
+        for (int t = 0; t < kShare; t += 4)
+          *reinterpret_cast<v4f*>(to + t) = v4f{x[t][i], x[t + 1][i], x[t + 2][i], x[t + 3][i]};
+      } else {
+#pragma unroll
+        for (int t = 0; t < kShare; ++t) to[t] = x[t][i];
+      }
+    } else if constexpr (kShare >= 4) {
+#pragma unroll
+      for (int t = 0; t < kShare; t += 4)
+        *reinterpret_cast<v2u*>(to + t) = v2u{OUT::pack(x[t][i] * by, x[t + 1][i] * by),
+                                              OUT::pack(x[t + 2][i] * by, x[t + 3][i] * by)};
+    } else if constexpr (kShare == 2) {
+      *reinterpret_cast<uint32_t*>(to) = OUT::pack(x[0][i] * by, x[1][i] * by);
+    } else {
+      *to = static_cast<PTR>(OUT::pack(x[0][i] * by, 0.0f));
     }
   }
 };
@@ -409,148 +875,221 @@ __device__ __forceinline__ int64_t unit_share(int64_t units, int64_t groups) {
   return s < 2 ? 2 : s;
 }
 
-template <class T, bool E4M3, int D, int NQ>
-__global__ void __launch_bounds__(kThreads, NQ == 1 && D < 256 ? 3 : 1) kv_decode_kernel(KvAttnArgs a) {
-  typedef Wave<T, E4M3, D, NQ> W;
-  __shared__ int64_t prefix_lds[kKvPlanRows + 1];
-  __shared__ int64_t sums[kWaves];
-  __shared__ Merge<T, D, NQ> merge;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t me = blockIdx.x;
-  const int64_t* prefix = a.prefix;
-  const int qg = (a.G + 16 * NQ - 1) / (16 * NQ);
-  const int64_t gh = static_cast<int64_t>(a.Hkv) * qg;
-  if (a.Q <= kKvPlanRows) {   // one round trip to memory, less than another launch
-    constexpr int kPer = kKvPlanRows / kThreads;
+// Integers that no kernel of this launch writes, read through the scalar cache.
+typedef const __attribute__((address_space(4))) int32_t* ScalarInts;
+__device__ __forceinline__ ScalarInts scalar_ints(const int32_t* p) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+  const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(at));
+  const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(at >> 32));
+  return reinterpret_cast<ScalarInts>(static_cast<uintptr_t>(static_cast<uint64_t>(hi) << 32 | lo));
+}
+
+// The plan of a decode launch, the same in every workgroup: pages before each row.
+template <int WAVES>
+struct Plan {
+  int64_t prefix_lds[kKvPlanRows + 1];
+  int64_t sums[WAVES];
+
+  // Returns the prefix (in LDS, or the one that kv_plan_kernel left in the workspace).
+  __device__ __forceinline__ const int64_t* make(const KvAttnArgs& a) {
+    if (a.Q > kKvPlanRows) return a.prefix;
+    // one round trip to memory, less than another launch
+    constexpr int kPer = kKvPlanRows / (64 * WAVES);
+    const bool first = blockIdx.x == 0;
     int64_t n[kPer], sum = 0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int64_t r = kPer * threadIdx.x + i;
       int code = 0;
       n[i] = r < a.Q ? row_pages(a, r, &code) : 0;
-      if (me == 0) report(a, code);
+      if (first) report(a, code);
       sum += n[i];
     }
     int64_t total;
-    int64_t at = block_scan<kWaves>(sum, sums, &total) - sum;
+    int64_t at = block_scan<WAVES>(sum, sums, &total) - sum;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int64_t r = kPer * threadIdx.x + i;
       if (r <= a.Q) {
         prefix_lds[r] = at;
-        if (me == 0) a.prefix[r] = at;
+        if (first) a.prefix[r] = at;
       }
       at += n[i];
     }
     if (threadIdx.x == 0) {
       prefix_lds[a.Q] = total;
-      if (me == 0) a.prefix[a.Q] = total;
+      if (first) a.prefix[a.Q] = total;
     }
     __syncthreads();
-    prefix = prefix_lds;
+    return prefix_lds;
   }
-  const int64_t units = prefix[a.Q] * gh;
-  const int64_t share = unit_share(units, gridDim.x);
-  int64_t cur = me * share;
-  const int64_t stop = cur + share < units ? cur + share : units;
-  const int group_rows = a.G < 16 * NQ ? a.G : 16 * NQ;
+};
 
-  W w;
-  w.init();
-  while (cur < stop) {
-    // the row that unit `cur` belongs to: the last one whose prefix is not above it
+// A workgroup's run of units, one (row, head group) at a time.
+struct Segment {
+  int64_t r;        // row
+  int g;            // head group
+  int pa, pb;       // pages [pa, pb) of the row's n
+  int64_t n;
+  int seq, start, end;
+
+  // The segment at unit `cur`, which it advances.
+  __device__ __forceinline__ void take(const KvAttnArgs& a, const int64_t* prefix, int64_t gh, int64_t* cur,
+                                       int64_t stop) {
+    // the row that the unit belongs to: the last one whose prefix is not above it
     int64_t lo = 0, hi = a.Q;
-    const int64_t page_unit = cur / gh;
+    const int64_t page_unit = *cur / gh;
     while (hi - lo > 1) {
       const int64_t mid = (lo + hi) >> 1;
       if (prefix[mid] <= page_unit) lo = mid;
       else hi = mid;
     }
-    const int64_t r = (static_cast<int64_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(lo >> 32))) << 32) |
-                      static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(lo)));
-    const int64_t n = prefix[r + 1] - prefix[r];
-    const int64_t in_row = cur - prefix[r] * gh;
-    const int g = __builtin_amdgcn_readfirstlane(static_cast<int>(in_row / n));
-    const int pa = __builtin_amdgcn_readfirstlane(static_cast<int>(in_row - g * n));
-    const int64_t left = stop - cur;
-    const int pb = __builtin_amdgcn_readfirstlane(static_cast<int>(n - pa < left ? n : pa + left));
-    cur += pb - pa;
+    r = __builtin_amdgcn_readfirstlane(static_cast<int>(lo));   // Q < 2^24
+    n = prefix[r + 1] - prefix[r];
+    const int64_t in_row = *cur - prefix[r] * gh;
+    g = __builtin_amdgcn_readfirstlane(static_cast<int>(in_row / n));
+    pa = __builtin_amdgcn_readfirstlane(static_cast<int>(in_row - g * n));
+    const int64_t left = stop - *cur;
+    pb = __builtin_amdgcn_readfirstlane(static_cast<int>(n - pa < left ? n : pa + left));
+    *cur += pb - pa;
+    seq = scalar_ints(a.seq_of_row)[r];
+    start = scalar_ints(a.row_start)[r];
+    end = scalar_ints(a.row_end)[r];
+  }
+};
 
-    const int kvh = g / qg, first = (g % qg) * 16 * NQ;
-    const int rows = a.G - first < 16 * NQ ? a.G - first : 16 * NQ;
-    const int seq = a.seq_of_row[r], start = a.row_start[r], end = a.row_end[r];
-    const int32_t* table = a.table + static_cast<int64_t>(seq) * a.max_pages;
+template <class T, bool E4M3, int D>
+__global__ void __launch_bounds__(kThreads, 2) kv_decode_kernel(KvAttnArgs a) {
+  constexpr int kTile = register_tile(D, E4M3), kPer = 64 / kTile;   // tiles of a page
+  typedef Wave<T, E4M3, D, 1, kTile> W;
+  __shared__ Plan<kWaves> plan;
+  __shared__ Merge<T, D> merge;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t* prefix = plan.make(a);
+  const int64_t units = prefix[a.Q] * a.Hkv;
+  const int64_t share = unit_share(units, gridDim.x);
+  int64_t cur = blockIdx.x * share;
+  const int64_t stop = cur + share < units ? cur + share : units;
+  W w;
+  w.init();
+  while (cur < stop) {
+    Segment sg;
+    sg.take(a, prefix, a.Hkv, &cur, stop);
+    const int64_t r = sg.r;
+    const int kvh = sg.g;
+    const int start = sg.start, end = sg.end;
+    const int32_t* table = a.table + static_cast<int64_t>(sg.seq) * a.max_pages;
     const int p0 = start >> 6;
-    const int t_lo = 2 * (p0 + pa) > (start >> 5) ? 2 * (p0 + pa) : (start >> 5);
-    const int t_hi = 2 * (p0 + pb) < ((end + 31) >> 5) ? 2 * (p0 + pb) : ((end + 31) >> 5);
+    const int t_lo = max(kPer * (p0 + sg.pa), start / kTile);
+    const int t_hi = min(kPer * (p0 + sg.pb), (end + kTile - 1) / kTile);
     const char* kb = a.k + kvh * a.k_head;
     const char* vb = a.v + kvh * a.v_head;
-    const int64_t head0 = r * a.H + static_cast<int64_t>(kvh) * a.G + first;
+    const int64_t head0 = r * a.H + static_cast<int64_t>(kvh) * a.G;
     w.start();
-    w.load_q(a.q + r * a.q_row + (static_cast<int64_t>(kvh) * a.G + first) * D * 2, rows, a.q_flip);
+    w.load_q(a.q + r * a.q_row + static_cast<int64_t>(kvh) * a.G * D * 2, a.G, a.q_flip, nullptr);
 
     bool bad = false;
-    auto page_of = [&](int t) {
-      int p = table[t >> 1];
-      if (p < 0 || p >= a.P_phys) {   // nothing of it is read; page 0 stands in
-        bad = true;
-        p = 0;
-      }
-      return p;
-    };
+    int next = t_lo + wave < t_hi ? table[(t_lo + wave) / kPer] : 0;   // entry of the next tile's page, read early
+    int64_t page = 0;
     // positions outside the window are not read: their lanes read the nearest one inside
     auto clamp = [&](int pos) { return min(max(pos, start), end - 1) & 63; };
-    auto load_keys = [&](int t, int page) {
-      const char* base = kb + page * a.k_page;
-#pragma unroll
-      for (int b = 0; b < 2; ++b)
-        w.load_k(b, base + static_cast<uint32_t>(clamp(32 * t + 16 * b + w.col) * static_cast<int>(a.k_pos)));
-    };
-    auto load_values = [&](int t, int page) {
-      const char* base = vb + page * a.v_page;
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        w.load_v(j, base + static_cast<uint32_t>(clamp(32 * t + 16 * (j >> 2) + 4 * w.grp + (j & 3)) *
-                                                 static_cast<int>(a.v_pos)));
-    };
-    int t = t_lo + wave;
-    if (t < t_hi) {
-      int page = page_of(t);
-      load_keys(t, page);
-      load_values(t, page);
-      int next_page = t + kWaves < t_hi ? page_of(t + kWaves) : 0;
-      while (true) {
-        const int tn = t + kWaves;
-        const bool more = tn < t_hi;
-        const bool edge = 32 * t < start || 32 * t + 32 > end;
-        uint32_t inside = 0xFFu;
-        if (edge) {
-          inside = 0;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const int pos = 32 * t + 16 * (j >> 2) + 4 * w.grp + (j & 3);
-            inside |= (pos >= start && pos < end ? 1u : 0u) << j;
+    run_tiles(
+        w, t_lo + wave, t_hi, a.c,
+        [&](int t) {
+          page = next;
+          if (t + kWaves < t_hi) next = table[(t + kWaves) / kPer];
+          if (page < 0 || page >= a.P_phys) {   // nothing of it is read; page 0 stands in
+            bad = true;
+            page = 0;
           }
-        }
-        v4f s[NQ][2];
-        v4u p[NQ];
-        w.scores(s);
-        if (more) load_keys(tn, next_page);
-        w.weights(s, a.c, edge, inside, p);
-        if (edge) w.clear_outside(inside);
-        w.add_values(p);
-        if (!more) break;
-        load_values(tn, next_page);
-        if (tn + kWaves < t_hi) next_page = page_of(tn + kWaves);
-        t = tn;
-      }
-    }
+          const char* base = kb + page * a.k_page;
+#pragma unroll
+          for (int b = 0; b < W::kTiles; ++b)
+            w.load_k(b, base + static_cast<uint32_t>(clamp(kTile * t + 16 * b + w.col) * static_cast<int>(a.k_pos)));
+        },
+        [&](int t) {
+          const char* base = vb + page * a.v_page;
+#pragma unroll
+          for (int j = 0; j < W::kMine; ++j)
+            w.load_v(j, base + static_cast<uint32_t>(clamp(kTile * t + w.mine(j)) * static_cast<int>(a.v_pos)));
+        },
+        [&](int t, int* lo, int* hi) {
+          *lo = start - kTile * t;
+          *hi = end - kTile * t;
+        });
     if (bad && w.lane == 0) atomicOr(a.status, kStBadPage);
-    const bool whole = pa == 0 && pb == n;
-    const int64_t slot = 2 * me + (pa == 0 ? 1 : 0);
-    merge.run(w, bad, rows, a.v_scale, static_cast<char*>(a.out) + head0 * D * 2,
-              a.lse == nullptr ? nullptr : a.lse + head0, whole ? nullptr : a.part_o + slot * group_rows * D,
-              a.part_ml + slot * group_rows);
+    const bool whole = sg.pa == 0 && sg.pb == sg.n;
+    const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (sg.pa == 0 ? 1 : 0);
+    merge.run(w, bad, a.G, a.v_scale, static_cast<char*>(a.out) + head0 * D * 2,
+              a.lse == nullptr ? nullptr : a.lse + head0, whole ? nullptr : a.part_o + slot * a.G * D,
+              a.part_ml + slot * a.G);
+  }
+}
+
+template <class T, bool E4M3, int D, int NQ>
+__global__ void __launch_bounds__(kThreads, 2) kv_decode_staged_kernel(KvAttnArgs a) {
+  typedef Ring<T, E4M3, D, NQ> R;
+  constexpr int kHeads = R::kHeads, kPer = 64 / R::kStagePos;   // stages of a page
+  __shared__ Plan<kWaves> plan;
+  __shared__ __align__(16) R ring;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int half = wave / R::kParts, part = wave % R::kParts;
+  const int64_t* prefix = plan.make(a);
+  const int qg = (a.G + kHeads - 1) / kHeads;
+  const int64_t gh = static_cast<int64_t>(a.Hkv) * qg;
+  const int64_t units = prefix[a.Q] * gh;
+  const int64_t share = unit_share(units, gridDim.x);
+  int64_t cur = blockIdx.x * share;
+  const int64_t stop = cur + share < units ? cur + share : units;
+  const int group_rows = a.G < kHeads ? a.G : kHeads;
+  typename R::W w;
+  w.init();
+  while (cur < stop) {
+    Segment s;
+    s.take(a, prefix, gh, &cur, stop);
+    const int kvh = s.g / qg, at = half * 16 * NQ, first = (s.g % qg) * kHeads + at;
+    const int rows = a.G - first < 16 * NQ ? a.G - first : 16 * NQ;   // of this half; none perhaps
+    // Two stages: every wait is for all copies anyway, and a table entry may be loaded as they are. More:
+    // it goes through the scalar cache, whose loads are counted apart.
+    const int32_t* table_at = a.table + static_cast<int64_t>(s.seq) * a.max_pages;
+    typename Pick<R::kStages == 2, const int32_t*, ScalarInts>::type table;
+    if constexpr (R::kStages == 2) table = table_at;
+    else table = scalar_ints(table_at);
+    const int p0 = (s.start >> 6) + s.pa, n = (s.pb - s.pa) * kPer;
+    const char* kb = a.k + kvh * a.k_head;
+    const char* vb = a.v + kvh * a.v_head;
+    const int64_t head0 = s.r * a.H + static_cast<int64_t>(kvh) * a.G + first;
+    w.start();
+    w.load_q(a.q + s.r * a.q_row + (static_cast<int64_t>(kvh) * a.G + first) * D * 2, rows, a.q_flip, nullptr);
+    bool bad = false;
+    int next = table[p0];   // the entry of the page to be fetched next, read early
+    int64_t page = 0;
+    ring.run(
+        w, n, part, a.c,
+        [&](int i) {
+          if (i % kPer == 0) {
+            page = next;
+            if (i + kPer < n) next = table[p0 + i / kPer + 1];
+            if (page < 0 || page >= a.P_phys) {   // nothing of it is read; page 0 stands in
+              bad = true;
+              page = 0;
+            }
+          }
+          const int at = 64 * (p0 + i / kPer);
+          ring.copy_page(a, kb + page * a.k_page, vb + page * a.v_page, i, wave, w.lane, i % kPer * R::kStagePos,
+                         s.start - at, min(s.end - at, 64));
+        },
+        [&](int i, int* lo, int* hi) {
+          const int at = 64 * (p0 + i / kPer) + i % kPer * R::kStagePos;
+          *lo = s.start - at;
+          *hi = s.end - at;
+        });
+    if (bad && threadIdx.x == 0) atomicOr(a.status, kStBadPage);
+    const bool whole = s.pa == 0 && s.pb == s.n;
+    const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (s.pa == 0 ? 1 : 0);
+    ring.finish(w, half, part, bad, rows, a.v_scale, static_cast<char*>(a.out) + head0 * D * 2,
+                a.lse == nullptr ? nullptr : a.lse + head0,
+                whole ? nullptr : a.part_o + (slot * group_rows + at) * D, a.part_ml + slot * group_rows + at);
   }
 }
 
@@ -558,11 +1097,11 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 && D < 256 ? 3 : 1) kv_decod
 
 // Writes one head's row as a constant (0 for an empty window, NaN for a failed one).
 template <class T, int D>
-__device__ __forceinline__ void fill_row(const KvAttnArgs& a, int64_t head, bool failed) {
+__device__ __forceinline__ void fill_row(const KvAttnArgs& a, int64_t head, bool failed, int tid, int threads) {
   const float x = failed ? __builtin_nanf("") : 0.0f;
   const uint32_t y = T::pack(x, x);
-  for (int i = threadIdx.x; i < D / 2; i += kThreads) reinterpret_cast<uint32_t*>(a.out)[head * (D / 2) + i] = y;
-  if (threadIdx.x == 0 && a.lse != nullptr) a.lse[head] = failed ? x : -__builtin_inff();
+  for (int i = tid; i < D / 2; i += threads) reinterpret_cast<uint32_t*>(a.out)[head * (D / 2) + i] = y;
+  if (tid == 0 && a.lse != nullptr) a.lse[head] = failed ? x : -__builtin_inff();
 }
 
 // One workgroup joins the partial sums of one (row, head): partial i < n is in
@@ -611,7 +1150,7 @@ __device__ __forceinline__ void join_row(const KvAttnArgs& a, int64_t head, int 
 }
 
 template <class T, int D>
-__global__ void __launch_bounds__(kThreads) kv_decode_join_kernel(KvAttnArgs a, int nq, int groups) {
+__global__ void __launch_bounds__(kThreads) kv_decode_join_kernel(KvAttnArgs a, int per, int groups) {
   const int64_t head = blockIdx.x;
   const int64_t r = head / a.H;
   const int h = static_cast<int>(head - r * a.H);
@@ -619,18 +1158,18 @@ __global__ void __launch_bounds__(kThreads) kv_decode_join_kernel(KvAttnArgs a, 
   if (n == 0) {
     int code;
     row_pages(a, r, &code);
-    fill_row<T, D>(a, head, code != 0);
+    fill_row<T, D>(a, head, code != 0, threadIdx.x, kThreads);
     return;
   }
-  const int qg = (a.G + 16 * nq - 1) / (16 * nq);
+  const int qg = (a.G + per - 1) / per;
   const int64_t gh = static_cast<int64_t>(a.Hkv) * qg;
   const int64_t share = unit_share(a.prefix[a.Q] * gh, groups);
   const int kvh = h / a.G, in_kv = h - kvh * a.G;
-  const int64_t from = a.prefix[r] * gh + (static_cast<int64_t>(kvh) * qg + in_kv / (16 * nq)) * n;
+  const int64_t from = a.prefix[r] * gh + (static_cast<int64_t>(kvh) * qg + in_kv / per) * n;
   const int64_t w0 = from / share, w1 = (from + n - 1) / share;
   if (w0 == w1) return;   // one workgroup had all of it and wrote the output
   // the first part is its workgroup's last one (slot 2 w + 1), the others are first ones (slot 2 w)
-  join_row<T, D>(a, head, in_kv % (16 * nq), a.G < 16 * nq ? a.G : 16 * nq, w1 - w0 + 1, 2 * w0 + 1, 2 * w0, 2);
+  join_row<T, D>(a, head, in_kv % per, a.G < per ? a.G : per, w1 - w0 + 1, 2 * w0 + 1, 2 * w0, 2);
 }
 
 // --- selected form ------------------------------------------------------------
@@ -641,118 +1180,170 @@ __device__ __forceinline__ int64_t split_share(int64_t n, int splits) {
   return (tiles + splits - 1) / splits * kTilePos;
 }
 
-template <class T, bool E4M3, int D, int NQ>
-__global__ void __launch_bounds__(kThreads, NQ == 1 && D < 256 ? 3 : 1) kv_selected_kernel(KvAttnArgs a) {
-  typedef Wave<T, E4M3, D, NQ> W;
-  __shared__ int64_t k_off[kKvSelBlock];
-  __shared__ int64_t v_off[kKvSelBlock];
-  __shared__ Merge<T, D, NQ> merge;
+// One workgroup's part of a selected launch.
+struct ListPart {
+  int64_t r, item;
+  int g, split;
+  int64_t n, from, to;   // slots [from, to) of the row's n
+
+  // False where there is nothing to attend to; a row that is empty or invalid is `fill`ed by split 0.
+  __device__ __forceinline__ bool take(const KvAttnArgs& a, int64_t gh, bool* fill) {
+    // Workgroups go to the eight dies in turn: each die gets a run of neighbouring
+    // rows, whose lists share most of their slots, so that its L2 holds them.
+    const int64_t per_die = gridDim.x / 8;
+    item = (blockIdx.x & 7) * per_die + (blockIdx.x >> 3);
+    *fill = false;
+    if (item >= a.Q * gh * a.splits) return false;
+    r = item / (gh * a.splits);
+    const int64_t rest = item - r * gh * a.splits;
+    g = static_cast<int>(rest / a.splits);
+    split = static_cast<int>(rest - static_cast<int64_t>(g) * a.splits);
+    n = a.count[r];
+    if (n > a.K && rest == 0 && threadIdx.x == 0) atomicOr(a.status, kStBadWindow);
+    if (n <= 0 || n > a.K) {
+      *fill = split == 0;
+      return false;
+    }
+    const int64_t share = split_share(n, a.splits);
+    from = split * share;
+    to = from + share < n ? from + share : n;
+    return from < to;
+  }
+};
+
+template <class T, bool E4M3, int D>
+__global__ void __launch_bounds__(kThreads, 2) kv_selected_kernel(KvAttnArgs a) {
+  constexpr int kTile = register_tile(D, E4M3);
+  typedef Wave<T, E4M3, D, 1, kTile> W;
+  __shared__ int list[kKvSelBlock];
+  __shared__ Merge<T, D> merge;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int qg = (a.G + 16 * NQ - 1) / (16 * NQ);
-  const int64_t gh = static_cast<int64_t>(a.Hkv) * qg;
-  // Workgroups go to the eight dies in turn: each die gets a run of neighbouring
-  // rows, whose lists share most of their slots, so that its L2 holds them.
-  const int64_t per_die = (gridDim.x + 7) / 8;
-  const int64_t item = (blockIdx.x & 7) * per_die + (blockIdx.x >> 3);
-  if (item >= a.Q * gh * a.splits) return;
-  const int64_t r = item / (gh * a.splits);
-  const int64_t rest = item - r * gh * a.splits;
-  const int g = static_cast<int>(rest / a.splits), split = static_cast<int>(rest - static_cast<int64_t>(g) * a.splits);
-  const int kvh = g / qg, first = (g % qg) * 16 * NQ;
-  const int rows = a.G - first < 16 * NQ ? a.G - first : 16 * NQ;
-  const int64_t head0 = r * a.H + static_cast<int64_t>(kvh) * a.G + first;
-  const int64_t n = a.count[r];
-  if (n > a.K && rest == 0 && threadIdx.x == 0) atomicOr(a.status, kStBadWindow);
-  if (n <= 0 || n > a.K) {
-    if (split == 0)
-      for (int h = 0; h < rows; ++h) fill_row<T, D>(a, head0 + h, n != 0);
+  ListPart p;
+  bool fill;
+  const bool any = p.take(a, a.Hkv, &fill);
+  if (!any && !fill) return;
+  const int64_t head0 = p.r * a.H + static_cast<int64_t>(p.g) * a.G;
+  if (!any) {
+    for (int h = 0; h < a.G; ++h) fill_row<T, D>(a, head0 + h, p.n != 0, threadIdx.x, kThreads);
     return;
   }
-  const int64_t share = split_share(n, a.splits);
-  const int64_t from = split * share;
-  const int64_t to = from + share < n ? from + share : n;
-  if (from >= to) return;
-
   W w;
   w.init();
   w.start();
-  w.load_q(a.q + r * a.q_row + (static_cast<int64_t>(kvh) * a.G + first) * D * 2, rows, a.q_flip);
-  const char* kb = a.k + kvh * a.k_head;
-  const char* vb = a.v + kvh * a.v_head;
-  const int32_t* list = a.slots + r * a.K;
+  w.load_q(a.q + p.r * a.q_row + static_cast<int64_t>(p.g) * a.G * D * 2, a.G, a.q_flip, nullptr);
+  const char* kb = a.k + p.g * a.k_head;
+  const char* vb = a.v + p.g * a.v_head;
+  // strides are multiples of 16 bytes, a page's below 2^36: their products take one 32-bit multiplication
+  const uint32_t k_page = static_cast<uint32_t>(a.k_page >> 4), v_page = static_cast<uint32_t>(a.v_page >> 4);
+  const uint32_t k_pos = static_cast<uint32_t>(a.k_pos >> 4), v_pos = static_cast<uint32_t>(a.v_pos >> 4);
+  auto offset = [](int slot, uint32_t page, uint32_t pos) {
+    const uint32_t s = static_cast<uint32_t>(slot);
+    return (static_cast<uint64_t>(s >> 6) * page + (s & 63) * pos) << 4;
+  };
   bool bad = false;
-  for (int64_t b0 = from; b0 < to; b0 += kKvSelBlock) {
-    const int len = static_cast<int>(to - b0 < kKvSelBlock ? to - b0 : kKvSelBlock);
-    if (b0 != from) __syncthreads();
+  for (int64_t b0 = p.from; b0 < p.to; b0 += kKvSelBlock) {
+    const int len = static_cast<int>(p.to - b0 < kKvSelBlock ? p.to - b0 : kKvSelBlock);
+    if (b0 != p.from) __syncthreads();
     bool mine = false;
     for (int i = threadIdx.x; i < len; i += kThreads) {
-      const int s = list[b0 + i];
-      const bool ok = s >= 0 && s < 64 * a.P_phys;
-      mine |= !ok;
-      const int page = s >> 6, pos = s & 63;
-      k_off[i] = page * a.k_page + pos * a.k_pos;
-      v_off[i] = page * a.v_page + pos * a.v_pos;
+      const int s = a.slots[p.r * a.K + b0 + i];
+      list[i] = s;
+      mine |= s < 0 || s >= 64 * a.P_phys;
     }
     if (__syncthreads_or(mine)) {   // nothing of the list is read
       bad = true;
       break;
     }
-    auto load_keys = [&](int t) {
+    run_tiles(
+        w, wave, (len + kTile - 1) / kTile, a.c,
+        [&](int t) {
 #pragma unroll
-      for (int b = 0; b < 2; ++b) w.load_k(b, kb + k_off[min(32 * t + 16 * b + w.col, len - 1)]);
-    };
-    auto load_values = [&](int t) {
+          for (int b = 0; b < W::kTiles; ++b)
+            w.load_k(b, kb + offset(list[min(kTile * t + 16 * b + w.col, len - 1)], k_page, k_pos));
+        },
+        [&](int t) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) w.load_v(j, vb + v_off[min(32 * t + 16 * (j >> 2) + 4 * w.grp + (j & 3), len - 1)]);
-    };
-    const int tiles = (len + kTilePos - 1) / kTilePos;
-    int t = wave;
-    if (t < tiles) {
-      load_keys(t);
-      load_values(t);
-      while (true) {
-        const int tn = t + kWaves;
-        const bool more = tn < tiles;
-        const bool edge = 32 * t + 32 > len;
-        uint32_t inside = 0xFFu;
-        if (edge) {
-          inside = 0;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) inside |= (32 * t + 16 * (j >> 2) + 4 * w.grp + (j & 3) < len ? 1u : 0u) << j;
-        }
-        v4f s[NQ][2];
-        v4u p[NQ];
-        w.scores(s);
-        if (more) load_keys(tn);
-        w.weights(s, a.c, edge, inside, p);
-        if (edge) w.clear_outside(inside);
-        w.add_values(p);
-        if (!more) break;
-        load_values(tn);
-        t = tn;
-      }
-    }
+          for (int j = 0; j < W::kMine; ++j) w.load_v(j, vb + offset(list[min(kTile * t + w.mine(j), len - 1)], v_page, v_pos));
+        },
+        [&](int t, int* lo, int* hi) {
+          *lo = 0;
+          *hi = len - kTile * t;
+        });
   }
   if (bad && threadIdx.x == 0) atomicOr(a.status, kStBadPage);
-  const int group_rows = a.G < 16 * NQ ? a.G : 16 * NQ;
+  merge.run(w, bad, a.G, a.v_scale, static_cast<char*>(a.out) + head0 * D * 2, a.lse == nullptr ? nullptr : a.lse + head0,
+            a.splits == 1 ? nullptr : a.part_o + p.item * a.G * D, a.part_ml + p.item * a.G);
+}
+
+template <class T, bool E4M3, int D, int NQ>
+__global__ void __launch_bounds__(kThreads, 2) kv_selected_staged_kernel(KvAttnArgs a) {
+  typedef Ring<T, E4M3, D, NQ> R;
+  constexpr int kHeads = R::kHeads;
+  __shared__ __align__(16) R ring;
+  __shared__ int list[kKvSelBlock];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int half = wave / R::kParts, part = wave % R::kParts;
+  const int qg = (a.G + kHeads - 1) / kHeads;
+  ListPart p;
+  bool fill;
+  const bool any = p.take(a, static_cast<int64_t>(a.Hkv) * qg, &fill);
+  if (!any && !fill) return;
+  const int kvh = p.g / qg, at = half * 16 * NQ, first = (p.g % qg) * kHeads + at;
+  const int rows = a.G - first < 16 * NQ ? a.G - first : 16 * NQ;   // of this half; none perhaps
+  const int64_t head0 = p.r * a.H + static_cast<int64_t>(kvh) * a.G + first;
+  if (!any) {
+    for (int h = 0; h < rows; ++h) fill_row<T, D>(a, head0 + h, p.n != 0, threadIdx.x % (64 * R::kParts), 64 * R::kParts);
+    return;
+  }
+  typename R::W w;
+  w.init();
+  w.start();
+  w.load_q(a.q + p.r * a.q_row + (static_cast<int64_t>(kvh) * a.G + first) * D * 2, rows, a.q_flip, nullptr);
+  const char* kb = a.k + kvh * a.k_head;
+  const char* vb = a.v + kvh * a.v_head;
+  bool bad = false;
+  for (int64_t b0 = p.from; b0 < p.to; b0 += kKvSelBlock) {
+    const int len = static_cast<int>(p.to - b0 < kKvSelBlock ? p.to - b0 : kKvSelBlock);
+    if (b0 != p.from) __syncthreads();
+    bool mine = false;
+    for (int i = threadIdx.x; i < len; i += kThreads) {
+      const int s = a.slots[p.r * a.K + b0 + i];
+      list[i] = s;
+      mine |= s < 0 || s >= 64 * a.P_phys;
+    }
+    if (__syncthreads_or(mine)) {   // nothing of the list is read
+      bad = true;
+      break;
+    }
+    const int n = (len + R::kStagePos - 1) / R::kStagePos;
+    const uint32_t list_at = lds_address(list);
+    ring.run(
+        w, n, part, a.c, [&](int i) { ring.copy_list(a, kb, vb, i, wave, w.lane, list_at, len); },
+        [&](int i, int* lo, int* hi) {
+          *lo = 0;
+          *hi = len - R::kStagePos * i;
+        });
+  }
+  if (bad && threadIdx.x == 0) atomicOr(a.status, kStBadPage);
+  const int group_rows = a.G < kHeads ? a.G : kHeads;
   const bool whole = a.splits == 1;
-  merge.run(w, bad, rows, a.v_scale, static_cast<char*>(a.out) + head0 * D * 2,
-            a.lse == nullptr ? nullptr : a.lse + head0, whole ? nullptr : a.part_o + item * group_rows * D,
-            a.part_ml + item * group_rows);
+  ring.finish(w, half, part, bad, rows, a.v_scale, static_cast<char*>(a.out) + head0 * D * 2,
+              a.lse == nullptr ? nullptr : a.lse + head0,
+              whole ? nullptr : a.part_o + (p.item * group_rows + at) * D, a.part_ml + p.item * group_rows + at);
 }
 
 template <class T, int D>
-__global__ void __launch_bounds__(kThreads) kv_selected_join_kernel(KvAttnArgs a, int nq) {
+__global__ void __launch_bounds__(kThreads) kv_selected_join_kernel(KvAttnArgs a, int per) {
   const int64_t head = blockIdx.x;
   const int64_t r = head / a.H;
   const int h = static_cast<int>(head - r * a.H);
   const int64_t n = a.count[r];
   if (n <= 0 || n > a.K) return;   // written already
-  const int qg = (a.G + 16 * nq - 1) / (16 * nq);
+  const int qg = (a.G + per - 1) / per;
   const int kvh = h / a.G, in_kv = h - kvh * a.G;
   const int64_t share = split_share(n, a.splits);
-  const int64_t slot = ((r * a.Hkv + kvh) * qg + in_kv / (16 * nq)) * a.splits;
-  join_row<T, D>(a, head, in_kv % (16 * nq), a.G < 16 * nq ? a.G : 16 * nq, (n + share - 1) / share, slot, slot, 1);
+  const int64_t slot = ((r * a.Hkv + kvh) * qg + in_kv / per) * a.splits;
+  join_row<T, D>(a, head, in_kv % per, a.G < per ? a.G : per, (n + share - 1) / share, slot, slot, 1);
 }
 
 // --- accumulated weights ------------------------------------------------------
@@ -775,10 +1366,11 @@ __device__ __forceinline__ float row_sum(float x) {
 template <class T, bool E4M3, int D, int NQ>
 __global__ void __launch_bounds__(kThreads, NQ == 1 && D < 256 ? 4 : 2)
     kv_weights_kernel(KvAttnArgs a, const float* __restrict__ lse, float* __restrict__ acc, int64_t acc_stride) {
-  typedef Wave<T, E4M3, D, NQ> W;
+  typedef Wave<T, E4M3, D, NQ, 32, (NQ > 1)> W;
   __shared__ int seq_lo[kWeightSeqs], seq_hi[kWeightSeqs];
   __shared__ int64_t prefix[kWeightSeqs + 1];
   __shared__ int64_t sums[kWaves];
+  __shared__ v4u q_lds[W::kShared ? NQ * W::kChunks * 64 : 1];
   __shared__ float part[kWeightTiles * kTilePos];
   __shared__ int covered[kWeightTiles * kTilePos];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -865,7 +1457,9 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 && D < 256 ? 4 : 2)
             const int kvh = g / qg, first = (g % qg) * 16 * NQ;
             const int rows = a.G - first < 16 * NQ ? a.G - first : 16 * NQ;
             const int64_t head0 = r * a.H + static_cast<int64_t>(kvh) * a.G + first;
-            w.load_q(a.q + r * a.q_row + (static_cast<int64_t>(kvh) * a.G + first) * D * 2, rows, 0u);
+            if (W::kShared) __syncthreads();
+            w.load_q(a.q + r * a.q_row + (static_cast<int64_t>(kvh) * a.G + first) * D * 2, rows, 0u, q_lds);
+            if (W::kShared) __syncthreads();
             float sub[NQ];
             bool counts[NQ];
 #pragma unroll
@@ -925,21 +1519,23 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 && D < 256 ? 4 : 2)
 
 // --- dispatch -----------------------------------------------------------------
 
-template <class T, bool E4M3, int D, int NQ>
+template <class T, bool E4M3, int D, int TILES>
 void decode_on(const KvAttnArgs& a, hipStream_t st) {
-  const int groups = kv_decode_groups(D, a.G);
+  const int groups = kKvDecodeGroups;
   if (a.Q > kKvPlanRows) kv_plan_kernel<<<dim3(1), dim3(1024), 0, st>>>(a);
-  kv_decode_kernel<T, E4M3, D, NQ><<<dim3(groups), dim3(kThreads), 0, st>>>(a);
-  kv_decode_join_kernel<T, D><<<dim3(static_cast<unsigned>(a.Q * a.H)), dim3(kThreads), 0, st>>>(a, NQ, groups);
+  if constexpr (TILES == 1) kv_decode_kernel<T, E4M3, D><<<dim3(groups), dim3(kThreads), 0, st>>>(a);
+  else kv_decode_staged_kernel<T, E4M3, D, TILES / 2><<<dim3(groups), dim3(kThreads), 0, st>>>(a);
+  kv_decode_join_kernel<T, D><<<dim3(static_cast<unsigned>(a.Q * a.H)), dim3(kThreads), 0, st>>>(a, 16 * TILES, groups);
 }
 
-template <class T, bool E4M3, int D, int NQ>
+template <class T, bool E4M3, int D, int TILES>
 void selected_on(const KvAttnArgs& a, hipStream_t st) {
-  const int64_t items = a.Q * a.Hkv * kv_q_groups(D, a.G) * a.splits;
+  const int64_t items = a.Q * a.Hkv * kv_head_groups(D, a.G) * a.splits;
   const unsigned grid = static_cast<unsigned>((items + 7) / 8 * 8);
-  kv_selected_kernel<T, E4M3, D, NQ><<<dim3(grid), dim3(kThreads), 0, st>>>(a);
+  if constexpr (TILES == 1) kv_selected_kernel<T, E4M3, D><<<dim3(grid), dim3(kThreads), 0, st>>>(a);
+  else kv_selected_staged_kernel<T, E4M3, D, TILES / 2><<<dim3(grid), dim3(kThreads), 0, st>>>(a);
   if (a.splits > 1)
-    kv_selected_join_kernel<T, D><<<dim3(static_cast<unsigned>(a.Q * a.H)), dim3(kThreads), 0, st>>>(a, NQ);
+    kv_selected_join_kernel<T, D><<<dim3(static_cast<unsigned>(a.Q * a.H)), dim3(kThreads), 0, st>>>(a, 16 * TILES);
 }
 
 template <class T, bool E4M3, int D, int NQ>
@@ -949,13 +1545,14 @@ void weights_on(const KvAttnArgs& a, const float* lse, float* acc, int64_t acc_s
 
 // Calls f<type, 8-bit cache, dim, query tiles>() for the call's types and sizes.
 template <class T, bool E4M3, class F>
-void by_size(const KvAttnArgs& a, F&& f) {
-  const int nq = kv_q_tiles(a.D, a.G);
+void by_size(const KvAttnArgs& a, int nq, F&& f) {
   if (a.D == 64) {
     if (nq == 1) f.template operator()<T, E4M3, 64, 1>();
+    else if (nq == 2) f.template operator()<T, E4M3, 64, 2>();
     else f.template operator()<T, E4M3, 64, 4>();
   } else if (a.D == 128) {
     if (nq == 1) f.template operator()<T, E4M3, 128, 1>();
+    else if (nq == 2) f.template operator()<T, E4M3, 128, 2>();
     else f.template operator()<T, E4M3, 128, 4>();
   } else {
     if (nq == 1) f.template operator()<T, E4M3, 256, 1>();
@@ -964,14 +1561,14 @@ void by_size(const KvAttnArgs& a, F&& f) {
 }
 
 template <class F>
-hipError_t by_type(const KvAttnArgs& a, F&& f) {
+hipError_t by_type(const KvAttnArgs& a, int nq, F&& f) {
   const bool e4m3 = a.kv_type == MQA_KV_E4M3;
   if (a.q_type == MQA_KV_BF16) {
-    if (e4m3) by_size<Bf16, true>(a, f);
-    else by_size<Bf16, false>(a, f);
+    if (e4m3) by_size<Bf16, true>(a, nq, f);
+    else by_size<Bf16, false>(a, nq, f);
   } else {
-    if (e4m3) by_size<Fp16, true>(a, f);
-    else by_size<Fp16, false>(a, f);
+    if (e4m3) by_size<Fp16, true>(a, nq, f);
+    else by_size<Fp16, false>(a, nq, f);
   }
   return hipGetLastError();
 }
@@ -1003,18 +1600,22 @@ struct WeightsOn {
 // Splits of the selected form: one workgroup per (row, head group) once they
 // fill the device, else enough splits of at least four tiles each.
 int32_t kv_selected_splits(int64_t Q, int64_t K, int D, int G, int Hkv) {
-  const int64_t items = Q * Hkv * kv_q_groups(D, G);
-  const int64_t room = kv_decode_groups(D, G);
+  const int64_t items = Q * Hkv * kv_head_groups(D, G);
+  const int64_t room = kKvDecodeGroups;
   int64_t s = items <= 0 ? 1 : room / items;
   const int64_t most = (K + 4 * kTilePos - 1) / (4 * kTilePos);
   if (s > most) s = most;
   return static_cast<int32_t>(s < 1 ? 1 : s);
 }
 
-hipError_t launch_kv_decode(const KvAttnArgs& a, hipStream_t st) { return by_type(a, DecodeOn{a, st}); }
-hipError_t launch_kv_selected(const KvAttnArgs& a, hipStream_t st) { return by_type(a, SelectedOn{a, st}); }
+hipError_t launch_kv_decode(const KvAttnArgs& a, hipStream_t st) {
+  return by_type(a, kv_tiles(a.D, a.G), DecodeOn{a, st});
+}
+hipError_t launch_kv_selected(const KvAttnArgs& a, hipStream_t st) {
+  return by_type(a, kv_tiles(a.D, a.G), SelectedOn{a, st});
+}
 hipError_t launch_kv_weights(const KvAttnArgs& a, const float* lse, float* acc, int64_t acc_stride, hipStream_t st) {
-  return by_type(a, WeightsOn{a, lse, acc, acc_stride, st});
+  return by_type(a, kv_tiles(a.D, a.G), WeightsOn{a, lse, acc, acc_stride, st});
 }
 
 }  // namespace mqa

@@ -16,6 +16,35 @@ p = P(0x1000)
 NULL, MISALIGNED, SIZE, UNSUPPORTED = -2, -3, -4, -9
 
 
+class Cache(ctypes.Structure):
+    _fields_ = [("k", P), ("v", P), ("k_stride", ctypes.c_int64 * 3), ("v_stride", ctypes.c_int64 * 3),
+                ("num_phys_pages", ctypes.c_int64), ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("type", ctypes.c_int32), ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float)]
+
+
+class Query(ctypes.Structure):
+    _fields_ = [("q", P), ("row_stride", ctypes.c_int64), ("num_rows", ctypes.c_int64), ("num_heads", ctypes.c_int32),
+                ("type", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class Array(ctypes.Structure):
+    _fields_ = [("src", P), ("dst", P), ("src_stride", ctypes.c_int64 * 3), ("dst_stride", ctypes.c_int64 * 3),
+                ("row_bytes", ctypes.c_int64), ("rows_per_position", ctypes.c_int64)]
+
+
+def test_packed_structures_have_the_header_s_layout():
+    for packed, plain in ((mqa._KV_CACHE, Cache), (mqa._KV_QUERY, Query), (mqa._KV_ARRAY, Array)):
+        assert packed.size == ctypes.sizeof(plain)
+    c = Cache.from_buffer_copy(mqa._KV_CACHE.pack(1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 11, 12, 0.5, 0.25))
+    assert (c.k, c.v, list(c.k_stride), list(c.v_stride), c.num_phys_pages, c.num_kv_heads, c.head_dim, c.type, c.k_scale,
+            c.v_scale) == (1, 2, [3, 4, 5], [6, 7, 8], 9, 10, 11, 12, 0.5, 0.25)
+    q = Query.from_buffer_copy(mqa._KV_QUERY.pack(1, 2, 3, 4, 5, 0.5))
+    assert (q.q, q.row_stride, q.num_rows, q.num_heads, q.type, q.scale) == (1, 2, 3, 4, 5, 0.5)
+    a = Array.from_buffer_copy(mqa._KV_ARRAY.pack(*range(1, 11)))
+    assert (a.src, a.dst, list(a.src_stride), list(a.dst_stride), a.row_bytes, a.rows_per_position) == (
+        1, 2, [3, 4, 5], [6, 7, 8], 9, 10)
+
+
 @pytest.fixture(scope="module")
 def lib():
     if not os.path.exists(mqa.LIB_PATH):
@@ -38,14 +67,14 @@ def test_library_exports_every_declared_symbol(lib):
 def query(**over):
     a = dict(q=0x1000, row_stride=8 * 128, num_rows=4, num_heads=8, type=0, scale=0.1)
     a.update(over)
-    return mqa._KvQuery(**a)
+    return Query(**a)
 
 
 def cache(**over):
     k_stride, v_stride = over.pop("k_stride", (64 * 256, 256, 128)), over.pop("v_stride", (64 * 256, 256, 128))
     a = dict(k=0x1000, v=0x1000, num_phys_pages=10, num_kv_heads=2, head_dim=128, type=0, k_scale=1.0, v_scale=1.0)
     a.update(over)
-    c = mqa._KvCache(**a)
+    c = Cache(**a)
     c.k_stride[:] = k_stride
     c.v_stride[:] = v_stride
     return c
@@ -138,7 +167,7 @@ def test_eviction_is_checked_on_the_host(lib):
         a = dict(src=0x1000, dst=0x1000, row_bytes=64, rows_per_position=2)
         strides = over.pop("stride", (64 * 128, 128, 64))
         a.update(over)
-        x = mqa._KvArray(**a)
+        x = Array(**a)
         x.src_stride[:] = strides
         x.dst_stride[:] = (64 * 128, 128, 64)
         return lib.mqa_kv_compact(keep, p, n, budget, p, sp, P_src, dst_table, dp, P_dst, ctypes.byref(x) if count else None,
@@ -171,7 +200,7 @@ def good():
     (ValueError, dict(k_pages=torch.zeros(3, 64, 128, 2, dtype=torch.bfloat16).transpose(2, 3))),
     (TypeError, dict(block_table=torch.zeros(2, 3))), (ValueError, dict(row_end=torch.zeros(3, dtype=torch.int32))),
     (TypeError, dict(out=torch.zeros(4, 8, 128, dtype=torch.float16))), (ValueError, dict(out=torch.zeros(4, 8, 64, dtype=torch.bfloat16))),
-    (ValueError, dict(out=None)), (ValueError, dict(lse=torch.zeros(8, 4))), (TypeError, dict(lse=torch.zeros(4, 8).double())),
+    (TypeError, dict(out=None)), (ValueError, dict(lse=torch.zeros(8, 4))), (TypeError, dict(lse=torch.zeros(4, 8).double())),
     (TypeError, dict(workspace=torch.zeros(8))),
 ])
 def test_binding_rejects_malformed_attention_tensors(exc, over):
@@ -194,7 +223,7 @@ def test_binding_rejects_malformed_lists_sums_and_arrays():
                      (ValueError, torch.zeros(192, 2).t()), (ValueError, torch.zeros(192).expand(2, 192))):
         with pytest.raises(exc):
             w(acc)
-    with pytest.raises(ValueError):
+    with pytest.raises(TypeError):
         w(torch.zeros(2, 192), lse=None)
     with pytest.raises(ValueError):
         mqa.mqa_kv_evict_select(torch.zeros(2, 9), i(2), 5, 1, i(2, 4), i(2))
