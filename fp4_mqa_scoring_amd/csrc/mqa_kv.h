@@ -49,7 +49,6 @@ constexpr int kv_group_rows(int D, int G) { return G < 16 * kv_tiles(D, G) ? G :
 
 // Workgroups of the decode form: what 256 compute units hold at once.
 constexpr int kKvDecodeGroups = 512;
-constexpr int kKvWeightGroups = 1024; // workgroups of the accumulated weights
 constexpr int kKvPlanRows = 1024;     // rows up to which every workgroup plans for itself
 constexpr int kKvSelBlock = 1024;     // slots staged at once by the selected form
 
@@ -70,7 +69,16 @@ struct KvEvictArgs {
   int32_t* kept;
   float* kept_acc;
   int32_t* status;
+  // workspace of long sequences
+  uint32_t* counts;   // [n_seq, chunks, 3, 2048] counts of each chunk's digits
+  uint32_t* state;    // [n_seq, 4]
 };
+// Sequences of up to 16,384 positions (the capacity's bound, as the host knows no lengths) take one
+// workgroup; longer ones one per chunk.
+constexpr int kKvEvictChunk = 8192;
+constexpr int64_t kv_evict_chunks(int64_t max_len) {
+  return max_len <= 16384 ? 1 : (max_len + kKvEvictChunk - 1) / kKvEvictChunk;
+}
 hipError_t launch_kv_evict_select(const KvEvictArgs& a, hipStream_t st);
 
 constexpr int kKvMaxArrays = 8;

@@ -237,8 +237,11 @@ int32_t mqa_kv_weights_accumulate(const mqa_kv_query* q, const float* lse, const
 }
 
 int64_t mqa_kv_evict_workspace_bytes(int64_t num_seqs, int64_t max_len) {
-  if (num_seqs < 0 || num_seqs > kMaxItems || max_len < 0 || max_len > 0x7FFFFFFFll - 512) return MQA_ERR_BAD_SIZE;
-  return 0;
+  // workgroups of 1,024 threads, counted in 32 bits
+  if (num_seqs < 0 || max_len < 0 || max_len > 0x7FFFFFFFll - 512) return MQA_ERR_BAD_SIZE;
+  const int64_t chunks = mqa::kv_evict_chunks(max_len);
+  if (num_seqs > kMaxItems / 4 / chunks) return MQA_ERR_BAD_SIZE;
+  return chunks == 1 ? 0 : align_up(num_seqs * 4 * 4) + align_up(num_seqs * chunks * 3 * 2048 * 4);
 }
 
 int32_t mqa_kv_evict_select(const float* acc, int64_t acc_stride, const int32_t* seq_len, int64_t num_seqs,
@@ -260,8 +263,10 @@ int32_t mqa_kv_evict_select(const float* acc, int64_t acc_stride, const int32_t*
   int32_t rc = enter(st, specs, sizeof(specs) / sizeof(specs[0]), guard, &info, /*allow_capture=*/true);
   if (rc != MQA_OK || !rows) return rc;
   mqa::KvEvictArgs a{acc, acc_stride, seq_len, num_seqs, max_len, budget, recent, keep, kept, kept_acc,
-                     mqa::status_word()};
+                     mqa::status_word(), nullptr, nullptr};
   if (a.status == nullptr) return MQA_ERR_HIP;
+  a.state = static_cast<uint32_t*>(workspace);
+  a.counts = reinterpret_cast<uint32_t*>(static_cast<char*>(workspace) + align_up(num_seqs * 4 * 4));
   return hip_rc(mqa::launch_kv_evict_select(a, st));
 }
 

@@ -176,11 +176,8 @@ struct Wave {
   __device__ __forceinline__ void load_q(const char* p, int rows, uint32_t flip, v4u* lds) {
     if constexpr (kShared) {
       q_lds = lds + lane;
-#pragma unroll
-      for (int i = 0; i < NQ * kChunks; i += kWaves) {
-        const int x = i + (threadIdx.x >> 6);
+      for (int x = threadIdx.x >> 6; x < NQ * kChunks; x += blockDim.x >> 6)
         lds[64 * x + lane] = query(p, x / kChunks, x % kChunks, rows, flip);
-      }
     } else {
 #pragma unroll
       for (int n = 0; n < NQ; ++n)
@@ -1363,17 +1360,26 @@ __device__ __forceinline__ float row_sum(float x) {
 // acc[seq, p] += sum over rows and heads of exp(s_p - lse). The unit of work is one
 // page of one sequence with all of its rows and heads, so that a position's sum
 // has one owner and one order. Bound by the keys' bytes.
+//
+// Up to 16 heads per key head: eight waves, of which `hg` (a power of two) take the key
+// heads in turn and 8 / hg the tiles of 32 positions; each of the former sums for itself in LDS and
+// the sums are added in order at the end. More heads: four waves take tiles, the queries lie in LDS.
+// The next tile's keys are loaded into the registers that the product has just read.
+constexpr int weight_waves(int nq) { return nq == 1 ? 8 : 4; }
+
 template <class T, bool E4M3, int D, int NQ>
-__global__ void __launch_bounds__(kThreads, NQ == 1 && D < 256 ? 4 : 2)
-    kv_weights_kernel(KvAttnArgs a, const float* __restrict__ lse, float* __restrict__ acc, int64_t acc_stride) {
+__global__ void __launch_bounds__(64 * weight_waves(NQ), D == 256 ? 2 : NQ == 1 ? 4 : 3)
+    kv_weights_kernel(KvAttnArgs a, const float* __restrict__ lse, float* __restrict__ acc, int64_t acc_stride, int hg) {
   typedef Wave<T, E4M3, D, NQ, 32, (NQ > 1)> W;
+  constexpr int kBlock = kWeightTiles * kTilePos, kWeightWaves = weight_waves(NQ), kWeightThreads = 64 * kWeightWaves;
   __shared__ int seq_lo[kWeightSeqs], seq_hi[kWeightSeqs];
   __shared__ int64_t prefix[kWeightSeqs + 1];
-  __shared__ int64_t sums[kWaves];
+  __shared__ int64_t sums[kWeightWaves];
   __shared__ v4u q_lds[W::kShared ? NQ * W::kChunks * 64 : 1];
-  __shared__ float part[kWeightTiles * kTilePos];
-  __shared__ int covered[kWeightTiles * kTilePos];
+  __shared__ float part[(NQ > 1 ? 1 : kWeightWaves) * kBlock];
+  __shared__ int covered[kBlock];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int head_at = wave % hg, tile_at = wave / hg, tile_step = kWeightWaves / hg;
   const int64_t me = blockIdx.x;
   const int qg = (a.G + 16 * NQ - 1) / (16 * NQ);
   W w;
@@ -1381,12 +1387,12 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 && D < 256 ? 4 : 2)
   for (int64_t s0 = 0; s0 < a.n_seq; s0 += kWeightSeqs) {
     // the positions that any row of each sequence looks at
     __syncthreads();
-    for (int i = threadIdx.x; i < kWeightSeqs; i += kThreads) {
+    for (int i = threadIdx.x; i < kWeightSeqs; i += kWeightThreads) {
       seq_lo[i] = 0x7FFFFFFF;
       seq_hi[i] = 0;
     }
     __syncthreads();
-    for (int64_t r = threadIdx.x; r < a.Q; r += kThreads) {
+    for (int64_t r = threadIdx.x; r < a.Q; r += kWeightThreads) {
       int code = 0;
       const int n = row_pages(a, r, &code);
       if (me == 0 && s0 == 0) report(a, code);
@@ -1397,7 +1403,7 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 && D < 256 ? 4 : 2)
       }
     }
     __syncthreads();
-    constexpr int kPer = kWeightSeqs / kThreads;
+    constexpr int kPer = kWeightSeqs / kWeightThreads;
     int64_t n[kPer], sum = 0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
@@ -1406,7 +1412,7 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 && D < 256 ? 4 : 2)
       sum += n[i];
     }
     int64_t units;
-    int64_t at = block_scan<kWaves>(sum, sums, &units) - sum;
+    int64_t at = block_scan<kWeightWaves>(sum, sums, &units) - sum;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       prefix[kPer * threadIdx.x + i] = at;
@@ -1415,7 +1421,7 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 && D < 256 ? 4 : 2)
     if (threadIdx.x == 0) prefix[kWeightSeqs] = units;
     __syncthreads();
 
-    const int64_t share = unit_share(units, gridDim.x);
+    const int64_t share = (units + gridDim.x - 1) / gridDim.x;
     int64_t cur = me * share;
     const int64_t stop = cur + share < units ? cur + share : units;
     while (cur < stop) {
@@ -1435,11 +1441,9 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 && D < 256 ? 4 : 2)
       cur += pn;
       const int t_lo = 2 * ((seq_lo[si] >> 6) + pa), t_hi = t_lo + 2 * static_cast<int>(pn);
       const int32_t* table = a.table + seq * a.max_pages;
-      __syncthreads();
-      for (int i = threadIdx.x; i < kWeightTiles * kTilePos; i += kThreads) {
-        part[i] = 0.0f;
-        covered[i] = 0;
-      }
+      __syncthreads();   // the sums of the run before are written
+      for (int i = threadIdx.x; i < hg * kBlock; i += kWeightThreads) part[i] = 0.0f;
+      for (int i = threadIdx.x; i < kBlock; i += kWeightThreads) covered[i] = 0;
       __syncthreads();
       for (int64_t r0 = 0; r0 < a.Q; r0 += 64) {
         const int64_t rl = r0 + w.lane;
@@ -1448,18 +1452,35 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 && D < 256 ? 4 : 2)
           int code;
           mine = row_pages(a, rl, &code) > 0 && a.row_start[rl] < 32 * t_hi && a.row_end[rl] > 32 * t_lo;
         }
-        uint64_t todo = __ballot(mine);
+        uint64_t todo = __ballot(mine);   // the same in every wave
         while (todo) {
           const int64_t r = r0 + __builtin_ctzll(todo);
           todo &= todo - 1;
           const int start = a.row_start[r], end = a.row_end[r];
-          for (int g = 0; g < a.Hkv * qg; ++g) {
+          // this wave's tiles of the row's window
+          const int first_t = max(t_lo, start >> 5), last_t = min(t_hi, (end + 31) >> 5);
+          const int from = first_t + (tile_at - (first_t - t_lo) % tile_step + tile_step) % tile_step;
+          for (int g = head_at; g < a.Hkv * qg; g += hg) {
             const int kvh = g / qg, first = (g % qg) * 16 * NQ;
             const int rows = a.G - first < 16 * NQ ? a.G - first : 16 * NQ;
             const int64_t head0 = r * a.H + static_cast<int64_t>(kvh) * a.G + first;
+            const char* kb = a.k + kvh * a.k_head;
+            bool good = false, next_good = false;
+            // positions outside the window are not read: their lanes read the nearest one inside
+            auto load_keys = [&](int t) {
+              int64_t page = table[t >> 1];
+              next_good = page >= 0 && page < a.P_phys;
+              if (!next_good) page = 0;
+              const char* base = kb + page * a.k_page;
+#pragma unroll
+              for (int b = 0; b < 2; ++b) {
+                const int pos = min(max(32 * t + 16 * b + w.col, start), end - 1) & 63;
+                w.load_k(b, base + static_cast<uint32_t>(pos * static_cast<int>(a.k_pos)));
+              }
+            };
+            if (from < last_t) load_keys(from);
             if (W::kShared) __syncthreads();
             w.load_q(a.q + r * a.q_row + (static_cast<int64_t>(kvh) * a.G + first) * D * 2, rows, 0u, q_lds);
-            if (W::kShared) __syncthreads();
             float sub[NQ];
             bool counts[NQ];
 #pragma unroll
@@ -1468,21 +1489,12 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 && D < 256 ? 4 : 2)
               sub[n] = h < rows ? lse[head0 + h] : __builtin_inff();
               counts[n] = __builtin_fabsf(sub[n]) < __builtin_inff();
             }
-            for (int t = t_lo + wave; t < t_hi; t += kWaves) {
-              if (32 * t + 32 <= start || 32 * t >= end) continue;
-              const int page = table[t >> 1];
-              if (page < 0 || page >= a.P_phys) {
-                if (w.lane == 0) atomicOr(a.status, kStBadPage);
-                continue;
-              }
-              const char* base = a.k + kvh * a.k_head + page * a.k_page;
-#pragma unroll
-              for (int b = 0; b < 2; ++b) {
-                const int pos = min(max(32 * t + 16 * b + w.col, start), end - 1) & 63;
-                w.load_k(b, base + static_cast<uint32_t>(pos * static_cast<int>(a.k_pos)));
-              }
+            if (W::kShared) __syncthreads();
+            for (int t = from; t < last_t; t += tile_step) {
               v4f s[NQ][2];
               w.scores(s);
+              good = next_good;
+              if (t + tile_step < last_t) load_keys(t + tile_step);
               float x[8] = {};
 #pragma unroll
               for (int n = 0; n < NQ; ++n)
@@ -1499,10 +1511,12 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 && D < 256 ? 4 : 2)
                 const float z = row_sum(x[j]);
                 y = w.col == j ? z : y;
               }
-              if (w.col < 8) {
-                const int pos = 32 * t + 16 * (w.col >> 2) + 4 * w.grp + (w.col & 3);
+              if (!good) {
+                if (w.lane == 0) atomicOr(a.status, kStBadPage);
+              } else if (w.col < 8) {
+                const int pos = 32 * t + w.mine(w.col);
                 if (pos >= start && pos < end) {
-                  part[pos - 32 * t_lo] += y;
+                  part[head_at * kBlock + pos - 32 * t_lo] += y;
                   covered[pos - 32 * t_lo] = 1;
                 }
               }
@@ -1511,8 +1525,12 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 && D < 256 ? 4 : 2)
         }
       }
       __syncthreads();
-      for (int i = threadIdx.x; i < 32 * (t_hi - t_lo); i += kThreads)
-        if (covered[i]) acc[seq * acc_stride + 32 * t_lo + i] += part[i];
+      for (int i = threadIdx.x; i < 32 * (t_hi - t_lo); i += kWeightThreads)
+        if (covered[i]) {
+          float total = part[i];
+          for (int h = 1; h < hg; ++h) total += part[h * kBlock + i];
+          acc[seq * acc_stride + 32 * t_lo + i] += total;
+        }
     }
   }
 }
@@ -1540,7 +1558,11 @@ void selected_on(const KvAttnArgs& a, hipStream_t st) {
 
 template <class T, bool E4M3, int D, int NQ>
 void weights_on(const KvAttnArgs& a, const float* lse, float* acc, int64_t acc_stride, hipStream_t st) {
-  kv_weights_kernel<T, E4M3, D, NQ><<<dim3(kKvWeightGroups), dim3(kThreads), 0, st>>>(a, lse, acc, acc_stride);
+  // as many workgroups as 256 compute units hold: two of eight waves, three of four
+  int hg = 1;   // key heads at once
+  if (NQ == 1)
+    while (hg < weight_waves(NQ) && 2 * hg <= a.Hkv) hg *= 2;
+  kv_weights_kernel<T, E4M3, D, NQ><<<dim3(NQ == 1 ? 512 : 768), dim3(64 * weight_waves(NQ)), 0, st>>>(a, lse, acc, acc_stride, hg);
 }
 
 // Calls f<type, 8-bit cache, dim, query tiles>() for the call's types and sizes.
