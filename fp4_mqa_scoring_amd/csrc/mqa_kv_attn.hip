@@ -1101,72 +1101,116 @@ __device__ __forceinline__ void fill_row(const KvAttnArgs& a, int64_t head, bool
   if (tid == 0 && a.lse != nullptr) a.lse[head] = failed ? x : -__builtin_inff();
 }
 
-// One workgroup joins the partial sums of one (row, head): partial i < n is in
-// slot slot0 + i * step (the first one in slot first_slot).
-template <class T, int D>
+// Joins the partial sums of one (row, head): partial i < n is in slot slot0 + i * step
+// (the first one in slot first_slot). WAVES waves (of the whole workgroup: 4) take the partials in turn, eight at
+// a time, as the positions were taken before: with a running maximum, so that sums and maxima
+// are loaded together.
+template <class T, int D, int WAVES>
 __device__ __forceinline__ void join_row(const KvAttnArgs& a, int64_t head, int in_group, int group_rows, int64_t n,
                                          int64_t first_slot, int64_t slot0, int64_t step) {
-  __shared__ float tops[kWaves];
-  __shared__ float sums[kWaves];
-  __shared__ float acc_lds[kWaves][D];
-  constexpr int kPer = D / 64;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  auto slot_of = [&](int64_t i) { return i == 0 ? first_slot : slot0 + i * step; };
-  float top = -__builtin_inff();
-  for (int64_t i = threadIdx.x; i < n; i += kThreads)
-    top = fmaxf(top, a.part_ml[slot_of(i) * group_rows + in_group].x);
-  for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
-  if (lane == 0) tops[wave] = top;
-  __syncthreads();
-  top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-  const float ref = top == -__builtin_inff() ? 0.0f : top;
-  float acc[kPer] = {}, sum = 0.0f;
-#pragma unroll 8
-  for (int64_t i = wave; i < n; i += kWaves) {
-    const int64_t s = slot_of(i) * group_rows + in_group;
-    const float2 ml = a.part_ml[s];
-    const float f = __builtin_amdgcn_exp2f(ml.x - ref);
-    sum += ml.y * f;
+  constexpr int kPer = D / 64, kBatch = 8;
+  const int lane = threadIdx.x & 63, wave = WAVES == 1 ? 0 : threadIdx.x >> 6;
+  float m = -__builtin_inff(), sum = 0.0f, acc[kPer] = {};
+  for (int64_t i0 = wave; i0 < n; i0 += kBatch * WAVES) {
+    float2 ml[kBatch];
+    float o[kBatch][kPer];
+    float top = m;
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) acc[e] += f * a.part_o[s * D + lane + 64 * e];
+    for (int x = 0; x < kBatch; ++x) {
+      const int64_t i = i0 + x * WAVES;
+      ml[x] = make_float2(-__builtin_inff(), 0.0f);
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) o[x][e] = 0.0f;
+      if (i < n) {
+        const int64_t s = (i == 0 ? first_slot : slot0 + i * step) * group_rows + in_group;
+        ml[x] = a.part_ml[s];
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) o[x][e] = a.part_o[s * D + kPer * lane + e];
+      }
+    }
+#pragma unroll
+    for (int x = 0; x < kBatch; ++x) top = fmaxf(top, ml[x].x);
+    const float ref = top == -__builtin_inff() ? 0.0f : top;
+    const float by = __builtin_amdgcn_exp2f(m - ref);
+    m = top;
+    sum *= by;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) acc[e] *= by;
+#pragma unroll
+    for (int x = 0; x < kBatch; ++x) {
+      const float f = __builtin_amdgcn_exp2f(ml[x].x - ref);
+      sum += ml[x].y * f;
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) acc[e] += o[x][e] * f;
+    }
   }
-  if (lane == 0) sums[wave] = sum;
+  if constexpr (WAVES > 1) {
+    __shared__ float2 ml_lds[WAVES];
+    __shared__ float acc_lds[WAVES][D];
+    if (lane == 0) ml_lds[wave] = make_float2(m, sum);
 #pragma unroll
-  for (int e = 0; e < kPer; ++e) acc_lds[wave][lane + 64 * e] = acc[e];
-  __syncthreads();
-  sum = (sums[0] + sums[1]) + (sums[2] + sums[3]);
+    for (int e = 0; e < kPer; ++e) acc_lds[wave][kPer * lane + e] = acc[e];
+    __syncthreads();
+    if (wave > 0) return;
+    float top = m;
+#pragma unroll
+    for (int i = 1; i < WAVES; ++i) top = fmaxf(top, ml_lds[i].x);
+    const float ref = top == -__builtin_inff() ? 0.0f : top;
+    const float by = __builtin_amdgcn_exp2f(m - ref);
+    m = top;
+    sum *= by;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) acc[e] *= by;
+#pragma unroll
+    for (int i = 1; i < WAVES; ++i) {
+      const float f = __builtin_amdgcn_exp2f(ml_lds[i].x - ref);
+      sum += ml_lds[i].y * f;
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) acc[e] += acc_lds[i][kPer * lane + e] * f;
+    }
+  }
   const float inv = a.v_scale / sum;
-  for (int i = threadIdx.x; i < D / 2; i += kThreads) {
-    float x[2];
+  uint16_t* out = static_cast<uint16_t*>(a.out) + head * D + kPer * lane;
+  if constexpr (kPer == 1) {
+    *out = static_cast<uint16_t>(T::pack(acc[0] * inv, 0.0f));
+  } else {
 #pragma unroll
-    for (int e = 0; e < 2; ++e)
-      x[e] = ((acc_lds[0][2 * i + e] + acc_lds[1][2 * i + e]) + (acc_lds[2][2 * i + e] + acc_lds[3][2 * i + e])) * inv;
-    reinterpret_cast<uint32_t*>(a.out)[head * (D / 2) + i] = T::pack(x[0], x[1]);
+    for (int e = 0; e < kPer; e += 2)
+      *reinterpret_cast<uint32_t*>(out + e) = T::pack(acc[e] * inv, acc[e + 1] * inv);
   }
-  if (threadIdx.x == 0 && a.lse != nullptr) a.lse[head] = (top + __builtin_amdgcn_logf(sum)) * kLn2;
+  if (lane == 0 && a.lse != nullptr) a.lse[head] = (m + __builtin_amdgcn_logf(sum)) * kLn2;
 }
 
-template <class T, int D>
+// Head of a join launch: one per workgroup, or (WAVES 1) one per wave; -1 behind the last.
+template <int WAVES>
+__device__ __forceinline__ int64_t join_head(const KvAttnArgs& a) {
+  if (WAVES > 1) return blockIdx.x;
+  const int64_t head = static_cast<int64_t>(blockIdx.x) * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  return head < a.Q * a.H ? head : -1;
+}
+
+template <class T, int D, int WAVES>
 __global__ void __launch_bounds__(kThreads) kv_decode_join_kernel(KvAttnArgs a, int per, int groups) {
-  const int64_t head = blockIdx.x;
+  const int64_t head = join_head<WAVES>(a);
+  if (head < 0) return;
   const int64_t r = head / a.H;
   const int h = static_cast<int>(head - r * a.H);
-  const int64_t n = a.prefix[r + 1] - a.prefix[r];
+  const int64_t before = a.prefix[r], n = a.prefix[r + 1] - before, all = a.prefix[a.Q];
   if (n == 0) {
     int code;
     row_pages(a, r, &code);
-    fill_row<T, D>(a, head, code != 0, threadIdx.x, kThreads);
+    fill_row<T, D>(a, head, code != 0, WAVES > 1 ? threadIdx.x : threadIdx.x & 63, 64 * WAVES);
     return;
   }
   const int qg = (a.G + per - 1) / per;
   const int64_t gh = static_cast<int64_t>(a.Hkv) * qg;
-  const int64_t share = unit_share(a.prefix[a.Q] * gh, groups);
+  const int64_t share = unit_share(all * gh, groups);
   const int kvh = h / a.G, in_kv = h - kvh * a.G;
-  const int64_t from = a.prefix[r] * gh + (static_cast<int64_t>(kvh) * qg + in_kv / per) * n;
+  const int64_t from = before * gh + (static_cast<int64_t>(kvh) * qg + in_kv / per) * n;
   const int64_t w0 = from / share, w1 = (from + n - 1) / share;
   if (w0 == w1) return;   // one workgroup had all of it and wrote the output
   // the first part is its workgroup's last one (slot 2 w + 1), the others are first ones (slot 2 w)
-  join_row<T, D>(a, head, in_kv % per, a.G < per ? a.G : per, w1 - w0 + 1, 2 * w0 + 1, 2 * w0, 2);
+  join_row<T, D, WAVES>(a, head, in_kv % per, a.G < per ? a.G : per, w1 - w0 + 1, 2 * w0 + 1, 2 * w0, 2);
 }
 
 // --- selected form ------------------------------------------------------------
@@ -1329,9 +1373,10 @@ __global__ void __launch_bounds__(kThreads, 2) kv_selected_staged_kernel(KvAttnA
               whole ? nullptr : a.part_o + (p.item * group_rows + at) * D, a.part_ml + p.item * group_rows + at);
 }
 
-template <class T, int D>
+template <class T, int D, int WAVES>
 __global__ void __launch_bounds__(kThreads) kv_selected_join_kernel(KvAttnArgs a, int per) {
-  const int64_t head = blockIdx.x;
+  const int64_t head = join_head<WAVES>(a);
+  if (head < 0) return;
   const int64_t r = head / a.H;
   const int h = static_cast<int>(head - r * a.H);
   const int64_t n = a.count[r];
@@ -1340,7 +1385,7 @@ __global__ void __launch_bounds__(kThreads) kv_selected_join_kernel(KvAttnArgs a
   const int kvh = h / a.G, in_kv = h - kvh * a.G;
   const int64_t share = split_share(n, a.splits);
   const int64_t slot = ((r * a.Hkv + kvh) * qg + in_kv / per) * a.splits;
-  join_row<T, D>(a, head, in_kv % per, a.G < per ? a.G : per, (n + share - 1) / share, slot, slot, 1);
+  join_row<T, D, WAVES>(a, head, in_kv % per, a.G < per ? a.G : per, (n + share - 1) / share, slot, slot, 1);
 }
 
 // --- accumulated weights ------------------------------------------------------
@@ -1537,13 +1582,22 @@ __global__ void __launch_bounds__(64 * weight_waves(NQ), D == 256 ? 2 : NQ == 1 
 
 // --- dispatch -----------------------------------------------------------------
 
+// Heads up to which a whole workgroup joins one (a long sequence has hundreds of parts); beyond, there are
+// few parts each and a wave does.
+constexpr int64_t kJoinHeads = 512;
+
 template <class T, bool E4M3, int D, int TILES>
 void decode_on(const KvAttnArgs& a, hipStream_t st) {
   const int groups = kKvDecodeGroups;
   if (a.Q > kKvPlanRows) kv_plan_kernel<<<dim3(1), dim3(1024), 0, st>>>(a);
   if constexpr (TILES == 1) kv_decode_kernel<T, E4M3, D><<<dim3(groups), dim3(kThreads), 0, st>>>(a);
   else kv_decode_staged_kernel<T, E4M3, D, TILES / 2><<<dim3(groups), dim3(kThreads), 0, st>>>(a);
-  kv_decode_join_kernel<T, D><<<dim3(static_cast<unsigned>(a.Q * a.H)), dim3(kThreads), 0, st>>>(a, 16 * TILES, groups);
+  const int64_t heads = a.Q * a.H;
+  if (heads <= kJoinHeads)
+    kv_decode_join_kernel<T, D, kWaves><<<dim3(static_cast<unsigned>(heads)), dim3(kThreads), 0, st>>>(a, 16 * TILES, groups);
+  else
+    kv_decode_join_kernel<T, D, 1>
+        <<<dim3(static_cast<unsigned>((heads + kWaves - 1) / kWaves)), dim3(kThreads), 0, st>>>(a, 16 * TILES, groups);
 }
 
 template <class T, bool E4M3, int D, int TILES>
@@ -1553,7 +1607,8 @@ void selected_on(const KvAttnArgs& a, hipStream_t st) {
   if constexpr (TILES == 1) kv_selected_kernel<T, E4M3, D><<<dim3(grid), dim3(kThreads), 0, st>>>(a);
   else kv_selected_staged_kernel<T, E4M3, D, TILES / 2><<<dim3(grid), dim3(kThreads), 0, st>>>(a);
   if (a.splits > 1)
-    kv_selected_join_kernel<T, D><<<dim3(static_cast<unsigned>(a.Q * a.H)), dim3(kThreads), 0, st>>>(a, 16 * TILES);
+    kv_selected_join_kernel<T, D, 1>
+        <<<dim3(static_cast<unsigned>((a.Q * a.H + kWaves - 1) / kWaves)), dim3(kThreads), 0, st>>>(a, 16 * TILES);
 }
 
 template <class T, bool E4M3, int D, int NQ>
