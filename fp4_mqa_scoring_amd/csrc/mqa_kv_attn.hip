@@ -50,6 +50,9 @@ struct Pick<false, A, B> { typedef B type; };
 constexpr int kThreads = 256;
 constexpr int kWaves = 4;
 constexpr int kTilePos = 32;
+// A maximum that is passed by less than this (log2 domain) stays: weights of up to 2^8 lose nothing, and the
+// sums are multiplied once or twice instead of in nearly every one of the first tiles.
+constexpr float kSlack = 8.0f;
 constexpr float kLn2 = 0.69314718055994530942f;
 
 struct Bf16 {
@@ -271,9 +274,9 @@ struct Wave {
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
       top[n] = groups_max(top[n]) * c;
-      rise |= top[n] > m[n];
+      rise |= top[n] > m[n] + kSlack;
     }
-    if (__any(rise)) {   // rare after the first tiles
+    if (__any(rise)) {
 #pragma unroll
       for (int n = 0; n < NQ; ++n) {
         const float to = fmaxf(m[n], top[n]);
@@ -510,11 +513,25 @@ struct Ring {
     __asm__ __volatile__("" ::: "memory");
   }
 
-  // A word of LDS, by hand as the stages' reads are.
-  static __device__ __forceinline__ int read_word(uint32_t at) {
-    int x;
-    __asm__ __volatile__("ds_read_b32 %0, %1\n\ts_waitcnt lgkmcnt(0)" : "=&v"(x) : "v"(at) : "memory");
-    return x;
+  // This lane's slots of stage i of the list at LDS address `list`, by hand as the stages' reads are.
+  static __device__ __forceinline__ void read_slots(int (&slot)[kCopies], int i, int wave, int lane, uint32_t list) {
+    const uint32_t at = list + 4 * (kStagePos * i + copy_row(wave, 0, lane));
+    if constexpr (kCopies == 4) {
+      __asm__ __volatile__(
+          "ds_read_b32 %0, %4\n\tds_read_b32 %1, %4 offset:%5\n\t"
+          "ds_read_b32 %2, %4 offset:%6\n\tds_read_b32 %3, %4 offset:%7\n\ts_waitcnt lgkmcnt(0)"
+          : "=&v"(slot[0]), "=&v"(slot[1]), "=&v"(slot[2]), "=&v"(slot[3])
+          : "v"(at), "n"(4 * kCopyRows), "n"(8 * kCopyRows), "n"(12 * kCopyRows)
+          : "memory");
+    } else if constexpr (kCopies == 2) {
+      __asm__ __volatile__("ds_read_b32 %0, %2\n\tds_read_b32 %1, %2 offset:%3\n\ts_waitcnt lgkmcnt(0)"
+                           : "=&v"(slot[0]), "=&v"(slot[1])
+                           : "v"(at), "n"(4 * kCopyRows)
+                           : "memory");
+    } else {
+      static_assert(kCopies == 1, "one, two or four");
+      __asm__ __volatile__("ds_read_b32 %0, %1\n\ts_waitcnt lgkmcnt(0)" : "=&v"(slot[0]) : "v"(at) : "memory");
+    }
   }
 
   // The piece of a row that a lane fetches for its place in LDS.
@@ -537,16 +554,14 @@ struct Ring {
     }
   }
 
-  // The same of stage i of a list of `len` slots in LDS (the last one again behind its end). Strides
+  // The same of stage i of a list of slots in LDS, filled up to whole stages. Strides
   // are multiples of 16 bytes, a page's below 2^36: their products take one 32-bit multiplication.
   __device__ __forceinline__ void copy_list(const KvAttnArgs& a, const char* kb, const char* vb, int i, int wave,
-                                            int lane, uint32_t list, int len) {
+                                            int lane, uint32_t list) {
     const uint32_t k_page = static_cast<uint32_t>(a.k_page >> 4), v_page = static_cast<uint32_t>(a.v_page >> 4);
     const uint32_t k_pos = static_cast<uint32_t>(a.k_pos >> 4), v_pos = static_cast<uint32_t>(a.v_pos >> 4);
     int slot[kCopies];
-#pragma unroll
-    for (int c = 0; c < kCopies; ++c)
-      slot[c] = read_word(list + 4 * min(kStagePos * i + copy_row(wave, c, lane), len - 1));
+    read_slots(slot, i, wave, lane, list);
 #pragma unroll
     for (int c = 0; c < kCopies; ++c) {
       const int row = copy_row(wave, c, lane);
@@ -1347,8 +1362,9 @@ __global__ void __launch_bounds__(kThreads, 2) kv_selected_staged_kernel(KvAttnA
     const int len = static_cast<int>(p.to - b0 < kKvSelBlock ? p.to - b0 : kKvSelBlock);
     if (b0 != p.from) __syncthreads();
     bool mine = false;
-    for (int i = threadIdx.x; i < len; i += kThreads) {
-      const int s = a.slots[p.r * a.K + b0 + i];
+    const int n = (len + R::kStagePos - 1) / R::kStagePos;
+    for (int i = threadIdx.x; i < n * R::kStagePos; i += kThreads) {
+      const int s = a.slots[p.r * a.K + b0 + min(i, len - 1)];   // the last one again behind the end
       list[i] = s;
       mine |= s < 0 || s >= 64 * a.P_phys;
     }
@@ -1356,10 +1372,9 @@ __global__ void __launch_bounds__(kThreads, 2) kv_selected_staged_kernel(KvAttnA
       bad = true;
       break;
     }
-    const int n = (len + R::kStagePos - 1) / R::kStagePos;
     const uint32_t list_at = lds_address(list);
     ring.run(
-        w, n, part, a.c, [&](int i) { ring.copy_list(a, kb, vb, i, wave, w.lane, list_at, len); },
+        w, n, part, a.c, [&](int i) { ring.copy_list(a, kb, vb, i, wave, w.lane, list_at); },
         [&](int i, int* lo, int* hi) {
           *lo = 0;
           *hi = len - R::kStagePos * i;
