@@ -110,15 +110,27 @@ __device__ __forceinline__ float groups_sum(float x) {
   return __uint_as_float(s[0]) + __uint_as_float(s[1]);
 }
 
-// Passes matrix results on once they can be read, for a branch that overwrites a part of
-// them under a mask: behind such a branch this compiler has left out the wait for the
-// parts that it does not overwrite. A 16x16x32 product takes eight wait states.
-__device__ __forceinline__ void settle(v4f (&s)[1][1]) { __asm__ __volatile__("s_nop 7" : "+v"(s[0][0])); }
-__device__ __forceinline__ void settle(v4f (&s)[1][2]) {
-  __asm__ __volatile__("s_nop 7" : "+v"(s[0][0]), "+v"(s[0][1]));
+// Passes matrix results on once they can be read, which a 16x16x32 product's can after
+// eight wait states. Ordinary code waits for them by itself, but behind a branch that
+// overwrites a part of them under a mask (the edge of a window) this compiler has left out
+// the wait for the other parts, and a maximum was taken of what the registers held before.
+template <int N>
+__device__ __forceinline__ void settle(v4f (&s)[N][1]) {
+  static_assert(N == 1, "one tile of 16 positions goes with one of queries");
+  __asm__ __volatile__("s_nop 7" : "+v"(s[0][0]));
 }
-__device__ __forceinline__ void settle(v4f (&s)[2][2]) {
-  __asm__ __volatile__("s_nop 7" : "+v"(s[0][0]), "+v"(s[0][1]), "+v"(s[1][0]), "+v"(s[1][1]));
+template <int N>
+__device__ __forceinline__ void settle(v4f (&s)[N][2]) {
+  if constexpr (N == 1) {
+    __asm__ __volatile__("s_nop 7" : "+v"(s[0][0]), "+v"(s[0][1]));
+  } else if constexpr (N == 2) {
+    __asm__ __volatile__("s_nop 7" : "+v"(s[0][0]), "+v"(s[0][1]), "+v"(s[1][0]), "+v"(s[1][1]));
+  } else {
+    static_assert(N == 4, "one, two or four");
+    __asm__ __volatile__("s_nop 7"
+                         : "+v"(s[0][0]), "+v"(s[0][1]), "+v"(s[1][0]), "+v"(s[1][1]), "+v"(s[2][0]), "+v"(s[2][1]),
+                           "+v"(s[3][0]), "+v"(s[3][1]));
+  }
 }
 
 // The registers and steps of one wave: NQ tiles of 16 query heads of one row and
@@ -243,32 +255,25 @@ struct Wave {
         for (int a = 0; a < kTiles; ++a) s[n][a] = T::mfma(x[a], y, s[n][a]);
       }
     }
-  }
-
-  // The largest of this lane's scores.
-  static __device__ __forceinline__ float highest(const v4f (&s)[kTiles]) {
-    float x = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3]));
-#pragma unroll
-    for (int a = 1; a < kTiles; ++a) x = fmaxf(x, fmaxf(fmaxf(s[a][0], s[a][1]), fmaxf(s[a][2], s[a][3])));
-    return x;
+    settle(s);
   }
 
   // Scores to weights; `inside` bit j says whether this lane's j-th position counts
   // (looked at where `edge`). Returns the weights packed as the second product's operand.
   __device__ __forceinline__ void weights(v4f (&s)[NQ][kTiles], float c, bool edge, uint32_t inside, P (&p)[NQ]) {
     float top[NQ];
-    if (edge) {
-      settle(s);
 #pragma unroll
-      for (int n = 0; n < NQ; ++n) {
+    for (int n = 0; n < NQ; ++n) {
+      if (edge) {
 #pragma unroll
         for (int j = 0; j < kMine; ++j)
           if (!(inside >> j & 1)) s[n][j >> 2][j & 3] = -__builtin_inff();
-        top[n] = highest(s[n]);
       }
-    } else {
+      float x = fmaxf(fmaxf(s[n][0][0], s[n][0][1]), fmaxf(s[n][0][2], s[n][0][3]));
 #pragma unroll
-      for (int n = 0; n < NQ; ++n) top[n] = highest(s[n]);
+      for (int a = 1; a < kTiles; ++a)
+        x = fmaxf(x, fmaxf(fmaxf(s[n][a][0], s[n][a][1]), fmaxf(s[n][a][2], s[n][a][3])));
+      top[n] = x;
     }
     bool rise = false;
 #pragma unroll
