@@ -1447,15 +1447,19 @@ __global__ void __launch_bounds__(64 * weight_waves(NQ), D == 256 ? 2 : NQ == 1 
   __shared__ v4u q_lds[W::kShared ? NQ * W::kChunks * 64 : 1];
   __shared__ float part[(NQ > 1 ? 1 : kWeightWaves) * kBlock];
   __shared__ int covered[kBlock];
+  __shared__ int next_seq;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int head_at = wave % hg, tile_at = wave / hg, tile_step = kWeightWaves / hg;
   const int64_t me = blockIdx.x;
   const int qg = (a.G + 16 * NQ - 1) / (16 * NQ);
   W w;
   w.init();
-  for (int64_t s0 = 0; s0 < a.n_seq; s0 += kWeightSeqs) {
+  // kWeightSeqs sequences at a time, from the first that a row behind the ones before belongs to
+  int64_t s0 = 0;
+  do {
     // the positions that any row of each sequence looks at
     __syncthreads();
+    if (threadIdx.x == 0) next_seq = 0x7FFFFFFF;
     for (int i = threadIdx.x; i < kWeightSeqs; i += kWeightThreads) {
       seq_lo[i] = 0x7FFFFFFF;
       seq_hi[i] = 0;
@@ -1469,6 +1473,8 @@ __global__ void __launch_bounds__(64 * weight_waves(NQ), D == 256 ? 2 : NQ == 1 
       if (n > 0 && i >= 0 && i < kWeightSeqs) {
         atomicMin(&seq_lo[i], a.row_start[r]);
         atomicMax(&seq_hi[i], a.row_end[r]);
+      } else if (n > 0 && i >= kWeightSeqs) {
+        atomicMin(&next_seq, a.seq_of_row[r]);
       }
     }
     __syncthreads();
@@ -1489,6 +1495,7 @@ __global__ void __launch_bounds__(64 * weight_waves(NQ), D == 256 ? 2 : NQ == 1 
     }
     if (threadIdx.x == 0) prefix[kWeightSeqs] = units;
     __syncthreads();
+    const int64_t after = next_seq;
 
     const int64_t share = (units + gridDim.x - 1) / gridDim.x;
     int64_t cur = me * share;
@@ -1601,7 +1608,8 @@ __global__ void __launch_bounds__(64 * weight_waves(NQ), D == 256 ? 2 : NQ == 1 
           acc[seq * acc_stride + 32 * t_lo + i] += total;
         }
     }
-  }
+    s0 = after;
+  } while (s0 < a.n_seq);
 }
 
 // --- dispatch -----------------------------------------------------------------

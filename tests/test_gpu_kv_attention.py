@@ -243,6 +243,44 @@ def test_decode_nan_and_infinities_inside_the_window():
     assert torch.isnan(out).all() and (lse == float("-inf")).all()
 
 
+@pytest.mark.parametrize("H,Hkv", [(8, 2), (64, 1)])
+def test_parts_whose_scores_are_all_minus_infinity_drop_out(H, Hkv):
+    """Of a sequence that many workgroups share, the first and the last of them meet nothing but -infinity."""
+    n, lo, hi = 20000, 9001, 10002
+    c = Case([n], H, Hkv, 64, "bf16", seed=30)
+    q = c.queries(1).abs() + 0.1
+    pos = torch.arange(n)
+    out_of = pos[(pos < lo) | (pos >= hi)]
+    c.k[c.table[0].long()[out_of // 64], out_of % 64] = float("-inf")
+    c.dk = c.k.to(DEV)
+    want = Row(q[0], *c.at(0, lo, hi), 64 ** -0.5, c.qt)
+    out, lse = run_decode(c, q, [0], [0], [n])
+    assert_row(out[0], lse[0], want)
+    slots = (c.table[0].long()[pos // 64] * 64 + pos % 64)[None].numpy()
+    out, lse = run_selected(c, q, slots, [n])
+    assert_row(out[0], lse[0], want)
+
+
+def test_batches_without_rows_sequences_or_pages():
+    c = Case([70], 4, 2, 64, "bf16", seed=33)
+    q = c.queries(0)
+    assert run_decode(c, q, [], [], [])[0].shape == (0, 4, 64)
+    assert run_selected(c, q, np.zeros((0, 5), np.int64), [])[0].shape == (0, 4, 64)
+    mqa.mqa_fp4_status()
+    q = c.queries(3)
+    c.dk, c.dv = c.dk[:0], c.dv[:0]                 # no pages: empty windows and lists only
+    out, lse = run_decode(c, q, [0, 0, 0], [0, 5, 0], [0, 5, 1])
+    assert mqa.mqa_fp4_status() == mqa.STATUS_BAD_PAGE
+    assert (out[:2] == 0).all() and (lse[:2] == float("-inf")).all() and torch.isnan(out[2]).all()
+    out, lse = run_selected(c, q, np.zeros((3, 2), np.int64), [0, 0, 1])
+    assert mqa.mqa_fp4_status() == mqa.STATUS_BAD_PAGE
+    assert (out[:2] == 0).all() and (lse[:2] == float("-inf")).all() and torch.isnan(out[2]).all()
+    c.table = c.table[:0]                           # no sequences
+    out, lse = run_decode(c, q, [0, 0, -1], [0, 0, 0], [0, 0, 0])
+    assert mqa.mqa_fp4_status() == mqa.STATUS_BAD_WINDOW
+    assert torch.isnan(out).all() and torch.isnan(lse).all()
+
+
 def test_decode_offsets_beyond_32_bits():
     """A pool of 6 GiB whose used pages lie at both ends."""
     P = 6 * 2 ** 30 // (64 * 128 * 2)

@@ -109,6 +109,44 @@ def test_weights_with_more_sequences_than_one_plan_and_a_wide_pitch():
     assert ((got.double() - want).abs() <= tol).all()
 
 
+def test_weights_of_sequences_far_apart():
+    """Few rows among many sequences; the sums of the others keep their bits."""
+    n, places = 5000, [4999, 0, 2047, 2048, 1023]
+    c = Case([130] * 5, 2, 1, 64, "bf16", seed=9)
+    q = c.queries(5)
+    small = torch.rand(5, 64 * c.table.shape[1], generator=c.g)
+    order, zero, end = np.arange(5), np.zeros(5, int), np.array([130, 64, 1, 129, 100])
+    want, tol, _, lse = expected_weights(c, q, order, zero, end, small)
+    table = torch.full((n, c.table.shape[1]), -1, dtype=torch.int32)
+    table[places] = c.table
+    acc = torch.full((n, small.shape[1]), 0.25)
+    acc[places] = small
+    c.table = table
+    mqa.mqa_fp4_status()
+    got = run_weights(c, q, lse, places, zero, end, acc)
+    assert mqa.mqa_fp4_status() == 0
+    assert ((got[places].double() - want).abs() <= tol + 1e-300).all()
+    others = torch.ones(n, dtype=torch.bool)
+    others[places] = False
+    assert (got[others] == 0.25).all()
+
+
+def test_weights_without_rows_sequences_or_pages():
+    c = Case([70], 4, 2, 64, "bf16", seed=10)
+    acc = torch.rand(1, 128)
+    mqa.mqa_fp4_status()
+    assert torch.equal(run_weights(c, c.queries(0), torch.zeros(0, 4), [], [], [], acc), acc)
+    q = c.queries(2)
+    c.dk = c.dk[:0]
+    assert torch.equal(run_weights(c, q, torch.zeros(2, 4), [0, 0], [0, 3], [0, 3], acc), acc)
+    assert mqa.mqa_fp4_status() == 0
+    assert torch.equal(run_weights(c, q, torch.zeros(2, 4), [0, 0], [0, 0], [0, 1], acc), acc)
+    assert mqa.mqa_fp4_status() == mqa.STATUS_BAD_PAGE
+    c.table = c.table[:0]
+    run_weights(c, q, torch.zeros(2, 4), [0, -1], [0, 0], [0, 0], acc[:0])
+    assert mqa.mqa_fp4_status() == mqa.STATUS_BAD_WINDOW
+
+
 # --- the choice -------------------------------------------------------------------
 
 
@@ -172,6 +210,20 @@ def test_select_long_and_many(n, length):
     lens = [length - 7 * (s % 5) for s in range(n)]
     for budget, recent in ((length // 3, length // 20), (length - 100, 0), (5, 2)):
         check_select(acc, lens, budget, recent, *run_select(acc, lens, budget, recent))
+
+
+def test_select_and_compact_without_sequences_positions_or_budget():
+    e = torch.empty(0, dtype=torch.int32, device=DEV)
+    mqa.mqa_kv_evict_select(torch.empty(0, 5, device=DEV), e, 3, 1, e.view(0, 3), e)
+    keep, kept, _ = run_select(torch.empty(2, 0), [0, 0], 3, 1)
+    assert (keep == -1).all() and (kept == 0).all()
+    table = i32([[0], [1]])
+    pool, new = torch.rand(2, 64, device=DEV), torch.zeros(2, 64, device=DEV)
+    mqa.mqa_kv_compact(i32(keep), i32(kept), table, table, [(pool, new)])
+    mqa.mqa_kv_compact(e.view(0, 3), e, e.view(0, 1), e.view(0, 1), [(pool, new)])
+    mqa.mqa_kv_compact(i32(keep)[:, :0].contiguous(), i32(kept), table, table, [(pool, new)])
+    mqa.mqa_kv_compact(i32(keep), i32(kept), table, table, [])
+    assert (new == 0).all()
 
 
 def test_select_lengths_that_fail_closed():
@@ -332,3 +384,61 @@ def test_decode_step_with_selection_and_eviction():
         assert np.array_equal(slot2[r].cpu().numpy(), new_table[r].cpu().numpy()[new // 64] * 64 + new % 64)
         before = set(raw[r].cpu().numpy().tolist()) & set(keep[r].cpu().numpy().tolist())
         assert before <= set(keep[r].cpu().numpy()[new].tolist())
+
+
+@pytest.mark.parametrize("capacity", [64 * 40, 64 * 400])
+def test_accumulate_choose_and_move_in_graphs_and_on_streams(capacity):
+    """The three calls in one graph, replayed as the lengths and sums change, and at once on two streams."""
+    lengths, budget, recent, H = [2500, 700, 64], 333, 20, 8
+    c = Case(lengths, H, 2, 64, "bf16", seed=12, capacity=capacity // 64, spare=20)
+    q = c.queries(3).to(DEV)
+    used = set(c.table[c.table >= 0].tolist())
+    free = [p for p in range(c.P) if p not in used]
+    new_table = i32(np.array(free[:18]).reshape(3, 6))
+    table, seq, zero, end = c.table.to(DEV), i32([0, 1, 2]), i32([0, 0, 0]), i32(lengths)
+    size = mqa.mqa_kv_evict_workspace_bytes(3, capacity)
+    assert (size > 0) == (capacity > 16384)
+    lse = torch.full((3, H), 5.0, device=DEV)
+
+    def outputs():
+        return dict(acc=torch.rand(3, capacity, generator=torch.Generator().manual_seed(1)).to(DEV),
+                    keep=torch.zeros(3, budget, dtype=torch.int32, device=DEV),
+                    kept=torch.zeros(3, dtype=torch.int32, device=DEV), kept_acc=torch.zeros(3, budget, device=DEV),
+                    ws=torch.full((size,), 0xFF, dtype=torch.uint8, device=DEV), pool=torch.zeros_like(c.dk))
+
+    def step(o, stream=None):
+        mqa.mqa_kv_weights_accumulate(q, lse, c.dk, table, seq, zero, end, o["acc"], stream=stream)
+        mqa.mqa_kv_evict_select(o["acc"], end, budget, recent, o["keep"], o["kept"], o["ws"], kept_acc=o["kept_acc"],
+                                stream=stream)
+        mqa.mqa_kv_compact(o["keep"], o["kept"], table, new_table, [(c.dk, o["pool"])], stream=stream)
+
+    def same(a, b):
+        return all(torch.equal(a[k].view(torch.uint8), b[k].view(torch.uint8)) for k in ("acc", "keep", "kept", "kept_acc", "pool"))
+
+    eager = outputs()
+    step(eager)
+    torch.cuda.synchronize()
+    a = eager["acc"].cpu().numpy()
+    for s in range(3):
+        assert np.array_equal(eager["keep"][s, : eager["kept"][s]].cpu().numpy(), evict_keep(a[s], lengths[s], budget, recent))
+    sides = [(torch.cuda.Stream(), outputs()) for _ in range(2)]
+    torch.cuda.synchronize()
+    for st, o in sides:
+        step(o, st)
+    torch.cuda.synchronize()
+    assert all(same(o, eager) for _, o in sides)
+
+    o = outputs()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(o)
+    o["acc"].copy_(outputs()["acc"])
+    eager = outputs()
+    for i in range(3):
+        end.copy_(i32([max(0, n - 200 * i) for n in lengths]))
+        q.copy_(c.queries(3))
+        graph.replay()
+        torch.cuda.synchronize()
+        step(eager)
+        torch.cuda.synchronize()
+        assert same(o, eager), i
