@@ -74,10 +74,13 @@ struct KvEvictArgs {
   uint32_t* state;    // [n_seq, 4]
 };
 // Sequences of up to 16,384 positions (the capacity's bound, as the host knows no lengths) take one
-// workgroup; longer ones one per chunk.
-constexpr int kKvEvictChunk = 8192;
+// workgroup; longer ones one per chunk, of which there are at most 256.
+constexpr int kKvEvictPiece = 8192, kKvEvictChunks = 256;
+// Chunks that a launch and its workspace have room for.
 constexpr int64_t kv_evict_chunks(int64_t max_len) {
-  return max_len <= 16384 ? 1 : (max_len + kKvEvictChunk - 1) / kKvEvictChunk;
+  if (max_len <= 16384) return 1;
+  const int64_t pieces = (max_len + kKvEvictPiece - 1) / kKvEvictPiece;
+  return pieces < kKvEvictChunks ? pieces : kKvEvictChunks;
 }
 hipError_t launch_kv_evict_select(const KvEvictArgs& a, hipStream_t st);
 

@@ -222,12 +222,50 @@ __global__ void __launch_bounds__(kSelThreads) kv_evict_select_kernel(KvEvictArg
 
 // --- long sequences: one workgroup per chunk -----------------------------------
 
-constexpr int kChunkSteps = kKvEvictChunk / kSelThreads;   // 64-position steps of a wave
+// A chunk is one piece of 8,192 positions where up to 2,097,152 compete, else several, one in registers at a time:
+// every workgroup adds up all chunks' counts, which would come to outweigh the rest (5,000,000 positions: 150 us, with
+// chunks of one piece 975).
+constexpr int kChunkSteps = kKvEvictPiece / kSelThreads;   // 64-position steps of a wave
 constexpr int kDigitBins = 2048;                           // digits of 11, 11 and 10 bits
 __device__ __forceinline__ int digit_shift(int stage) { return stage == 0 ? 21 : stage == 1 ? 10 : 0; }
 __device__ __forceinline__ uint32_t digit_of(uint32_t key, int stage) {
   return key >> digit_shift(stage) & (stage == 2 ? 1023u : 2047u);
 }
+
+// One piece: this thread's positions and their sums.
+struct Piece {
+  float v[kChunkSteps];
+  int base;
+
+  __device__ __forceinline__ int position(int it) const {
+    return base + (threadIdx.x >> 6) * (64 * kChunkSteps) + 64 * it + (threadIdx.x & 63);
+  }
+  __device__ __forceinline__ void load(const SelectRow& row, int at) {
+    base = at;
+#pragma unroll
+    for (int it = 0; it < kChunkSteps; ++it) v[it] = position(it) < row.old ? row.acc[position(it)] : 0.0f;
+  }
+};
+
+// The chunks of a row of which `old` >= 1 positions compete: 2^shift pieces each, as few as make no more than
+// kKvEvictChunks of them. LONG false: capacities where that is one piece (choosing in the kernel costs 0.3 us a launch).
+template <bool LONG>
+struct Chunks {
+  int pieces, shift, n;
+
+  __device__ __forceinline__ explicit Chunks(int old) {
+    pieces = (old - 1) / kKvEvictPiece + 1;
+    const uint32_t over = static_cast<uint32_t>(pieces - 1) / kKvEvictChunks;
+    shift = !LONG || over == 0 ? 0 : 32 - __builtin_clz(over);
+    n = ((pieces - 1) >> shift) + 1;
+  }
+  __device__ __forceinline__ int first(int c) const { return (c << shift) * kKvEvictPiece; }   // position
+  __device__ __forceinline__ int pieces_of(int c) const {
+    if (!LONG) return 1;
+    const int left = pieces - (c << shift);
+    return left < 1 << shift ? left : 1 << shift;
+  }
+};
 
 struct ChunkMemory {
   uint32_t hist[2 * kDigitBins];   // two copies
@@ -275,20 +313,18 @@ __device__ __forceinline__ void chunk_digit(const uint32_t* counts, int chunks, 
 
 // Counts one digit of a chunk's keys whose upper digits are the m-th key's. state[s * 4 + 2 d, + 1]:
 // prefix and need behind digit d (d < 2).
+template <bool LONG>
 __global__ void __launch_bounds__(kSelThreads) kv_evict_count_kernel(KvEvictArgs a, int chunks, int stage) {
   __shared__ __align__(16) ChunkMemory lds;
   const int64_t s = blockIdx.x / chunks;
   const int c = static_cast<int>(blockIdx.x - s * chunks);
   const SelectRow row(a, s);
-  if (row.m == 0 || row.m == row.old || c * kKvEvictChunk >= row.old) return;
+  if (row.m == 0 || row.m == row.old) return;
+  const Chunks<LONG> of(row.old);
+  if (c >= of.n) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int from = c * kKvEvictChunk + wave * (64 * kChunkSteps);
-  float x[kChunkSteps];
-#pragma unroll
-  for (int it = 0; it < kChunkSteps; ++it) {
-    const int i = from + 64 * it + lane;
-    x[it] = i < row.old ? row.acc[i] : 0.0f;
-  }
+  Piece x;
+  x.load(row, of.first(c));
   uint32_t* counts = a.counts + s * chunks * 3 * kDigitBins;
   uint32_t* state = a.state + 4 * s;
   uint32_t prefix = 0, need = static_cast<uint32_t>(row.m);
@@ -297,7 +333,7 @@ __global__ void __launch_bounds__(kSelThreads) kv_evict_count_kernel(KvEvictArgs
       prefix = state[0];
       need = state[1];
     }
-    chunk_digit(counts, (row.old + kKvEvictChunk - 1) / kKvEvictChunk, stage - 1, lds, &prefix, &need);
+    chunk_digit(counts, of.n, stage - 1, lds, &prefix, &need);
     if (c == 0 && threadIdx.x == 0) {
       state[2 * (stage - 1)] = prefix;
       state[2 * (stage - 1) + 1] = need;
@@ -306,19 +342,23 @@ __global__ void __launch_bounds__(kSelThreads) kv_evict_count_kernel(KvEvictArgs
   for (int i = threadIdx.x; i < 2 * kDigitBins; i += kSelThreads) lds.hist[i] = 0;
   __syncthreads();
   const uint32_t mask = stage == 0 ? 0u : ~0u << digit_shift(stage - 1);
+  for (int left = of.pieces_of(c);;) {
 #pragma unroll
-  for (int it = 0; it < kChunkSteps; ++it) {
-    const uint32_t k = order_bits(x[it]);
-    const bool in = from + 64 * it + lane < row.old && ((k ^ prefix) & mask) == 0;
-    const uint64_t all = __ballot(in);
-    if (all == 0) continue;
-    const uint32_t digit = digit_of(k, stage);
-    // one addition for the lanes with the first one's digit
-    const int leader = __builtin_ctzll(all);
-    const uint32_t first = __builtin_amdgcn_readlane(static_cast<int>(digit), leader);
-    const uint64_t same = __ballot(in && digit == first);
-    if (in && (digit != first || lane == leader))
-      atomicAdd(&lds.hist[2 * digit + (lane & 1)], digit == first ? __popcll(same) : 1u);
+    for (int it = 0; it < kChunkSteps; ++it) {
+      const uint32_t k = order_bits(x.v[it]);
+      const bool in = x.position(it) < row.old && ((k ^ prefix) & mask) == 0;
+      const uint64_t all = __ballot(in);
+      if (all == 0) continue;
+      const uint32_t digit = digit_of(k, stage);
+      // one addition for the lanes with the first one's digit
+      const int leader = __builtin_ctzll(all);
+      const uint32_t first = __builtin_amdgcn_readlane(static_cast<int>(digit), leader);
+      const uint64_t same = __ballot(in && digit == first);
+      if (in && (digit != first || lane == leader))
+        atomicAdd(&lds.hist[2 * digit + (lane & 1)], digit == first ? __popcll(same) : 1u);
+    }
+    if (--left == 0) break;
+    x.load(row, x.base + kKvEvictPiece);
   }
   __syncthreads();
   uint32_t* mine = counts + (static_cast<int64_t>(c) * 3 + stage) * kDigitBins;
@@ -326,29 +366,27 @@ __global__ void __launch_bounds__(kSelThreads) kv_evict_count_kernel(KvEvictArgs
 }
 
 // Writes a chunk's kept positions where the counts say.
+template <bool LONG>
 __global__ void __launch_bounds__(kSelThreads) kv_evict_write_kernel(KvEvictArgs a, int chunks) {
   __shared__ __align__(16) ChunkMemory lds;
   const int64_t s = blockIdx.x / chunks;
   const int c = static_cast<int>(blockIdx.x - s * chunks);
   const SelectRow row(a, s);
   row.write_rest(a, s, c * kSelThreads + threadIdx.x, static_cast<int64_t>(chunks) * kSelThreads);
-  if (row.m == 0 || c * kKvEvictChunk >= row.old) return;
+  if (row.m == 0) return;
+  const Chunks<LONG> of(row.old);
+  if (c >= of.n) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int from = c * kKvEvictChunk + wave * (64 * kChunkSteps);
-  float x[kChunkSteps];
-#pragma unroll
-  for (int it = 0; it < kChunkSteps; ++it) {
-    const int i = from + 64 * it + lane;
-    x[it] = i < row.old ? row.acc[i] : 0.0f;
-  }
+  Piece x;
+  x.load(row, of.first(c));
   const bool all = row.m == row.old;
   uint32_t prefix = 0, need = 0;
-  int at = c * kKvEvictChunk, equals = 0;   // kept ones before the chunk where all are
+  int aboves = of.first(c), equals = 0;   // positions before the piece above the m-th key (every one where all are kept), equal to it
   if (!all) {
     const uint32_t* counts = a.counts + s * chunks * 3 * kDigitBins;
     prefix = a.state[4 * s + 2];
     need = a.state[4 * s + 3];
-    chunk_digit(counts, (row.old + kKvEvictChunk - 1) / kKvEvictChunk, 2, lds, &prefix, &need);
+    chunk_digit(counts, of.n, 2, lds, &prefix, &need);
     // keys above the m-th one in earlier chunks: by the digit at which they differ
     uint32_t above = 0, equal = 0;
     const uint32_t bin = 2 * threadIdx.x;
@@ -370,49 +408,58 @@ __global__ void __launch_bounds__(kSelThreads) kv_evict_write_kernel(KvEvictArgs
       lds.equal[wave] = equal;
     }
     __syncthreads();
-    at = 0;
+    aboves = 0;
     for (int i = 0; i < kSelWaves; ++i) {
-      at += static_cast<int>(lds.above[i]);
+      aboves += static_cast<int>(lds.above[i]);
       equals += static_cast<int>(lds.equal[i]);
     }
     __syncthreads();
   }
   const int want = static_cast<int>(need);
-  // the waves before this one
-  int above = 0, equal = 0;
+  for (int left = of.pieces_of(c);;) {
+    int above = 0, equal = 0;
 #pragma unroll
-  for (int it = 0; it < kChunkSteps; ++it) {
-    const bool valid = from + 64 * it + lane < row.old;
-    const uint32_t k = order_bits(x[it]);
-    above += __popcll(__ballot(valid && (all || k > prefix)));
-    equal += __popcll(__ballot(valid && !all && k == prefix));
-  }
-  if (lane == 0) {
-    lds.above[wave] = above;
-    lds.equal[wave] = equal;
-  }
-  __syncthreads();
-  for (int i = 0; i < wave; ++i) {
-    at += static_cast<int>(lds.above[i]);
-    equals += static_cast<int>(lds.equal[i]);
-  }
-  at += equals < want ? equals : want;
-#pragma unroll
-  for (int it = 0; it < kChunkSteps; ++it) {
-    const int i = from + 64 * it + lane;
-    const bool valid = i < row.old;
-    const uint32_t k = order_bits(x[it]);
-    const bool eq = valid && !all && k == prefix;
-    const uint64_t eqs = __ballot(eq);
-    const bool take = (valid && (all || k > prefix)) || (eq && equals + mbcnt64(eqs) < want);
-    const uint64_t taken = __ballot(take);
-    if (take) {
-      const int j = at + mbcnt64(taken);
-      row.keep[j] = i;
-      if (row.kept_acc != nullptr) row.kept_acc[j] = x[it];
+    for (int it = 0; it < kChunkSteps; ++it) {
+      const bool valid = x.position(it) < row.old;
+      const uint32_t k = order_bits(x.v[it]);
+      above += __popcll(__ballot(valid && (all || k > prefix)));
+      equal += __popcll(__ballot(valid && !all && k == prefix));
     }
-    at += __popcll(taken);
-    equals += __popcll(eqs);
+    if (lane == 0) {
+      lds.above[wave] = above;
+      lds.equal[wave] = equal;
+    }
+    __syncthreads();
+    // the waves before this one
+    int at = aboves, eq_at = equals;
+    for (int i = 0; i < wave; ++i) {
+      at += static_cast<int>(lds.above[i]);
+      eq_at += static_cast<int>(lds.equal[i]);
+    }
+    at += eq_at < want ? eq_at : want;
+#pragma unroll
+    for (int it = 0; it < kChunkSteps; ++it) {
+      const bool valid = x.position(it) < row.old;
+      const uint32_t k = order_bits(x.v[it]);
+      const bool eq = valid && !all && k == prefix;
+      const uint64_t eqs = __ballot(eq);
+      const bool take = (valid && (all || k > prefix)) || (eq && eq_at + mbcnt64(eqs) < want);
+      const uint64_t taken = __ballot(take);
+      if (take) {
+        const int j = at + mbcnt64(taken);
+        row.keep[j] = x.position(it);
+        if (row.kept_acc != nullptr) row.kept_acc[j] = x.v[it];
+      }
+      at += __popcll(taken);
+      eq_at += __popcll(eqs);
+    }
+    if (--left == 0) break;
+    for (int i = 0; i < kSelWaves; ++i) {
+      aboves += static_cast<int>(lds.above[i]);
+      equals += static_cast<int>(lds.equal[i]);
+    }
+    x.load(row, x.base + kKvEvictPiece);
+    __syncthreads();   // the counts are read
   }
 }
 
@@ -493,8 +540,11 @@ hipError_t launch_kv_evict_select(const KvEvictArgs& a, hipStream_t st) {
     kv_evict_select_kernel<<<grid, block, 0, st>>>(a);
   } else {
     const int n = static_cast<int>(chunks);
-    for (int stage = 0; stage < 3; ++stage) kv_evict_count_kernel<<<grid, block, 0, st>>>(a, n, stage);
-    kv_evict_write_kernel<<<grid, block, 0, st>>>(a, n);
+    const bool several = a.max_len > kKvEvictPiece * kKvEvictChunks;
+    const auto count = several ? kv_evict_count_kernel<true> : kv_evict_count_kernel<false>;
+    const auto write = several ? kv_evict_write_kernel<true> : kv_evict_write_kernel<false>;
+    for (int stage = 0; stage < 3; ++stage) count<<<grid, block, 0, st>>>(a, n, stage);
+    write<<<grid, block, 0, st>>>(a, n);
   }
   return hipGetLastError();
 }

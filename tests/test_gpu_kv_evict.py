@@ -212,6 +212,16 @@ def test_select_long_and_many(n, length):
         check_select(acc, lens, budget, recent, *run_select(acc, lens, budget, recent))
 
 
+def test_select_more_positions_than_chunks_of_one_piece():
+    """Above 2,097,152 positions a chunk has several pieces; shorter sequences beside them have not."""
+    g = torch.Generator(device=DEV).manual_seed(4)
+    lens = [5000001, 2097153, 2097152, 16385, 1, 0]
+    acc = torch.exp(2 * torch.randn(len(lens), 5000001, generator=g, device=DEV))
+    acc[1] = torch.randint(0, 4, (5000001,), generator=g, device=DEV).float() / 4
+    for budget, recent in ((1000003, 77), (2097152, 0), (5, 2)):
+        check_select(acc, lens, budget, recent, *run_select(acc, lens, budget, recent))
+
+
 def test_select_and_compact_without_sequences_positions_or_budget():
     e = torch.empty(0, dtype=torch.int32, device=DEV)
     mqa.mqa_kv_evict_select(torch.empty(0, 5, device=DEV), e, 3, 1, e.view(0, 3), e)

@@ -152,6 +152,17 @@ def test_workspace_sizes_refuse_bad_sizes(lib):
         mqa.mqa_kv_attention_decode_workspace_bytes(4, 8, 2, 80)
     with pytest.raises(mqa.MQAError):
         mqa.mqa_kv_evict_workspace_bytes(-1, 5)
+    for args in ((1, (1 << 31) - 512), (1 << 22, 5), (1 << 14, 1 << 30)):
+        with pytest.raises(mqa.MQAError):
+            mqa.mqa_kv_evict_workspace_bytes(*args)
+
+
+def test_workspaces_do_not_grow_with_the_capacity_for_ever():
+    assert mqa.mqa_kv_evict_workspace_bytes(1000, 16384) == 0
+    size = mqa.mqa_kv_evict_workspace_bytes(3, 1 << 21)
+    assert size == mqa.mqa_kv_evict_workspace_bytes(3, (1 << 31) - 513) == 256 + 3 * 256 * 3 * 2048 * 4
+    assert mqa.mqa_kv_attention_selected_workspace_bytes(1, 1 << 16, 8, 2, 128) == \
+        mqa.mqa_kv_attention_selected_workspace_bytes(1, (1 << 31) - 1, 8, 2, 128)
 
 
 def test_eviction_is_checked_on_the_host(lib):
