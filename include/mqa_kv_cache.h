@@ -18,8 +18,8 @@
  * pointer and the strides, in ELEMENTS, of page, position and head; the D
  * elements of one head are contiguous. So [P, 64, Hkv, D] and [P, Hkv, 64, D]
  * memory, or keys and values interleaved in one pool, all fit. Bases and
- * strides must be multiples of 16 bytes, strides not negative, and one page
- * must span less than 2 GiB. Everything behind a page, position or head that
+ * strides must be multiples of 16 bytes, strides not negative and below 2^35
+ * elements, and one page must span less than 2 GiB. Everything behind a page, position or head that
  * a call does not address is never read.
  *
  * Types. MQA_KV_BF16 and MQA_KV_FP16 caches go with queries and outputs of the
@@ -65,7 +65,7 @@ typedef struct mqa_kv_cache {
 } mqa_kv_cache;
 
 /* The queries: [num_rows, H, D] with a row stride (elements; a multiple of 16
- * bytes, at least H * D unless num_rows <= 1), the heads of one row contiguous, so that a
+ * bytes, H * D .. 2^32 unless num_rows <= 1), the heads of one row contiguous, so that a
  * slice of a fused projection's output fits. 16-byte aligned. */
 typedef struct mqa_kv_query {
   const void* q;
@@ -91,8 +91,9 @@ typedef struct mqa_kv_query {
  * end < start, and one whose window touches a page that maps outside [0,
  * P_phys), fails closed: out and lse are NaN and MQA_STATUS_BAD_WINDOW or
  * MQA_STATUS_BAD_PAGE is set. Nothing outside the windows is read, so NaN or
- * infinities there do not matter; inside they take part by IEEE rules (a NaN
- * or infinite score makes that head's out NaN).
+ * infinities there do not matter; inside they take part by IEEE rules: a NaN or
+ * +infinite score, or nothing but -infinite ones, make that head's out NaN; a
+ * -infinite score beside others drops out.
  * workspace: mqa_kv_attention_decode_workspace_bytes() bytes, 256-byte aligned.
  * The work is cut into equal shares over the whole batch's pages, whatever the
  * lengths are, so max_pages may be any capacity.
@@ -158,7 +159,9 @@ int32_t mqa_kv_weights_accumulate(const mqa_kv_query* q, const float* lse, const
  *   kept_acc float [num_seqs, budget]   optional: their acc, padded with 0 (the
  *            sums to go on with after mqa_kv_compact)
  * kept_acc must not overlap acc.
- * workspace: mqa_kv_evict_workspace_bytes() bytes, 256-byte aligned.
+ * workspace: mqa_kv_evict_workspace_bytes() bytes, 256-byte aligned: 0 (and the
+ * workspace then NULL) up to a max_len of 16,384, at most 6.3 MB per sequence.
+ * num_seqs: at most 16,383 whatever max_len is, 4,194,240 up to a max_len of 16,384.
  */
 int32_t mqa_kv_evict_select(const float* acc, int64_t acc_stride, const int32_t* seq_len, int64_t num_seqs,
                             int64_t max_len, int64_t budget, int64_t recent, int32_t* keep, int32_t* kept,
@@ -166,8 +169,9 @@ int32_t mqa_kv_evict_select(const float* acc, int64_t acc_stride, const int32_t*
 int64_t mqa_kv_evict_workspace_bytes(int64_t num_seqs, int64_t max_len);
 
 /* One paged array to compact: rows_per_position pieces of row_bytes bytes per
- * position, at byte strides of page, position and piece. Bases, strides and
- * row_bytes must be multiples of 4 bytes. src and dst may be one pool. */
+ * position (2^24 bytes together at most), at byte strides of page, position and
+ * piece, 0 .. 2^32. Bases, strides and row_bytes must be multiples of 4 bytes.
+ * src and dst may be one pool. */
 typedef struct mqa_kv_array {
   const void* src;
   void* dst;
