@@ -20,7 +20,8 @@ struct KvAttnArgs {
   int32_t H, Hkv, D;
   int32_t G;                 // query heads per key head
   int32_t q_type, kv_type;   // MQA_KV_*
-  float c;                   // |scale * k_scale| * log2(e)
+  float c;                   // |scale * k_scale| * log2(e), or 1 where that is 0
+  uint32_t q_keep;           // 0 where scale * k_scale is 0 (the queries count as 0), else all bits
   uint32_t q_flip;           // 0x80008000 where scale * k_scale is negative, else 0
   float score_scale;         // scale * k_scale (weights)
   float v_scale;
@@ -47,7 +48,7 @@ constexpr int kv_tiles(int D, int G) { return G <= 16 ? 1 : G <= 32 || D == 256 
 constexpr int kv_head_groups(int D, int G) { return (G + 16 * kv_tiles(D, G) - 1) / (16 * kv_tiles(D, G)); }
 constexpr int kv_group_rows(int D, int G) { return G < 16 * kv_tiles(D, G) ? G : 16 * kv_tiles(D, G); }
 
-// Workgroups of the decode form: what 256 compute units hold at once.
+// Workgroups of the decode form: what 256 compute units hold at once (two each, by LDS and registers).
 constexpr int kKvDecodeGroups = 512;
 constexpr int kKvPlanRows = 1024;     // rows up to which every workgroup plans for itself
 constexpr int kKvSelBlock = 1024;     // slots staged at once by the selected form

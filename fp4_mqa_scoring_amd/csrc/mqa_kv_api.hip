@@ -81,7 +81,10 @@ int32_t attn_args(const mqa_kv_query* q, const mqa_kv_cache* c, bool values, KvA
   a->kv_type = c->type;
   // the running maximum is taken before the scale, which therefore must not be
   // negative: a negative one changes the queries' signs instead
+  // and a zero one, so that -infinity times it stays that, clears the queries
   a->c = std::fabs(scale) * log2e;
+  a->q_keep = a->c > 0.0f ? ~0u : 0u;
+  if (!(a->c > 0.0f)) a->c = 1.0f;
   a->q_flip = std::signbit(scale) ? 0x80008000u : 0u;
   a->score_scale = scale;
   a->v_scale = c->v_scale;

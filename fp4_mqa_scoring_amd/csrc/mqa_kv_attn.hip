@@ -90,13 +90,25 @@ struct Fp16 {
   }
 };
 
+// Maxima by hand: fmaxf quiets either operand first, an instruction each. A NaN gives way to a number here too.
+__device__ __forceinline__ float max2(float x, float y) {
+  float r;
+  __asm__("v_max_f32 %0, %1, %2" : "=v"(r) : "v"(x), "v"(y));
+  return r;
+}
+__device__ __forceinline__ float max3(float x, float y, float z) {
+  float r;
+  __asm__("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(x), "v"(y), "v"(z));
+  return r;
+}
+
 // Maximum / sum over the four lane groups of 16 (lanes l, l ^ 16, l ^ 32, l ^ 48).
 __device__ __forceinline__ float groups_max(float x) {
   const uint32_t b = __float_as_uint(x);
   const auto r = __builtin_amdgcn_permlane32_swap(b, b, false, false);
-  const uint32_t y = __float_as_uint(fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1])));
+  const uint32_t y = __float_as_uint(max2(__uint_as_float(r[0]), __uint_as_float(r[1])));
   const auto s = __builtin_amdgcn_permlane16_swap(y, y, false, false);
-  return fmaxf(__uint_as_float(s[0]), __uint_as_float(s[1]));
+  return max2(__uint_as_float(s[0]), __uint_as_float(s[1]));
 }
 
 __device__ __forceinline__ float groups_sum(float x) {
@@ -181,26 +193,26 @@ struct Wave {
 
   // This lane's part of step c of query tile n: of heads [0, rows) at `p`, one after
   // another, the dims that the keys' pieces hold there.
-  __device__ __forceinline__ v4u query(const char* p, int n, int c, int rows, uint32_t flip) const {
+  __device__ __forceinline__ v4u query(const char* p, int n, int c, int rows, uint32_t keep, uint32_t flip) const {
     const int h = 16 * n + col;
     const int dim = E4M3 ? 64 * (c >> 1) + 16 * grp + 8 * (c & 1) : 32 * c + 8 * grp;
     v4u x = {0, 0, 0, 0};
     if (h < rows) x = *reinterpret_cast<const v4u*>(p + (static_cast<int64_t>(h) * D + dim) * 2);
-    return x ^ v4u{flip, flip, flip, flip};
+    return (x & v4u{keep, keep, keep, keep}) ^ v4u{flip, flip, flip, flip};
   }
 
   // Loads the queries: into registers, or by the whole workgroup into `lds`
   // (NQ * kChunks * 64 of it; a barrier must follow, and one precede).
-  __device__ __forceinline__ void load_q(const char* p, int rows, uint32_t flip, v4u* lds) {
+  __device__ __forceinline__ void load_q(const char* p, int rows, uint32_t keep, uint32_t flip, v4u* lds) {
     if constexpr (kShared) {
       q_lds = lds + lane;
       for (int x = threadIdx.x >> 6; x < NQ * kChunks; x += blockDim.x >> 6)
-        lds[64 * x + lane] = query(p, x / kChunks, x % kChunks, rows, flip);
+        lds[64 * x + lane] = query(p, x / kChunks, x % kChunks, rows, keep, flip);
     } else {
 #pragma unroll
       for (int n = 0; n < NQ; ++n)
 #pragma unroll
-        for (int c = 0; c < kChunks; ++c) q[n][c] = query(p, n, c, rows, flip);
+        for (int c = 0; c < kChunks; ++c) q[n][c] = query(p, n, c, rows, keep, flip);
     }
   }
 
@@ -261,21 +273,26 @@ struct Wave {
     settle(s);
   }
 
+  // The same bits, known only where this stands: what is made of them stays behind the branch around it.
+  static __device__ __forceinline__ uint32_t here(uint32_t inside) {
+    __asm__ __volatile__("" : "+v"(inside));
+    return inside;
+  }
+
   // Scores to weights; `inside` bit j says whether this lane's j-th position counts
   // (looked at where `edge`). Returns the weights packed as the second product's operand.
   __device__ __forceinline__ void weights(v4f (&s)[NQ][kTiles], float c, bool edge, uint32_t inside, P (&p)[NQ]) {
     float top[NQ];
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
-      if (edge) {
+      if (edge) {   // a score of -infinity is a weight of 0, as c > 0
+        const uint32_t in = here(inside);
 #pragma unroll
-        for (int j = 0; j < kMine; ++j)
-          if (!(inside >> j & 1)) s[n][j >> 2][j & 3] = -__builtin_inff();
+        for (int j = 0; j < kMine; ++j) s[n][j >> 2][j & 3] = (in >> j & 1) ? s[n][j >> 2][j & 3] : -__builtin_inff();
       }
-      float x = fmaxf(fmaxf(s[n][0][0], s[n][0][1]), fmaxf(s[n][0][2], s[n][0][3]));
+      float x = max2(max3(s[n][0][0], s[n][0][1], s[n][0][2]), s[n][0][3]);
 #pragma unroll
-      for (int a = 1; a < kTiles; ++a)
-        x = fmaxf(x, fmaxf(fmaxf(s[n][a][0], s[n][a][1]), fmaxf(s[n][a][2], s[n][a][3])));
+      for (int a = 1; a < kTiles; ++a) x = max3(max3(x, s[n][a][0], s[n][a][1]), s[n][a][2], s[n][a][3]);
       top[n] = x;
     }
     bool rise = false;
@@ -302,7 +319,6 @@ struct Wave {
 #pragma unroll
       for (int j = 0; j < kMine; ++j) {
         w[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n][j >> 2][j & 3], c, -ref));
-        if (edge) w[j] = (inside >> j & 1) ? w[j] : 0.0f;
       }
       float sum = (w[0] + w[1]) + (w[2] + w[3]);
       if constexpr (POS == 32) sum += (w[4] + w[5]) + (w[6] + w[7]);
@@ -323,6 +339,7 @@ struct Wave {
 
   // Values outside the window are whatever the cache holds there, NaN perhaps.
   __device__ __forceinline__ void clear_outside(uint32_t inside) {
+    inside = here(inside);
 #pragma unroll
     for (int j = 0; j < kMine; ++j)
 #pragma unroll
@@ -456,6 +473,13 @@ __device__ __forceinline__ void run_tiles(W& w, int t, int t_hi, float c, KEYS&&
 // two waves per SIMD leave.
 constexpr int register_tile(int D, bool e4m3) { return D == 256 && !e4m3 ? 16 : 32; }
 
+// Offset of a slot in units of 16 bytes, of which the strides are multiples. A page's is below 2^36 bytes, 63
+// positions' below 2^31: one 32-bit multiplication and one of 24 bits.
+__device__ __forceinline__ uint64_t slot_offset(int slot, uint32_t page, uint32_t pos) {
+  const uint32_t s = static_cast<uint32_t>(slot);
+  return static_cast<uint64_t>(s >> 6) * page + __umul24(s & 63, pos);
+}
+
 // --- more heads: positions staged in LDS ------------------------------------------
 //
 // Two waves (a half) carry the first heads, two the others; each takes half of a stage
@@ -487,7 +511,8 @@ template <class T, bool E4M3, int D, int NQ>
 struct Ring {
   static constexpr int kParts = 2;
   static constexpr int kPos = D < 256 ? 32 : 16;             // positions of a wave
-  // SLACK 8: the vector unit is what bounds a long list of slots (2,048 rows of 1,024: 136 us, 152 without)
+  // SLACK 8: the vector unit is what bounds a long list of slots (2,048 rows of 1,024: 136 us, 152 without, before
+  // other instructions were saved: now 129)
   typedef Wave<T, E4M3, D, NQ, kPos, false, 8> W;
   static constexpr int kStagePos = kParts * kPos;
   static constexpr int kRow = D * W::kBytes;                 // bytes of one position
@@ -563,23 +588,25 @@ struct Ring {
     }
   }
 
-  // The same of stage i of a list of slots in LDS, filled up to whole stages. Strides
-  // are multiples of 16 bytes, a page's below 2^36: their products take one 32-bit multiplication.
+  // The same of stage i of a list of slots in LDS, filled up to whole stages.
   __device__ __forceinline__ void copy_list(const KvAttnArgs& a, const char* kb, const char* vb, int i, int wave,
                                             int lane, uint32_t list) {
     const uint32_t k_page = static_cast<uint32_t>(a.k_page >> 4), v_page = static_cast<uint32_t>(a.v_page >> 4);
     const uint32_t k_pos = static_cast<uint32_t>(a.k_pos >> 4), v_pos = static_cast<uint32_t>(a.v_pos >> 4);
     int slot[kCopies];
     read_slots(slot, i, wave, lane, list);
+    uint64_t off[kCopies];
 #pragma unroll
     for (int c = 0; c < kCopies; ++c) {
-      const int row = copy_row(wave, c, lane);
-      const uint32_t page = static_cast<uint32_t>(slot[c]) >> 6, pos = static_cast<uint32_t>(slot[c]) & 63;
-      const uint64_t k_off = static_cast<uint64_t>(page) * k_page + pos * k_pos;
-      const uint64_t v_off = static_cast<uint64_t>(page) * v_page + pos * v_pos;
-      copy(i % kStages, 0, wave, c, kb + (k_off << 4) + 16 * source_piece(0, row, lane));
-      copy(i % kStages, 1, wave, c, vb + (v_off << 4) + 16 * source_piece(1, row, lane));
+      off[c] = slot_offset(slot[c], k_page, k_pos);
+      copy(i % kStages, 0, wave, c, kb + (off[c] << 4) + 16 * source_piece(0, copy_row(wave, c, lane), lane));
     }
+    if (k_page != v_page || k_pos != v_pos)
+#pragma unroll
+      for (int c = 0; c < kCopies; ++c) off[c] = slot_offset(slot[c], v_page, v_pos);
+#pragma unroll
+    for (int c = 0; c < kCopies; ++c)
+      copy(i % kStages, 1, wave, c, vb + (off[c] << 4) + 16 * source_piece(1, copy_row(wave, c, lane), lane));
   }
 
   // Keys of positions kPos part + 16 a + col into w.k.
@@ -1007,7 +1034,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv_decode_kernel(KvAttnArgs a) {
     const char* vb = a.v + kvh * a.v_head;
     const int64_t head0 = r * a.H + static_cast<int64_t>(kvh) * a.G;
     w.start();
-    w.load_q(a.q + r * a.q_row + static_cast<int64_t>(kvh) * a.G * D * 2, a.G, a.q_flip, nullptr);
+    w.load_q(a.q + r * a.q_row + static_cast<int64_t>(kvh) * a.G * D * 2, a.G, a.q_keep, a.q_flip, nullptr);
 
     bool bad = false;
     int next = t_lo + wave < t_hi ? table[(t_lo + wave) / kPer] : 0;   // entry of the next tile's page, read early
@@ -1081,7 +1108,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv_decode_staged_kernel(KvAttnArg
     const char* vb = a.v + kvh * a.v_head;
     const int64_t head0 = s.r * a.H + static_cast<int64_t>(kvh) * a.G + first;
     w.start();
-    w.load_q(a.q + s.r * a.q_row + (static_cast<int64_t>(kvh) * a.G + first) * D * 2, rows, a.q_flip, nullptr);
+    w.load_q(a.q + s.r * a.q_row + (static_cast<int64_t>(kvh) * a.G + first) * D * 2, rows, a.q_keep, a.q_flip, nullptr);
     bool bad = false;
     int next = table[p0];   // the entry of the page to be fetched next, read early
     int64_t page = 0;
@@ -1295,16 +1322,11 @@ __global__ void __launch_bounds__(kThreads, 2) kv_selected_kernel(KvAttnArgs a) 
   W w;
   w.init();
   w.start();
-  w.load_q(a.q + p.r * a.q_row + static_cast<int64_t>(p.g) * a.G * D * 2, a.G, a.q_flip, nullptr);
+  w.load_q(a.q + p.r * a.q_row + static_cast<int64_t>(p.g) * a.G * D * 2, a.G, a.q_keep, a.q_flip, nullptr);
   const char* kb = a.k + p.g * a.k_head;
   const char* vb = a.v + p.g * a.v_head;
-  // strides are multiples of 16 bytes, a page's below 2^36: their products take one 32-bit multiplication
   const uint32_t k_page = static_cast<uint32_t>(a.k_page >> 4), v_page = static_cast<uint32_t>(a.v_page >> 4);
   const uint32_t k_pos = static_cast<uint32_t>(a.k_pos >> 4), v_pos = static_cast<uint32_t>(a.v_pos >> 4);
-  auto offset = [](int slot, uint32_t page, uint32_t pos) {
-    const uint32_t s = static_cast<uint32_t>(slot);
-    return (static_cast<uint64_t>(s >> 6) * page + (s & 63) * pos) << 4;
-  };
   bool bad = false;
   for (int64_t b0 = p.from; b0 < p.to; b0 += kKvSelBlock) {
     const int len = static_cast<int>(p.to - b0 < kKvSelBlock ? p.to - b0 : kKvSelBlock);
@@ -1324,11 +1346,12 @@ __global__ void __launch_bounds__(kThreads, 2) kv_selected_kernel(KvAttnArgs a) 
         [&](int t) {
 #pragma unroll
           for (int b = 0; b < W::kTiles; ++b)
-            w.load_k(b, kb + offset(list[min(kTile * t + 16 * b + w.col, len - 1)], k_page, k_pos));
+            w.load_k(b, kb + (slot_offset(list[min(kTile * t + 16 * b + w.col, len - 1)], k_page, k_pos) << 4));
         },
         [&](int t) {
 #pragma unroll
-          for (int j = 0; j < W::kMine; ++j) w.load_v(j, vb + offset(list[min(kTile * t + w.mine(j), len - 1)], v_page, v_pos));
+          for (int j = 0; j < W::kMine; ++j)
+            w.load_v(j, vb + (slot_offset(list[min(kTile * t + w.mine(j), len - 1)], v_page, v_pos) << 4));
         },
         [&](int t, int* lo, int* hi) {
           *lo = 0;
@@ -1363,7 +1386,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv_selected_staged_kernel(KvAttnA
   typename R::W w;
   w.init();
   w.start();
-  w.load_q(a.q + p.r * a.q_row + (static_cast<int64_t>(kvh) * a.G + first) * D * 2, rows, a.q_flip, nullptr);
+  w.load_q(a.q + p.r * a.q_row + (static_cast<int64_t>(kvh) * a.G + first) * D * 2, rows, a.q_keep, a.q_flip, nullptr);
   const char* kb = a.k + kvh * a.k_head;
   const char* vb = a.v + kvh * a.v_head;
   bool bad = false;
@@ -1556,7 +1579,7 @@ __global__ void __launch_bounds__(64 * weight_waves(NQ), D == 256 ? 2 : NQ == 1 
             };
             if (from < last_t) load_keys(from);
             if (W::kShared) __syncthreads();
-            w.load_q(a.q + r * a.q_row + (static_cast<int64_t>(kvh) * a.G + first) * D * 2, rows, 0u, q_lds);
+            w.load_q(a.q + r * a.q_row + (static_cast<int64_t>(kvh) * a.G + first) * D * 2, rows, ~0u, 0u, q_lds);
             float sub[NQ];
             bool counts[NQ];
 #pragma unroll
