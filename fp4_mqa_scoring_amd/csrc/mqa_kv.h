@@ -51,7 +51,7 @@ constexpr int kv_group_rows(int D, int G) { return G < 16 * kv_tiles(D, G) ? G :
 // Workgroups of the decode form: what 256 compute units hold at once (two each, by LDS and registers).
 constexpr int kKvDecodeGroups = 512;
 constexpr int kKvPlanRows = 1024;     // rows up to which every workgroup plans for itself
-constexpr int kKvSelBlock = 1024;     // slots staged at once by the selected form
+constexpr int kKvSelBlock = 1024;     // slots of a list in LDS at once (selected form)
 
 int32_t kv_selected_splits(int64_t Q, int64_t K, int D, int G, int Hkv);
 

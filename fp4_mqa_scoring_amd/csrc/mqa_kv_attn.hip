@@ -20,9 +20,12 @@
 // are t, t + D/16, t + 2 D/16, ...
 //
 // What bounds it: decode reads every key and value once for at most 64 query
-// heads and is bound by memory. The four waves of a workgroup take every fourth
-// 32-position tile; the next tile's keys are loaded into the registers that the
-// first product has just read, its values into those that the second has.
+// heads and is bound by memory (MI355X, whose large copies run at 4.9 TB/s: 64
+// sequences of 32K to 131K positions under 64 heads 5.6 to 5.8 TB/s, 32 of 2K to
+// 16K under 32 heads over 8 key heads 5.2). Lists of slots that rows share are read
+// from the L2 caches (2,048 rows of 1,024 slots, 64 heads: 129 us, 8.3 TB/s and
+// 530 TFLOP/s). Up to 16 heads per key head go through registers, more through LDS,
+// both below with the reasons.
 #include "mqa_fp4_topk.h"
 #include "mqa_kv.h"
 #include "mqa_kv_cache.h"
@@ -511,8 +514,7 @@ template <class T, bool E4M3, int D, int NQ>
 struct Ring {
   static constexpr int kParts = 2;
   static constexpr int kPos = D < 256 ? 32 : 16;             // positions of a wave
-  // SLACK 8: the vector unit is what bounds a long list of slots (2,048 rows of 1,024: 136 us, 152 without, before
-  // other instructions were saved: now 129)
+  // SLACK 8: the vector unit is what a long list of slots waits for most (2,048 rows of 1,024: 130 us, 140 without)
   typedef Wave<T, E4M3, D, NQ, kPos, false, 8> W;
   static constexpr int kStagePos = kParts * kPos;
   static constexpr int kRow = D * W::kBytes;                 // bytes of one position
@@ -917,7 +919,9 @@ __global__ void __launch_bounds__(1024) kv_plan_kernel(KvAttnArgs a) {
 }
 
 // Pages of one (row, head group) are its units of work; a workgroup takes
-// `share` consecutive units of all (row, head group) pairs laid end to end, at least two pages.
+// `share` consecutive units of all (row, head group) pairs laid end to end, at least two pages:
+// every part is joined again (one sequence of 1,500 positions, 8 key heads: 10.3 us with at least one page,
+// 10.4 with two and half the parts, 11.7 with four).
 __device__ __forceinline__ int64_t unit_share(int64_t units, int64_t groups) {
   const int64_t s = (units + groups - 1) / groups;
   return s < 2 ? 2 : s;
@@ -1668,7 +1672,8 @@ void selected_on(const KvAttnArgs& a, hipStream_t st) {
 
 template <class T, bool E4M3, int D, int NQ>
 void weights_on(const KvAttnArgs& a, const float* lse, float* acc, int64_t acc_stride, hipStream_t st) {
-  // as many workgroups as 256 compute units hold: two of eight waves, three of four
+  // as many workgroups as 256 compute units hold: two of eight waves, three of four (32 sequences of 4K to 32K
+  // under 64 heads 44 us; twice as many 50, as every workgroup plans for itself)
   int hg = 1;   // key heads at once
   if (NQ == 1)
     while (hg < weight_waves(NQ) && 2 * hg <= a.Hkv) hg *= 2;
@@ -1730,7 +1735,8 @@ struct WeightsOn {
 }  // namespace
 
 // Splits of the selected form: one workgroup per (row, head group) once they
-// fill the device, else enough splits of at least four tiles each.
+// fill the device, else enough splits of at least four tiles each, one per wave of the register form
+// (16 rows of 512 slots under 64 heads: 12.7 us; at least two tiles each, 13.3).
 int32_t kv_selected_splits(int64_t Q, int64_t K, int D, int G, int Hkv) {
   const int64_t items = Q * Hkv * kv_head_groups(D, G);
   const int64_t room = kKvDecodeGroups;
