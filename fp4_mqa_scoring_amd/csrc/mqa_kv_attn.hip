@@ -1734,16 +1734,26 @@ struct WeightsOn {
 
 }  // namespace
 
-// Splits of the selected form: one workgroup per (row, head group) once they
-// fill the device, else enough splits of at least four tiles each, one per wave of the register form
-// (16 rows of 512 slots under 64 heads: 12.7 us; at least two tiles each, 13.3).
+// Splits of the selected form, a power of two with no more workgroups than the device holds: the least sum of what a
+// row's longest part takes (ns per 32 positions of a workgroup that runs alone, which takes one to four of them at
+// once) and, where there are several parts, the launch that joins them, its trips to memory and the sums' bytes.
+// Measured, us with 1, 2, 4, 8 and 16 splits under 64 heads, D = 128: 1 row of 512 slots 13.5, 13.0, 11.0, -, 11.3; 64
+// rows of 512 14.5, 16.9, 18.2; 64 of 1,024 -, 21.6, 19.5, 23.3; 200 of 1,024 24.8, 33.3; 16 of 2,048 -, -, 18.7, 16.1, 18.3.
 int32_t kv_selected_splits(int64_t Q, int64_t K, int D, int G, int Hkv) {
-  const int64_t items = Q * Hkv * kv_head_groups(D, G);
-  const int64_t room = kKvDecodeGroups;
-  int64_t s = items <= 0 ? 1 : room / items;
-  const int64_t most = (K + 4 * kTilePos - 1) / (4 * kTilePos);
-  if (s > most) s = most;
-  return static_cast<int32_t>(s < 1 ? 1 : s);
+  const int64_t items = Q * Hkv * kv_head_groups(D, G), tiles = (K + kTilePos - 1) / kTilePos;
+  const int64_t at_once = (G > 16 ? 2 : 4) / (D == 256 ? 2 : 1), tile_ns = (G > 16 ? 490 : 310) * (D == 256 ? 3 : 2) / 2;
+  const int64_t join_ns = 2700;
+  const int64_t part_ns = 80 + Q * Hkv * G * D * 4 / 1250;   // 0.8 ns per 1,000 bytes of sums
+  int64_t best = 1, least = tiles * tile_ns;
+  for (int64_t s = 2; s * items <= kKvDecodeGroups && s <= tiles; s *= 2) {
+    const int64_t longest = ((tiles + s - 1) / s + at_once - 1) / at_once * at_once;
+    const int64_t ns = longest * tile_ns + join_ns + s * part_ns;
+    if (ns < least) {
+      least = ns;
+      best = s;
+    }
+  }
+  return static_cast<int32_t>(best);
 }
 
 hipError_t launch_kv_decode(const KvAttnArgs& a, hipStream_t st) {

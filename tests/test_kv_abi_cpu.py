@@ -161,8 +161,10 @@ def test_workspaces_do_not_grow_with_the_capacity_for_ever():
     assert mqa.mqa_kv_evict_workspace_bytes(1000, 16384) == 0
     size = mqa.mqa_kv_evict_workspace_bytes(3, 1 << 21)
     assert size == mqa.mqa_kv_evict_workspace_bytes(3, (1 << 31) - 513) == 256 + 3 * 256 * 3 * 2048 * 4
-    assert mqa.mqa_kv_attention_selected_workspace_bytes(1, 1 << 16, 8, 2, 128) == \
-        mqa.mqa_kv_attention_selected_workspace_bytes(1, (1 << 31) - 1, 8, 2, 128)
+    for K in range(6, 32):      # at most 512 parts of each head's sums, maximum and sum
+        for rows in (1, 3, 100, 511, 512, 5000):
+            size = mqa.mqa_kv_attention_selected_workspace_bytes(rows, (1 << K) - 1, 8, 2, 128)
+            assert 0 <= size <= 512 * 4 * (128 + 2) * 4 + 512
 
 
 def test_eviction_is_checked_on_the_host(lib):
