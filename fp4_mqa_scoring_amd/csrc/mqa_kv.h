@@ -35,6 +35,7 @@ struct KvAttnArgs {
   const int32_t *slots, *count;
   int64_t K;
   int32_t splits;
+  uint32_t join_cost;        // of one more part, in pages (16 bits behind the point; decode)
   // workspace
   int64_t* prefix;           // [Q + 1] window pages of the rows before each row (decode)
   float* part_o;             // [slots of partial sums, heads, D]

@@ -918,13 +918,16 @@ __global__ void __launch_bounds__(1024) kv_plan_kernel(KvAttnArgs a) {
   if (threadIdx.x == 0) a.prefix[a.Q] = base;
 }
 
-// Pages of one (row, head group) are its units of work; a workgroup takes
-// `share` consecutive units of all (row, head group) pairs laid end to end, at least two pages:
-// every part is joined again (one sequence of 1,500 positions, 8 key heads: 10.3 us with at least one page,
-// 10.4 with two and half the parts, 11.7 with four).
-__device__ __forceinline__ int64_t unit_share(int64_t units, int64_t groups) {
-  const int64_t s = (units + groups - 1) / groups;
-  return s < 2 ? 2 : s;
+// Pages of one (row, head group) are its units of work; a workgroup takes a share of consecutive units of all
+// (row, head group) pairs laid end to end: an equal one, or where that would make many short parts the power of two
+// nearest to sqrt(units * join_cost), at which the parts and their joining take the least together (decode_on() has the
+// figures). In whole numbers: the launches of one call must agree on it.
+__device__ __forceinline__ int64_t unit_share(const KvAttnArgs& a, int64_t units, int64_t groups) {
+  const int64_t equal = (units + groups - 1) / groups;
+  const uint32_t some = static_cast<uint32_t>(units < 1 << 24 ? units : 1 << 24);
+  const uint32_t x = static_cast<uint32_t>(static_cast<uint64_t>(some) * a.join_cost >> 16);   // below 2^23
+  const int64_t s = x < 2 ? 1 : 1 << ((32 - __builtin_clz(x - 1)) >> 1);   // the least with 2 s^2 >= x
+  return equal > s ? equal : s;
 }
 
 // Integers that no kernel of this launch writes, read through the scalar cache.
@@ -1019,7 +1022,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv_decode_kernel(KvAttnArgs a) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t* prefix = plan.make(a);
   const int64_t units = prefix[a.Q] * a.Hkv;
-  const int64_t share = unit_share(units, gridDim.x);
+  const int64_t share = unit_share(a, units, gridDim.x);
   int64_t cur = blockIdx.x * share;
   const int64_t stop = cur + share < units ? cur + share : units;
   W w;
@@ -1090,7 +1093,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv_decode_staged_kernel(KvAttnArg
   const int qg = (a.G + kHeads - 1) / kHeads;
   const int64_t gh = static_cast<int64_t>(a.Hkv) * qg;
   const int64_t units = prefix[a.Q] * gh;
-  const int64_t share = unit_share(units, gridDim.x);
+  const int64_t share = unit_share(a, units, gridDim.x);
   int64_t cur = blockIdx.x * share;
   const int64_t stop = cur + share < units ? cur + share : units;
   const int group_rows = a.G < kHeads ? a.G : kHeads;
@@ -1259,7 +1262,7 @@ __global__ void __launch_bounds__(kThreads) kv_decode_join_kernel(KvAttnArgs a, 
   }
   const int qg = (a.G + per - 1) / per;
   const int64_t gh = static_cast<int64_t>(a.Hkv) * qg;
-  const int64_t share = unit_share(all * gh, groups);
+  const int64_t share = unit_share(a, all * gh, groups);
   const int kvh = h / a.G, in_kv = h - kvh * a.G;
   const int64_t from = before * gh + (static_cast<int64_t>(kvh) * qg + in_kv / per) * n;
   const int64_t w0 = from / share, w1 = (from + n - 1) / share;
@@ -1645,9 +1648,17 @@ __global__ void __launch_bounds__(64 * weight_waves(NQ), D == 256 ? 2 : NQ == 1 
 // few parts each and a wave does.
 constexpr int64_t kJoinHeads = 512;
 
+// Device us with shares of at least 1, 2, 4 and 8 pages, D = 128. 64 heads over 1 key head, 1 row: 512 positions 11.8, 12.8,
+// 15.0, 17.8; 8,192 16.8, 14.9, 15.6, 19.7; 32,768 37.2, 24.6, 20.3, 21.7; 131,072 -, -, 40.2, 31.0; 16 rows of 2,048 26.6,
+// 20.3, 18.8, 21.0. 32 over 8, 1 row: 64 7.9, 10.6, 16.2, 27.0; 2,048 9.8, 10.0, 11.3, 13.8; 8,192 13.9, 13.9, 13.0, 16.2.
 template <class T, bool E4M3, int D, int TILES>
-void decode_on(const KvAttnArgs& a, hipStream_t st) {
+void decode_on(KvAttnArgs a, hipStream_t st) {
   const int groups = kKvDecodeGroups;
+  // what one more part costs (its sums' bytes, its turn in the joining of its heads) by what a page takes, both in ns
+  const double page_ns = TILES > 1 ? (D == 256 ? 1600 : 1000) : 100 + 2.75 * D;
+  const double sums_ns = kv_group_rows(D, a.G) * D * 4 * 0.8e-3, turn_ns = a.Q * a.H <= kJoinHeads ? 20 : 80;
+  const double pairs = static_cast<double>(a.Q) * a.Hkv * kv_head_groups(D, a.G);
+  a.join_cost = static_cast<uint32_t>((sums_ns + turn_ns / pairs) / page_ns * 65536.0);
   if (a.Q > kKvPlanRows) kv_plan_kernel<<<dim3(1), dim3(1024), 0, st>>>(a);
   if constexpr (TILES == 1) kv_decode_kernel<T, E4M3, D><<<dim3(groups), dim3(kThreads), 0, st>>>(a);
   else kv_decode_staged_kernel<T, E4M3, D, TILES / 2><<<dim3(groups), dim3(kThreads), 0, st>>>(a);
