@@ -21,7 +21,7 @@ MQA_OK = 0
 ERRORS = {
     -1: "MQA_ERR_UNSUPPORTED_K", -2: "MQA_ERR_NULL_POINTER", -3: "MQA_ERR_MISALIGNED",
     -4: "MQA_ERR_BAD_SIZE", -5: "MQA_ERR_DEVICE", -6: "MQA_ERR_CAPTURING", -7: "MQA_ERR_HIP",
-    -8: "MQA_ERR_BAD_FLAGS", -9: "MQA_ERR_UNSUPPORTED",
+    -8: "MQA_ERR_BAD_FLAGS", -9: "MQA_ERR_UNSUPPORTED", -10: "MQA_ERR_OVERLAP",
 }
 ROW_BAD_WINDOW, ROW_BAD_PAGE, ROW_UNDERFILL, ROW_SELECTOR = -1, -2, -3, -4
 STATUS_BAD_WINDOW, STATUS_BAD_PAGE, STATUS_UNDERFILL, STATUS_SELECTOR = 1, 2, 4, 8
@@ -605,7 +605,7 @@ def mqa_kv_evict_select(acc, seq_len, budget, recent, keep, kept, workspace=None
     """Chooses what a budget keeps of every sequence: its last `recent` positions and the budget - recent
     earlier ones with the largest acc (float32 [n_seq, max_len]; seq_len int32 [n_seq]). Fills keep int32
     [n_seq, budget] (rising, padded with -1), kept int32 [n_seq] and, if given, kept_acc float32 [n_seq,
-    budget]. workspace: at least mqa_kv_evict_workspace_bytes(n_seq, max_len) bytes. Capturable."""
+    budget]; kept may be seq_len itself, nothing else may overlap. workspace: at least mqa_kv_evict_workspace_bytes(n_seq, max_len) bytes. Capturable."""
     torch = _kv()[0]
     if not isinstance(seq_len, torch.Tensor) or seq_len.dim() != 1:
         raise TypeError("seq_len must be a tensor of one dimension")

@@ -556,6 +556,7 @@ const char* mqa_fp4_error_string(int32_t code) {
     case MQA_ERR_HIP: return "HIP runtime error";
     case MQA_ERR_BAD_FLAGS: return "unknown flag bits";
     case MQA_ERR_UNSUPPORTED: return "unsupported type or head dimension";
+    case MQA_ERR_OVERLAP: return "an output overlaps another tensor of the call";
     default: return "unknown error";
   }
 }

@@ -119,6 +119,35 @@ inline int32_t check_ptrs_device(const PtrSpec* specs, int n, int dev) {
   return MQA_OK;
 }
 
+// Memory that a call reads or writes: `rows` pieces of `bytes` bytes at a byte stride.
+struct Span {
+  const void* p;
+  int64_t rows, stride, bytes;
+};
+
+// Whether two spans share a byte. Two of several rows each and different strides count as apart.
+inline bool overlap(const Span& a, const Span& b) {
+  if (a.p == nullptr || b.p == nullptr || a.rows < 1 || b.rows < 1 || a.bytes < 1 || b.bytes < 1) return false;
+  if (a.rows > 1 && b.rows > 1 && a.stride != b.stride) return false;
+  const __int128 d = static_cast<__int128>(reinterpret_cast<uintptr_t>(b.p)) - reinterpret_cast<uintptr_t>(a.p);
+  const __int128 s = a.rows > 1 ? a.stride : b.rows > 1 ? b.stride : 0;
+  // row j of b begins k = j - i strides and d bytes behind row i of a: is -b.bytes < d + k s < a.bytes for any k?
+  __int128 k = 1 - static_cast<__int128>(a.rows);
+  if (s > 0 && d + k * s <= -static_cast<__int128>(b.bytes)) k += (-b.bytes - (d + k * s)) / s + 1;   // the first above -b.bytes
+  return k < b.rows && d + k * s > -static_cast<__int128>(b.bytes) && d + k * s < a.bytes;
+}
+
+// No output may overlap an input or an output behind it.
+inline int32_t check_apart(const Span* outs, int n_outs, const Span* ins, int n_ins) {
+  for (int i = 0; i < n_outs; ++i) {
+    for (int j = i + 1; j < n_outs; ++j)
+      if (overlap(outs[i], outs[j])) return MQA_ERR_OVERLAP;
+    for (int j = 0; j < n_ins; ++j)
+      if (overlap(outs[i], ins[j])) return MQA_ERR_OVERLAP;
+  }
+  return MQA_OK;
+}
+
 inline int32_t check_capture(hipStream_t st) {
   hipStreamCaptureStatus cs = hipStreamCaptureStatusNone;
   if (hipStreamIsCapturing(st, &cs) != hipSuccess) {

@@ -73,7 +73,7 @@ struct KvEvictArgs {
   int32_t* status;
   // workspace of long sequences
   uint32_t* counts;   // [n_seq, chunks, 3, 2048] counts of each chunk's digits
-  uint32_t* state;    // [n_seq, 4]
+  uint32_t* state;    // [n_seq, 8] prefix and need behind the first two digits, and the length
 };
 // Sequences of up to 16,384 positions (the capacity's bound, as the host knows no lengths) take one
 // workgroup; longer ones one per chunk, of which there are at most 256.

@@ -244,7 +244,7 @@ int64_t mqa_kv_evict_workspace_bytes(int64_t num_seqs, int64_t max_len) {
   if (num_seqs < 0 || max_len < 0 || max_len > 0x7FFFFFFFll - 512) return MQA_ERR_BAD_SIZE;
   const int64_t chunks = mqa::kv_evict_chunks(max_len);
   if (num_seqs > kMaxItems / 4 / chunks) return MQA_ERR_BAD_SIZE;
-  return chunks == 1 ? 0 : align_up(num_seqs * 4 * 4) + align_up(num_seqs * chunks * 3 * 2048 * 4);
+  return chunks == 1 ? 0 : align_up(num_seqs * 8 * 4) + align_up(num_seqs * chunks * 3 * 2048 * 4);
 }
 
 int32_t mqa_kv_evict_select(const float* acc, int64_t acc_stride, const int32_t* seq_len, int64_t num_seqs,
@@ -260,16 +260,26 @@ int32_t mqa_kv_evict_select(const float* acc, int64_t acc_stride, const int32_t*
       {acc, rows && max_len > 0, 4}, {seq_len, rows, 4},  {keep, rows && budget > 0, 4},
       {kept, rows, 4},               {kept_acc, false, 4}, {workspace, rows && need > 0, 256},
   };
+  int32_t rc = check_ptrs_host(specs, sizeof(specs) / sizeof(specs[0]));
+  if (rc != MQA_OK) return rc;
+  const Span outs[] = {{keep, 1, 0, num_seqs * budget * 4},
+                       {kept, 1, 0, num_seqs * 4},
+                       {kept_acc, 1, 0, num_seqs * budget * 4},
+                       {workspace, 1, 0, need}};
+  // the kernels read every length before its kept is written, so that kept may take the lengths' place
+  const Span ins[] = {{acc, num_seqs, acc_stride * 4, max_len * 4}, {kept == seq_len ? nullptr : seq_len, 1, 0, num_seqs * 4}};
+  rc = check_apart(outs, 4, ins, 2);
+  if (rc != MQA_OK) return rc;
   const hipStream_t st = static_cast<hipStream_t>(stream);
   DeviceGuard guard;
   DeviceInfo info;
-  int32_t rc = enter(st, specs, sizeof(specs) / sizeof(specs[0]), guard, &info, /*allow_capture=*/true);
+  rc = enter(st, specs, sizeof(specs) / sizeof(specs[0]), guard, &info, /*allow_capture=*/true);
   if (rc != MQA_OK || !rows) return rc;
   mqa::KvEvictArgs a{acc, acc_stride, seq_len, num_seqs, max_len, budget, recent, keep, kept, kept_acc,
                      mqa::status_word(), nullptr, nullptr};
   if (a.status == nullptr) return MQA_ERR_HIP;
   a.state = static_cast<uint32_t*>(workspace);
-  a.counts = reinterpret_cast<uint32_t*>(static_cast<char*>(workspace) + align_up(num_seqs * 4 * 4));
+  a.counts = reinterpret_cast<uint32_t*>(static_cast<char*>(workspace) + align_up(num_seqs * 8 * 4));
   return hip_rc(mqa::launch_kv_evict_select(a, st));
 }
 

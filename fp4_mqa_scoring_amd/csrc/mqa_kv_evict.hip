@@ -181,11 +181,12 @@ struct SelectRow {
   bool bad;
   int old, m;   // positions that compete, and how many of them are kept
 
-  __device__ __forceinline__ SelectRow(const KvEvictArgs& a, int64_t s) {
+  // seq_len: of the sequence. What reads it in memory that is also a.kept does so before write_rest() writes there.
+  __device__ __forceinline__ SelectRow(const KvEvictArgs& a, int64_t s, int32_t seq_len) {
     acc = a.acc + s * a.acc_stride;
     keep = a.keep + s * a.budget;
     kept_acc = a.kept_acc == nullptr ? nullptr : a.kept_acc + s * a.budget;
-    len = a.seq_len[s];
+    len = seq_len;
     bad = len < 0 || len > a.max_len;
     n_kept = bad ? 0 : len < a.budget ? len : a.budget;
     old = static_cast<int>(n_kept == 0 ? 0 : len <= a.budget ? len : len - a.recent);
@@ -213,7 +214,8 @@ struct SelectRow {
 __global__ void __launch_bounds__(kSelThreads) kv_evict_select_kernel(KvEvictArgs a) {
   __shared__ __align__(16) SelectMemory lds;
   const int64_t s = blockIdx.x;
-  const SelectRow row(a, s);
+  const SelectRow row(a, s, a.seq_len[s]);
+  __syncthreads();   // every wave has read the length
   row.write_rest(a, s, threadIdx.x, kSelThreads);
   if (row.old == 0) return;
   if (row.old <= 4 * kSelThreads) select_old<4>(row.acc, row.keep, row.kept_acc, row.old, row.m, lds);
@@ -311,14 +313,17 @@ __device__ __forceinline__ void chunk_digit(const uint32_t* counts, int chunks, 
   *need = lds.need;
 }
 
-// Counts one digit of a chunk's keys whose upper digits are the m-th key's. state[s * 4 + 2 d, + 1]:
-// prefix and need behind digit d (d < 2).
+// Counts one digit of a chunk's keys whose upper digits are the m-th key's. state[s * 8 + 2 d, + 1]:
+// prefix and need behind digit d (d < 2); state[s * 8 + 4]: the length, for the last launch, in which
+// kept is written and may lie over the lengths.
 template <bool LONG>
 __global__ void __launch_bounds__(kSelThreads) kv_evict_count_kernel(KvEvictArgs a, int chunks, int stage) {
   __shared__ __align__(16) ChunkMemory lds;
   const int64_t s = blockIdx.x / chunks;
   const int c = static_cast<int>(blockIdx.x - s * chunks);
-  const SelectRow row(a, s);
+  const SelectRow row(a, s, a.seq_len[s]);
+  uint32_t* state = a.state + 8 * s;
+  if (stage == 0 && c == 0 && threadIdx.x == 0) state[4] = static_cast<uint32_t>(row.len);
   if (row.m == 0 || row.m == row.old) return;
   const Chunks<LONG> of(row.old);
   if (c >= of.n) return;
@@ -326,7 +331,6 @@ __global__ void __launch_bounds__(kSelThreads) kv_evict_count_kernel(KvEvictArgs
   Piece x;
   x.load(row, of.first(c));
   uint32_t* counts = a.counts + s * chunks * 3 * kDigitBins;
-  uint32_t* state = a.state + 4 * s;
   uint32_t prefix = 0, need = static_cast<uint32_t>(row.m);
   if (stage > 0) {
     if (stage == 2) {
@@ -371,7 +375,7 @@ __global__ void __launch_bounds__(kSelThreads) kv_evict_write_kernel(KvEvictArgs
   __shared__ __align__(16) ChunkMemory lds;
   const int64_t s = blockIdx.x / chunks;
   const int c = static_cast<int>(blockIdx.x - s * chunks);
-  const SelectRow row(a, s);
+  const SelectRow row(a, s, static_cast<int32_t>(a.state[8 * s + 4]));
   row.write_rest(a, s, c * kSelThreads + threadIdx.x, static_cast<int64_t>(chunks) * kSelThreads);
   if (row.m == 0) return;
   const Chunks<LONG> of(row.old);
@@ -384,8 +388,8 @@ __global__ void __launch_bounds__(kSelThreads) kv_evict_write_kernel(KvEvictArgs
   int aboves = of.first(c), equals = 0;   // positions before the piece above the m-th key (every one where all are kept), equal to it
   if (!all) {
     const uint32_t* counts = a.counts + s * chunks * 3 * kDigitBins;
-    prefix = a.state[4 * s + 2];
-    need = a.state[4 * s + 3];
+    prefix = a.state[8 * s + 2];
+    need = a.state[8 * s + 3];
     chunk_digit(counts, of.n, 2, lds, &prefix, &need);
     // keys above the m-th one in earlier chunks: by the digit at which they differ
     uint32_t above = 0, equal = 0;

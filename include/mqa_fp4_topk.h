@@ -85,6 +85,7 @@ extern "C" {
 #define MQA_ERR_HIP (-7)             /* a HIP runtime call failed (allocation, launch) */
 #define MQA_ERR_BAD_FLAGS (-8)       /* unknown bits in flags */
 #define MQA_ERR_UNSUPPORTED (-9)     /* a type or head dimension without a kernel (mqa_kv_cache.h) */
+#define MQA_ERR_OVERLAP (-10)        /* an output overlaps another tensor of the call (mqa_kv_cache.h) */
 
 /* ---- per-row codes in out_count -------------------------------------------- */
 #define MQA_ROW_BAD_WINDOW (-1)      /* start < 0, end < start or end > 64 * P_log */

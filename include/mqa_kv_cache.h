@@ -158,7 +158,8 @@ int32_t mqa_kv_weights_accumulate(const mqa_kv_query* q, const float* lse, const
  *   kept     int32 [num_seqs]           how many
  *   kept_acc float [num_seqs, budget]   optional: their acc, padded with 0 (the
  *            sums to go on with after mqa_kv_compact)
- * kept_acc must not overlap acc.
+ * kept may be seq_len itself: the new lengths take the old ones' place. Any other overlap of keep, kept,
+ * kept_acc or the workspace with each other, acc or seq_len is refused (MQA_ERR_OVERLAP).
  * workspace: mqa_kv_evict_workspace_bytes() bytes, 256-byte aligned: 0 (and the
  * workspace then NULL) up to a max_len of 16,384, at most 6.3 MB per sequence.
  * num_seqs: at most 16,383 whatever max_len is, 4,194,240 up to a max_len of 16,384.
