@@ -528,8 +528,8 @@ def mqa_kv_attention_decode(q, k_pages, v_pages, block_table, seq_of_row, row_st
                             lse=None, scale=None, k_scale=1.0, v_scale=1.0, stream=None):
     """Attention of new tokens over a paged key-value cache: q [Q, H, D] (bfloat16 or float16; the row
     stride is free), k_pages and v_pages [P, 64, Hkv, D] of q's type or float8_e4m3fn (page, position and
-    head strides are free), windows and block table as in mqa_fp4_topk_decode, out [Q, H, D], lse float32
-    [Q, H] or None, scale 1/sqrt(D) if None, workspace uint8 of at least
+    head strides are free), windows and block table as in mqa_fp4_topk_decode, out [Q, H, D] (a contiguous q
+    itself, or apart from it), lse float32 [Q, H] or None, scale 1/sqrt(D) if None, workspace uint8 of at least
     mqa_kv_attention_decode_workspace_bytes(Q, H, Hkv, D) bytes. Allocates nothing on the device and does
     not synchronise (capturable)."""
     query, shape = _kv_query(q, scale)

@@ -123,6 +123,13 @@ inline int32_t check_ptrs_device(const PtrSpec* specs, int n, int dev) {
 struct Span {
   const void* p;
   int64_t rows, stride, bytes;
+
+  Span(const void* p_, int64_t rows_, int64_t stride_, int64_t bytes_) : p(p_), rows(rows_), stride(stride_), bytes(bytes_) {
+    if (rows > 1 && stride <= bytes) {   // one piece
+      bytes += (rows - 1) * stride;
+      rows = 1;
+    }
+  }
 };
 
 // Whether two spans share a byte. Two of several rows each and different strides count as apart.

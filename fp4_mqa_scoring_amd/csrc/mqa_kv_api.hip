@@ -127,6 +127,19 @@ PartialLayout selected_layout(int64_t Q, int32_t D, int32_t G, int32_t Hkv, int3
   return partial_layout(0, splits > 1 ? Q * Hkv * mqa::kv_head_groups(D, G) * splits : 0, D, mqa::kv_group_rows(D, G));
 }
 
+// The outputs of an attention lie apart from each other and from what it reads besides the cache, but for out in
+// the queries' place: a workgroup that writes a head's row is the only one that reads it, or its launch comes later.
+int32_t check_attn_apart(const KvAttnArgs& a, const void* out, const float* lse, const void* workspace, int64_t bytes,
+                         const Span* ints, int n_ints) {
+  const int64_t row = static_cast<int64_t>(a.H) * a.D * 2;
+  const Span outs[] = {{out, 1, 0, a.Q * row}, {lse, 1, 0, a.Q * a.H * 4}, {workspace, 1, 0, bytes}};
+  const bool in_place = out == a.q && (a.Q <= 1 || a.q_row == row);
+  const Span q = {a.q, a.Q, a.q_row, row};
+  int32_t rc = check_apart(outs, 3, ints, n_ints);
+  if (rc == MQA_OK) rc = check_apart(outs + (in_place ? 1 : 0), in_place ? 2 : 3, &q, 1);
+  return rc;
+}
+
 void place(KvAttnArgs* a, const PartialLayout& l, void* workspace) {
   char* base = static_cast<char*>(workspace);
   a->prefix = reinterpret_cast<int64_t*>(base + l.prefix);
@@ -161,6 +174,12 @@ int32_t mqa_kv_attention_decode(const mqa_kv_query* q, const mqa_kv_cache* cache
       {seq_of_row, rows, 4},  {row_start, rows, 4}, {row_end, rows, 4}, {out, rows, 16},
       {lse, false, 4},        {workspace, rows, 256},
   };
+  rc = check_ptrs_host(specs, sizeof(specs) / sizeof(specs[0]));
+  if (rc != MQA_OK) return rc;
+  const Span ints[] = {{block_table, 1, 0, num_seqs * max_pages * 4}, {seq_of_row, 1, 0, a.Q * 4},
+                       {row_start, 1, 0, a.Q * 4}, {row_end, 1, 0, a.Q * 4}};
+  rc = check_attn_apart(a, out, lse, workspace, lay.total, ints, 4);
+  if (rc != MQA_OK) return rc;
   const hipStream_t st = static_cast<hipStream_t>(stream);
   DeviceGuard guard;
   DeviceInfo info;
@@ -199,6 +218,11 @@ int32_t mqa_kv_attention_selected(const mqa_kv_query* q, const mqa_kv_cache* cac
       {a.q, rows, 16},  {a.k, pages, 16},  {a.v, pages, 16},    {slots, rows && K > 0, 4},
       {count, rows, 4}, {out, rows, 16},   {lse, false, 4},     {workspace, rows && lay.total > 0, 256},
   };
+  rc = check_ptrs_host(specs, sizeof(specs) / sizeof(specs[0]));
+  if (rc != MQA_OK) return rc;
+  const Span ints[] = {{slots, 1, 0, a.Q * K * 4}, {count, 1, 0, a.Q * 4}};
+  rc = check_attn_apart(a, out, lse, workspace, lay.total, ints, 2);
+  if (rc != MQA_OK) return rc;
   const hipStream_t st = static_cast<hipStream_t>(stream);
   DeviceGuard guard;
   DeviceInfo info;
@@ -229,6 +253,14 @@ int32_t mqa_kv_weights_accumulate(const mqa_kv_query* q, const float* lse, const
       {a.q, rows, 16},        {lse, rows, 4},       {a.k, pages, 16},   {block_table, sums, 4},
       {seq_of_row, rows, 4},  {row_start, rows, 4}, {row_end, rows, 4}, {acc, sums, 4},
   };
+  rc = check_ptrs_host(specs, sizeof(specs) / sizeof(specs[0]));
+  if (rc != MQA_OK) return rc;
+  const Span out = {acc, num_seqs, acc_stride * 4, 64 * max_pages * 4};
+  const Span ins[] = {{a.q, a.Q, a.q_row, static_cast<int64_t>(a.H) * a.D * 2}, {lse, 1, 0, a.Q * a.H * 4},
+                      {block_table, 1, 0, num_seqs * max_pages * 4}, {seq_of_row, 1, 0, a.Q * 4},
+                      {row_start, 1, 0, a.Q * 4}, {row_end, 1, 0, a.Q * 4}};
+  rc = check_apart(&out, 1, ins, 6);
+  if (rc != MQA_OK) return rc;
   const hipStream_t st = static_cast<hipStream_t>(stream);
   DeviceGuard guard;
   DeviceInfo info;

@@ -14,6 +14,11 @@
  * stream, or replays of graphs that do not overlap); a workspace needs no
  * initialisation and holds nothing from one call to the next.
  *
+ * Outputs and workspaces must not overlap each other or anything that the call
+ * reads. Two may take an input's place: an attention's out its queries' (where
+ * those lie contiguous), and an eviction's kept the lengths. Overlaps with
+ * tensors other than caches and paged arrays are refused with MQA_ERR_OVERLAP.
+ *
  * The cache. Keys and values are tensors [P_phys, 64, Hkv, D] given by a base
  * pointer and the strides, in ELEMENTS, of page, position and head; the D
  * elements of one head are contiguous. So [P, 64, Hkv, D] and [P, Hkv, 64, D]
