@@ -55,7 +55,11 @@ constexpr int kWaves = 4;
 constexpr int kTilePos = 32;
 constexpr float kLn2 = 0.69314718055994530942f;
 
+// kTop: the largest weight is kept at 2^kTop. bf16's range is that of 32 bits, so 1 will do. fp16's normal numbers
+// end at 2^-14, and where one position outweighs many others the weights of these, which count together, would be lost to
+// its subnormal ones (4,096 of 2^-24.7 each: outputs wrong by 13 %); below 2^15 they lie at 2^-29 and less.
 struct Bf16 {
+  static constexpr int kTop = 0;
   static __device__ __forceinline__ v4f mfma(v4u a, v4u b, v4f c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c,
                                                    0, 0, 0);
@@ -75,6 +79,7 @@ struct Bf16 {
 };
 
 struct Fp16 {
+  static constexpr int kTop = 15;
   static __device__ __forceinline__ v4f mfma(v4u a, v4u b, v4f c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0,
                                                   0, 0);
@@ -122,6 +127,15 @@ __device__ __forceinline__ float groups_sum(float x) {
   return __uint_as_float(s[0]) + __uint_as_float(s[1]);
 }
 
+// log of a sum of weights held under the running maximum m (log2 domain, 2^kTop at the top): the
+// parts that make up for each other are taken out first, which is exact.
+template <class T>
+__device__ __forceinline__ float lse_of(float m, float sum) {
+  if constexpr (T::kTop == 0) return (m + __builtin_amdgcn_logf(sum)) * kLn2;
+  constexpr float kBy = 1.0f / (1 << T::kTop);
+  return ((m + static_cast<float>(T::kTop)) + __builtin_amdgcn_logf(sum * kBy)) * kLn2;
+}
+
 // Passes matrix results on once they can be read, which a 16x16x32 product's can after
 // eight wait states. Ordinary code waits for them by itself, but behind a branch that
 // overwrites a part of them under a mask (the edge of a window) this compiler has left out
@@ -148,8 +162,8 @@ __device__ __forceinline__ void settle(v4f (&s)[N][2]) {
 // The registers and steps of one wave: NQ tiles of 16 query heads of one row and
 // key head, POS (16 or 32) positions at a time.
 //
-// The running maximum moves when it is passed by more than SLACK (log2 domain). 0: the
-// largest weight is exactly 1, which the rounding of the weights to 16 bits leaves alone, and
+// The running maximum m is the largest score seen less kBias (log2 domain), so that the largest weight is 2^kTop at most,
+// and moves when it is passed by more than SLACK. 0: the largest weight is a power of two (to 2^-20), which the rounding of the weights to 16 bits leaves alone, and
 // where few weights count that is most of the rounding's error (relative error of the output 0.0018,
 // of its own rounding alone 0.0017, with SLACK 8 0.0022). 8: weights up to 2^8, whose relative rounding is the
 // same, and the sums are multiplied once or twice instead of in nearly every one of the first tiles.
@@ -164,6 +178,7 @@ struct Wave {
   static constexpr int kTiles = POS / 16;                // matrix tiles of positions
   static constexpr int kMine = POS / 4;                  // positions whose weights and values this lane holds
   static constexpr bool kShared = QL;                    // the queries lie in LDS
+  static constexpr int kBias = T::kTop == 0 ? 0 : T::kTop - SLACK;
   typedef typename Pick<POS == 32, v4u, v2u>::type P;    // weights of kMine positions, packed
 
   v4u q[kShared ? 1 : NQ][kShared ? 1 : kChunks];
@@ -301,7 +316,7 @@ struct Wave {
     bool rise = false;
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
-      top[n] = groups_max(top[n]) * c;
+      top[n] = kBias == 0 ? groups_max(top[n]) * c : __builtin_fmaf(groups_max(top[n]), c, static_cast<float>(-kBias));
       rise |= top[n] > m[n] + static_cast<float>(SLACK);
     }
     if (__any(rise)) {
@@ -433,7 +448,7 @@ struct Merge {
           const float inv = v_scale / e2.y;
           const v2u y = {T::pack(sum[0] * inv, sum[1] * inv), T::pack(sum[2] * inv, sum[3] * inv)};
           *reinterpret_cast<v2u*>(out + (static_cast<int64_t>(head) * D + d) * 2) = y;
-          if (d == 0 && lse != nullptr) lse[head] = (e2.x + __builtin_amdgcn_logf(e2.y)) * kLn2;
+          if (d == 0 && lse != nullptr) lse[head] = lse_of<T>(e2.x, e2.y);
         }
       }
     }
@@ -823,7 +838,7 @@ struct Ring {
       } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) store_dims<T>(reinterpret_cast<uint16_t*>(out) + at + i * W::kDims, got, i, inv);
-        if (w.grp == 0 && t0 == 0 && lse != nullptr) lse[head] = (my_top + __builtin_amdgcn_logf(my_sum)) * kLn2;
+        if (w.grp == 0 && t0 == 0 && lse != nullptr) lse[head] = lse_of<T>(my_top, my_sum);
       }
     }
     __syncthreads();   // the stages may be filled again
@@ -1236,7 +1251,7 @@ __device__ __forceinline__ void join_row(const KvAttnArgs& a, int64_t head, int 
     for (int e = 0; e < kPer; e += 2)
       *reinterpret_cast<uint32_t*>(out + e) = T::pack(acc[e] * inv, acc[e + 1] * inv);
   }
-  if (lane == 0 && a.lse != nullptr) a.lse[head] = (m + __builtin_amdgcn_logf(sum)) * kLn2;
+  if (lane == 0 && a.lse != nullptr) a.lse[head] = lse_of<T>(m, sum);
 }
 
 // Head of a join launch: one per workgroup, or (WAVES 1) one per wave; -1 behind the last.
