@@ -31,9 +31,11 @@ int32_t check_heads(int64_t num_rows, int32_t H, int32_t Hkv, int32_t D) {
   return MQA_OK;
 }
 
-// Strides of one tensor of the cache, checked and in bytes.
-int32_t cache_strides(const int64_t* stride, const mqa_kv_cache& c, int64_t* page, int64_t* pos, int64_t* head) {
+// Strides of one tensor of the cache, checked and in bytes. Those of one page or one head are never taken, and
+// may be anything (as torch's are): 0 in their place.
+int32_t cache_strides(const int64_t* strides, const mqa_kv_cache& c, int64_t* page, int64_t* pos, int64_t* head) {
   const int64_t bytes = element_bytes(c.type), D = c.head_dim;
+  const int64_t stride[3] = {c.num_phys_pages > 1 ? strides[0] : 0, strides[1], c.num_kv_heads > 1 ? strides[2] : 0};
   for (int i = 0; i < 3; ++i) {
     if (stride[i] < 0 || stride[i] >= (1ll << 35)) return MQA_ERR_BAD_SIZE;
     if (stride[i] * bytes % 16) return MQA_ERR_MISALIGNED;
@@ -344,20 +346,23 @@ int32_t mqa_kv_compact(const int32_t* keep, const int32_t* kept, int64_t num_seq
     bool wide = x.row_bytes % 16 == 0 && reinterpret_cast<uintptr_t>(x.src) % 16 == 0 &&
                 reinterpret_cast<uintptr_t>(x.dst) % 16 == 0;
     if (x.row_bytes % 4) return MQA_ERR_MISALIGNED;
-    for (int k = 0; k < 3; ++k) {
-      if (x.src_stride[k] < 0 || x.src_stride[k] > (1ll << 32) || x.dst_stride[k] < 0 || x.dst_stride[k] > (1ll << 32))
-        return MQA_ERR_BAD_SIZE;
-      if (x.src_stride[k] % 4 || x.dst_stride[k] % 4) return MQA_ERR_MISALIGNED;
-      wide = wide && x.src_stride[k] % 16 == 0 && x.dst_stride[k] % 16 == 0;
-    }
+    int64_t strides[2][3];   // of source and destination; those of one page or one piece, never taken, as 0
+    for (int d = 0; d < 2; ++d)
+      for (int k = 0; k < 3; ++k) {
+        const bool taken = k == 1 || (k == 2 ? x.rows_per_position : d == 0 ? num_src_phys_pages : num_dst_phys_pages) > 1;
+        const int64_t stride = strides[d][k] = taken ? (d == 0 ? x.src_stride : x.dst_stride)[k] : 0;
+        if (stride < 0 || stride > (1ll << 32)) return MQA_ERR_BAD_SIZE;
+        if (stride % 4) return MQA_ERR_MISALIGNED;
+        wide = wide && stride % 16 == 0;
+      }
     y.src = static_cast<const char*>(x.src);
     y.dst = static_cast<char*>(x.dst);
-    y.src_page = x.src_stride[0];
-    y.src_pos = x.src_stride[1];
-    y.src_row = x.src_stride[2];
-    y.dst_page = x.dst_stride[0];
-    y.dst_pos = x.dst_stride[1];
-    y.dst_row = x.dst_stride[2];
+    y.src_page = strides[0][0];
+    y.src_pos = strides[0][1];
+    y.src_row = strides[0][2];
+    y.dst_page = strides[1][0];
+    y.dst_pos = strides[1][1];
+    y.dst_row = strides[1][2];
     y.wide = wide;
     y.rows = x.rows_per_position;
     y.units = x.row_bytes / (wide ? 16 : 4);

@@ -24,7 +24,8 @@
  * elements of one head are contiguous. So [P, 64, Hkv, D] and [P, Hkv, 64, D]
  * memory, or keys and values interleaved in one pool, all fit. Bases and
  * strides must be multiples of 16 bytes, strides not negative and below 2^35
- * elements, and one page must span less than 2 GiB. Everything behind a page, position or head that
+ * elements, and one page must span less than 2 GiB; the page stride of one page and the
+ * head stride of one head are not looked at. Everything behind a page, position or head that
  * a call does not address is never read.
  *
  * Types. MQA_KV_BF16 and MQA_KV_FP16 caches go with queries and outputs of the
@@ -176,7 +177,8 @@ int64_t mqa_kv_evict_workspace_bytes(int64_t num_seqs, int64_t max_len);
 
 /* One paged array to compact: rows_per_position pieces of row_bytes bytes per
  * position (2^24 bytes together at most), at byte strides of page, position and
- * piece, 0 .. 2^32. Bases, strides and row_bytes must be multiples of 4 bytes.
+ * piece, 0 .. 2^32. Bases, strides and row_bytes must be multiples of 4 bytes; the
+ * page stride of a pool of one page and the piece stride of one piece are not looked at.
  * src and dst may be one pool. */
 typedef struct mqa_kv_array {
   const void* src;
