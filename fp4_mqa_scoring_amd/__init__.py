@@ -605,7 +605,8 @@ def mqa_kv_evict_select(acc, seq_len, budget, recent, keep, kept, workspace=None
     """Chooses what a budget keeps of every sequence: its last `recent` positions and the budget - recent
     earlier ones with the largest acc (float32 [n_seq, max_len]; seq_len int32 [n_seq]). Fills keep int32
     [n_seq, budget] (rising, padded with -1), kept int32 [n_seq] and, if given, kept_acc float32 [n_seq,
-    budget]; kept may be seq_len itself, nothing else may overlap. workspace: at least mqa_kv_evict_workspace_bytes(n_seq, max_len) bytes. Capturable."""
+    budget], the sums to go on with: the first ones of the next acc. kept may be seq_len itself, nothing else
+    may overlap. workspace: at least mqa_kv_evict_workspace_bytes(n_seq, max_len) bytes. Capturable."""
     torch = _kv()[0]
     if not isinstance(seq_len, torch.Tensor) or seq_len.dim() != 1:
         raise TypeError("seq_len must be a tensor of one dimension")

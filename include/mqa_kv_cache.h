@@ -162,8 +162,9 @@ int32_t mqa_kv_weights_accumulate(const mqa_kv_query* q, const float* lse, const
  *   budget   0 .. INT32_MAX;  0 <= recent <= budget
  *   keep     int32 [num_seqs, budget]   kept positions, rising, padded with -1
  *   kept     int32 [num_seqs]           how many
- *   kept_acc float [num_seqs, budget]   optional: their acc, padded with 0 (the
- *            sums to go on with after mqa_kv_compact)
+ *   kept_acc float [num_seqs, budget]   optional: their acc, padded with 0. To go on after mqa_kv_compact,
+ *            the caller copies it to the first `budget` sums of each sequence and clears those behind
+ *            (mqa_kv_weights_accumulate wants 64 * max_pages of them)
  * kept may be seq_len itself: the new lengths take the old ones' place. Any other overlap of keep, kept,
  * kept_acc or the workspace with each other, acc or seq_len is refused (MQA_ERR_OVERLAP).
  * workspace: mqa_kv_evict_workspace_bytes() bytes, 256-byte aligned: 0 (and the
