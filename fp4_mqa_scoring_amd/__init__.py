@@ -655,7 +655,8 @@ def mqa_kv_compact(keep, kept, src_table, dst_table, arrays, stream=None):
     src_table's pages to the first positions of dst_table's. arrays: up to KV_MAX_ARRAYS pairs (source,
     destination) of tensors [P, 64], [P, 64, X] or [P, 64, Y, X] (keys, values, the indexer's codes and
     scales, ...), whole 4-byte words per position; source and destination may be one pool, with
-    destination pages that the call does not read. Capturable."""
+    destination pages that the call does not read. One table serves all arrays, so a page counts as
+    inside the pools where every array has it (STATUS_BAD_PAGE otherwise). Capturable."""
     i32 = _kv()[0].int32
     keep_at, n, budget = _kv_table(keep, "keep", None)
     arrays = list(arrays)

@@ -137,8 +137,10 @@ int64_t mqa_kv_attention_selected_workspace_bytes(int64_t num_rows, int64_t K, i
  *   acc[seq, p] += sum over the sequence's rows r whose window holds p, and all heads h, of
  *                  exp(scale * k_scale * q[r, h] . k_p - lse[r, h])
  * with lse as the attention above returned it for the same rows (rows may also
- * be a whole prompt's). Reads the keys once. Rows are added in rising order,
- * without atomics. Positions outside every window keep their bits. A head whose lse is not finite
+ * be a whole prompt's). A position's keys are read once for every row whose window
+ * holds it and every 64 query heads of a key head (32 where D = 256). The order of the
+ * additions is fixed (by rows within a key head), without atomics: the same call gives the same
+ * bits. Positions outside every window keep their bits. A head whose lse is not finite
  * (an empty or failed row) adds nothing, nor does a row with a bad sequence or
  * window (MQA_STATUS_BAD_WINDOW) or a position whose page maps outside
  * [0, P_phys) (MQA_STATUS_BAD_PAGE).

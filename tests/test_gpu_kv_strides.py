@@ -56,3 +56,16 @@ def test_moves():
         mqa.mqa_kv_compact(keep, kept, page, page, [(a, b)])
         got = b.reshape(64, 8)
         assert torch.equal(got[:3], src[0, [1, 3, 63]]) and (got[3:] == 0).all()
+
+
+def test_moves_of_pools_of_different_sizes():
+    """A page that the smallest pool lacks is in none: what maps there is left out of every array."""
+    small, large = torch.rand(3, 64, device=DEV), torch.rand(5, 64, 2, device=DEV)
+    to = torch.zeros(4, 64, device=DEV), torch.zeros(6, 64, 2, device=DEV)
+    keep, kept = i32([[0, 64], [0, 1]]), i32([2, 2])
+    mqa.mqa_fp4_status()
+    mqa.mqa_kv_compact(keep, kept, i32([[1, 4], [2, 0]]), i32([[3], [4]]), [(small, to[0]), (large, to[1])])
+    assert mqa.mqa_fp4_status() == mqa.STATUS_BAD_PAGE
+    want = torch.zeros_like(to[0]), torch.zeros_like(to[1])
+    want[0][3, 0], want[1][3, 0] = small[1, 0], large[1, 0]
+    assert torch.equal(to[0], want[0]) and torch.equal(to[1], want[1])
