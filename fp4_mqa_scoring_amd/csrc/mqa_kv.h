@@ -49,7 +49,8 @@ constexpr int kv_tiles(int D, int G) { return G <= 16 ? 1 : G <= 32 || D == 256 
 constexpr int kv_head_groups(int D, int G) { return (G + 16 * kv_tiles(D, G) - 1) / (16 * kv_tiles(D, G)); }
 constexpr int kv_group_rows(int D, int G) { return G < 16 * kv_tiles(D, G) ? G : 16 * kv_tiles(D, G); }
 
-// Workgroups of the decode form: what 256 compute units hold at once (two each, by LDS and registers).
+// Workgroups of the decode form: two for each of 256 compute units, which is what LDS leaves the staged kernels room for,
+// and registers the others with D = 128 in 16 bits and D = 256. D = 64 would have room for four, 8 bits with fewer dims for three.
 constexpr int kKvDecodeGroups = 512;
 constexpr int kKvPlanRows = 1024;     // rows up to which every workgroup plans for itself
 constexpr int kKvSelBlock = 1024;     // slots of a list in LDS at once (selected form)

@@ -529,7 +529,10 @@ template <class T, bool E4M3, int D, int NQ>
 struct Ring {
   static constexpr int kParts = 2;
   static constexpr int kPos = D < 256 ? 32 : 16;             // positions of a wave
-  // SLACK 8: the vector unit is what a long list of slots waits for most (2,048 rows of 1,024: 130 us, 140 without)
+  // SLACK 8: where the bytes come from the L2 caches or are half as many, the vector unit is what a stage waits for most.
+  // us with 8 and with 0, 64 heads over one key head, D = 128: 2,048 lists of 1,024 slots 130, 140; 64 sequences of
+  // 16,384 positions in 8 bits 76.5, 83.6; 200 rows of one sequence of 8,192 in bf16 102.6, 109.8. From memory in bf16
+  // (64 of 32K to 131K) it makes no difference: 487.7, 488.6.
   typedef Wave<T, E4M3, D, NQ, kPos, false, 8> W;
   static constexpr int kStagePos = kParts * kPos;
   static constexpr int kRow = D * W::kBytes;                 // bytes of one position

@@ -39,7 +39,10 @@
  * Arithmetic. Products of the query with the keys, the scores, the softmax's
  * maximum and sum and the weighted sums of the values are held in 32 bits; the
  * weights are rounded to the query's type before they multiply the values, and
- * the output is rounded once. The order of the sums depends on the sizes and,
+ * the output is rounded once. Up to 16 heads per key head the largest weight is a
+ * power of two, which that rounding leaves alone; with more heads the running maximum
+ * follows the scores by up to 2^8, and the largest weight is rounded as the others
+ * are, by half a step of the type. The order of the sums depends on the sizes and,
  * for the decode form, on the windows of the whole batch, and on nothing else:
  * the same call gives the same bits.
  */
