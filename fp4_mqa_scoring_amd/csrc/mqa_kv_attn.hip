@@ -23,7 +23,7 @@
 // heads and is bound by memory (MI355X, whose large copies run at 4.9 TB/s: 64
 // sequences of 32K to 131K positions under 64 heads 5.6 to 5.8 TB/s, 32 of 2K to
 // 16K under 32 heads over 8 key heads 5.2). Lists of slots that rows share are read
-// from the L2 caches (2,048 rows of 1,024 slots, 64 heads: 129 us, 8.3 TB/s and
+// from the L2 caches (2,048 rows of 1,024 slots, 64 heads: 130 us, 8.3 TB/s and
 // 530 TFLOP/s). Up to 16 heads per key head go through registers, more through LDS,
 // both below with the reasons.
 #include "mqa_fp4_topk.h"
