@@ -127,8 +127,8 @@ __device__ __forceinline__ float groups_sum(float x) {
   return __uint_as_float(s[0]) + __uint_as_float(s[1]);
 }
 
-// log of a sum of weights held under the running maximum m (log2 domain, 2^kTop at the top): the
-// parts that make up for each other are taken out first, which is exact.
+// log of a sum of weights held under the running maximum m (log2 domain). kTop, which m lacks and the sum has too
+// much, goes from one to the other first: the logarithm of a sum near one is small, and so is its rounding.
 template <class T>
 __device__ __forceinline__ float lse_of(float m, float sum) {
   if constexpr (T::kTop == 0) return (m + __builtin_amdgcn_logf(sum)) * kLn2;
@@ -162,11 +162,11 @@ __device__ __forceinline__ void settle(v4f (&s)[N][2]) {
 // The registers and steps of one wave: NQ tiles of 16 query heads of one row and
 // key head, POS (16 or 32) positions at a time.
 //
-// The running maximum m is the largest score seen less kBias (log2 domain), so that the largest weight is 2^kTop at most,
-// and moves when it is passed by more than SLACK. 0: the largest weight is a power of two (to 2^-20), which the rounding of the weights to 16 bits leaves alone, and
-// where few weights count that is most of the rounding's error (relative error of the output 0.0018,
-// of its own rounding alone 0.0017, with SLACK 8 0.0022). 8: weights up to 2^8, whose relative rounding is the
-// same, and the sums are multiplied once or twice instead of in nearly every one of the first tiles.
+// The running maximum m is the largest score seen less kBias (log2 domain), so that the largest weight is 2^kTop at most
+// (bf16 with SLACK 8: 2^8), and moves when it is passed by more than SLACK. 0: the largest weight is a power of two (to
+// 2^-20), which the rounding of the weights to 16 bits leaves alone, and where few weights count that is most of the
+// rounding's error (bf16: relative error of the output 0.0018, of its own rounding alone 0.0017, with SLACK 8 0.0022). 8:
+// the relative rounding is the same, and the sums are multiplied once or twice instead of in nearly every one of the first tiles.
 template <class T, bool E4M3, int D, int NQ, int POS = 32, bool QL = false, int SLACK = 0>
 struct Wave {
   static constexpr int kPositions = POS;
