@@ -90,8 +90,14 @@ def lib() -> ctypes.CDLL:
         for name in ("mqa_kv_attention_decode_workspace_bytes", "mqa_kv_attention_selected_workspace_bytes",
                      "mqa_kv_evict_workspace_bytes"):
             getattr(L, name).restype = i64
+        L.mqa_kv_attention_decode_fp4.argtypes = L.mqa_kv_attention_decode.argtypes
+        L.mqa_kv_attention_selected_fp4.argtypes = L.mqa_kv_attention_selected.argtypes
+        L.mqa_kv_norm_rotate.argtypes = [P, P, P, i64, i32, i32, P]
+        L.mqa_kv_append.argtypes = [P, P, P, P]
+        L.mqa_kv_append_fp4.argtypes = [P, P, P, P]
         for name in ("mqa_kv_attention_decode", "mqa_kv_attention_selected", "mqa_kv_weights_accumulate",
-                     "mqa_kv_evict_select", "mqa_kv_compact"):
+                     "mqa_kv_evict_select", "mqa_kv_compact", "mqa_kv_attention_decode_fp4",
+                     "mqa_kv_attention_selected_fp4", "mqa_kv_norm_rotate", "mqa_kv_append", "mqa_kv_append_fp4"):
             getattr(L, name).restype = i32
         for name in ("mqa_fp4_topk_prefill", "mqa_fp4_topk_prefill_ex", "mqa_fp4_topk_prefill_static",
                      "mqa_fp4_dense_topk_prefill",
@@ -402,6 +408,10 @@ def mqa_fp4_set_stage_events(events) -> None:
 _KV_CACHE = struct.Struct("@PP3q3qqiiiff4x")    # mqa_kv_cache
 _KV_QUERY = struct.Struct("@Pqqiif4x")          # mqa_kv_query
 _KV_ARRAY = struct.Struct("@PP3q3qqq")          # mqa_kv_array
+_KV_CACHE_FP4 = struct.Struct("@4P12qqii")      # mqa_kv_cache_fp4
+_KV_ROWS = struct.Struct("@PqPqPfi")            # mqa_kv_rows
+_KV_TURN = struct.Struct("@PPiiif")             # mqa_kv_turn
+_KV_NEW = struct.Struct("@qi4xPqqPP")           # mqa_kv_new between its rows and its turn
 _kv_const = None
 
 
@@ -670,3 +680,207 @@ def mqa_kv_compact(keep, kept, src_table, dst_table, arrays, stream=None):
         min([src.shape[0] for src, _ in arrays], default=0), dst_at, dst_pages,
         min([dst.shape[0] for _, dst in arrays], default=0), made, len(arrays), _kv_stream(stream, keep.device))
     _rc(rc, "mqa_kv_compact")
+
+
+# --- caches in 4 bits (include/mqa_kv_fp4.h) ------------------------------------------
+
+
+def _kv_tensor(t, name, dtype, dims):
+    """t is a tensor of this type and number of dimensions (its last one contiguous); its shape and strides."""
+    if not isinstance(t, _kv()[0].Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    shape, stride = t.shape, t.stride()
+    if len(shape) != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, got {list(shape)}")
+    if shape[-1] > 1 and stride[-1] != 1 and t.numel():
+        raise ValueError(f"{name}: the elements of one head must be contiguous")
+    return shape, stride
+
+
+def _kv_cache_fp4(D, k_pages, k_scale, v_pages, v_scale):
+    """mqa_kv_cache_fp4 of codes [P, 64, Hkv, D / 2] and scales [P, 64, Hkv, D / 32] (v_pages None: keys only), and Hkv."""
+    u8 = _kv()[0].uint8
+    shape, k = _kv_tensor(k_pages, "k_pages", u8, 4)
+    P, page, heads, _ = shape
+    if page != 64 or shape[3] != D // 2 or heads < 1:
+        raise ValueError(f"k_pages must be [P, 64, Hkv, {D // 2}], got {list(shape)}")
+    scales = (P, 64, heads, D // 32)
+    got, ks = _kv_tensor(k_scale, "k_scale", u8, 4)
+    if got != scales:
+        raise ValueError(f"k_scale must be {list(scales)}, got {list(got)}")
+    v = vs = (0, 0, 0)
+    v_ptr = vs_ptr = 0
+    if v_pages is not None:
+        got, v = _kv_tensor(v_pages, "v_pages", u8, 4)
+        if got != shape:
+            raise ValueError(f"v_pages must be {list(shape)}, got {list(got)}")
+        got, vs = _kv_tensor(v_scale, "v_scale", u8, 4)
+        if got != scales:
+            raise ValueError(f"v_scale must be {list(scales)}, got {list(got)}")
+        v_ptr, vs_ptr = v_pages.data_ptr(), v_scale.data_ptr()
+    return _KV_CACHE_FP4.pack(k_pages.data_ptr(), v_ptr, k_scale.data_ptr(), vs_ptr, *k[:3], *v[:3], *ks[:3], *vs[:3], P,
+                              heads, D), heads
+
+
+def _kv_query_fp4(q, scale, k_pages, k_scale, v_pages, v_scale):
+    """mqa_kv_query, its shape, and mqa_kv_cache_fp4."""
+    query, shape = _kv_query(q, scale)
+    if v_pages is None:
+        raise TypeError("v_pages must be a torch.Tensor")
+    cache, heads = _kv_cache_fp4(shape[2], k_pages, k_scale, v_pages, v_scale)
+    if shape[1] % heads:
+        raise ValueError(f"k_pages: {shape[1]} query heads over {heads} key heads")
+    return query, shape, cache
+
+
+def mqa_kv_attention_decode_fp4(q, k_pages, k_scale, v_pages, v_scale, block_table, seq_of_row, row_start, row_end, out,
+                                workspace, lse=None, scale=None, stream=None):
+    """mqa_kv_attention_decode over a cache in 4 bits, the indexer's format: k_pages and v_pages uint8 [P, 64, Hkv,
+    D / 2] (two E2M1 codes to a byte, the even dim low), k_scale and v_scale uint8 [P, 64, Hkv, D / 32] (UE8M0);
+    page, position and head strides are free. The other arguments, and the workspace, as there. Capturable."""
+    query, shape, cache = _kv_query_fp4(q, scale, k_pages, k_scale, v_pages, v_scale)
+    rc = lib().mqa_kv_attention_decode_fp4(
+        query, cache, *_kv_windows(shape[:1], block_table, seq_of_row, row_start, row_end), *_kv_outputs(q, shape, out, lse),
+        *_kv_workspace(workspace), _kv_stream(stream, q.device))
+    _rc(rc, "mqa_kv_attention_decode_fp4")
+
+
+def mqa_kv_attention_selected_fp4(q, k_pages, k_scale, v_pages, v_scale, slots, count, out, workspace=None, lse=None,
+                                  scale=None, stream=None):
+    """mqa_kv_attention_selected over a cache in 4 bits (as in mqa_kv_attention_decode_fp4). Capturable."""
+    query, shape, cache = _kv_query_fp4(q, scale, k_pages, k_scale, v_pages, v_scale)
+    lists, _, K = _kv_table(slots, "slots", shape[0])
+    rc = lib().mqa_kv_attention_selected_fp4(
+        query, cache, lists, _kv_check(count, "count", _kv()[0].int32, shape[:1]), K, *_kv_outputs(q, shape, out, lse),
+        *_kv_workspace(workspace), _kv_stream(stream, q.device))
+    _rc(rc, "mqa_kv_attention_selected_fp4")
+
+
+# --- new heads: norm, rotation, appending (include/mqa_kv_append.h) ---------------------
+
+_KV_NO_ROWS = _KV_ROWS.pack(0, 0, 0, 0, 0, 0.0, 0)
+
+
+def _kv_rows(x, name, weight, weight_offset, out=None, like=None, outputs=False):
+    """mqa_kv_rows of x [T, H, D] (of `like`'s type, rows and D, if given) and its output."""
+    torch = _kv()[0]
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    kind, shape = x.dtype, x.shape
+    if kind != torch.bfloat16 and kind != torch.float16:
+        raise TypeError(f"{name} must be bfloat16 or float16, got {kind}")
+    if len(shape) != 3:
+        raise ValueError(f"{name} must be [T, H, D], got {list(shape)}")
+    T, H, D = shape
+    if like is not None and (kind != like.dtype or T != like.shape[0] or D != like.shape[2]):
+        raise ValueError(f"{name} must be {like.dtype} [{like.shape[0]}, H, {like.shape[2]}], got {kind} {list(shape)}")
+    rows = []
+    for t, what in ((x, name), (out, name + "_out"))[: 2 if outputs else 1]:
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{what} must be a torch.Tensor")
+        if t.dtype != kind or t.shape != shape:
+            raise ValueError(f"{what} must be {kind} {list(shape)}, got {t.dtype} {list(t.shape)}")
+        row, head, element = t.stride()
+        if T > 0 and ((D > 1 and element != 1) or (H > 1 and head != D)):
+            raise ValueError(f"the heads of one row of {what} must be contiguous")
+        rows += [t.data_ptr(), row if T > 1 else H * D]
+    if not outputs:
+        rows += [0, 0]
+    if weight is not None:
+        weight = _kv_check(weight, name + "_weight", kind, (D,))
+    return _KV_ROWS.pack(*rows, weight or 0, _f32(weight_offset), H)
+
+
+def _kv_turn(D, T, position, inv_freq, eps, rotary_offset, interleaved):
+    """mqa_kv_turn; position may be None."""
+    torch = _kv()[0]
+    if inv_freq is None:
+        return _KV_TURN.pack(0, 0, 0, 0, 0, _f32(eps))
+    freq = _kv_check(inv_freq, "inv_freq", torch.float32, (getattr(inv_freq, "shape", (0,)) or (0,))[:1])
+    at = 0 if position is None else _kv_check(position, "position", torch.int32, (T,))
+    return _KV_TURN.pack(freq, at or 0, 2 * inv_freq.shape[0], int(rotary_offset), int(bool(interleaved)), _f32(eps))
+
+
+def mqa_kv_norm_rotate(q, q_out, position=None, k=None, k_out=None, inv_freq=None, q_weight=None, k_weight=None, eps=1e-6,
+                       weight_offset=0.0, rotary_offset=0, interleaved=False, stream=None):
+    """Norms every head of q [T, H, D] (bfloat16 or float16; the row stride is free, as of a slice of a fused
+    projection's output) by its root mean square and q_weight [D] (+ weight_offset), rotates its dims from rotary_offset
+    on by position int32 [T] times inv_freq float32 [R / 2] (halves i and i + R / 2, or with `interleaved` dims 2 i and
+    2 i + 1), and writes q_out (q's shape; q itself, or apart from it); the same with k, k_out and k_weight in one
+    launch. Without a weight there is no norm, without inv_freq no rotation. Capturable."""
+    rows = _kv_rows(q, "q", q_weight, weight_offset, q_out, outputs=True)
+    T, _, D = q.shape
+    keys = None if k is None else _kv_rows(k, "k", k_weight, weight_offset, k_out, like=q, outputs=True)
+    if k is None and (k_weight is not None or k_out is not None):
+        raise ValueError("k_weight and k_out go with k")
+    turn = _kv_turn(D, T, position, inv_freq, eps, rotary_offset, interleaved)
+    rc = lib().mqa_kv_norm_rotate(rows, keys, turn, T, D, _kv()[1][q.dtype], _kv_stream(stream, q.device))
+    _rc(rc, "mqa_kv_norm_rotate")
+
+
+def _kv_append(what, k, v, cache, block_table, seq_of_row, position, rotary_position, inv_freq, k_weight, eps, weight_offset,
+               rotary_offset, interleaved, q, q_out, q_weight, stream):
+    i32 = _kv()[0].int32
+    keys = _kv_rows(k, "k", k_weight, weight_offset)
+    T, _, D = k.shape
+    values = _KV_NO_ROWS if v is None else _kv_rows(v, "v", None, 0.0, like=k)
+    queries = None if q is None else _kv_rows(q, "q", q_weight, weight_offset, q_out, like=k, outputs=True)
+    if q is None and (q_weight is not None or q_out is not None):
+        raise ValueError("q_weight and q_out go with q")
+    turn = _kv_turn(D, T, rotary_position, inv_freq, eps, rotary_offset, interleaved)
+    table, n_seq, pages = _kv_table(block_table, "block_table", None)
+    new = _KV_NEW.pack(T, _kv()[1][k.dtype], table, n_seq, pages, _kv_check(seq_of_row, "seq_of_row", i32, (T,)),
+                       _kv_check(position, "position", i32, (T,)))
+    rc = getattr(lib(), what)(keys + values + new + turn, queries, cache, _kv_stream(stream, k.device))
+    _rc(rc, what)
+
+
+def mqa_kv_append(k, v, k_pages, v_pages, block_table, seq_of_row, position, k_scale=1.0, v_scale=1.0,
+                  rotary_position=None, inv_freq=None, k_weight=None, eps=1e-6, weight_offset=0.0, rotary_offset=0,
+                  interleaved=False, q=None, q_out=None, q_weight=None, stream=None):
+    """Appends keys and values k, v [T, Hkv, D] (v and v_pages None: keys only) to a paged cache k_pages, v_pages
+    [P, 64, Hkv, D] of their type or float8_e4m3fn (then divided by k_scale, v_scale): row r goes to position
+    position[r] of sequence seq_of_row[r] (int32 [T]) through block_table (int32 [n_seq, max_pages]); a row at position
+    -1 is padding. Keys are normed by k_weight and rotated by rotary_position (position if None) times inv_freq on
+    the way, and in the same launch queries q into q_out, as in mqa_kv_norm_rotate. Capturable."""
+    torch, types, _ = _kv()
+    if not isinstance(k, torch.Tensor) or k.dim() != 3:
+        raise (ValueError if isinstance(k, torch.Tensor) else TypeError)("k must be a tensor [T, Hkv, D]")
+    if (v is None) != (v_pages is None):
+        raise ValueError("v and v_pages go together")
+    _, H, D = k.shape
+    tensors, strides = (k_pages,) if v is None else (k_pages, v_pages), []
+    for t, name in zip(tensors, ("k_pages", "v_pages")):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.dtype != k.dtype and t.dtype != torch.float8_e4m3fn or t.dtype != k_pages.dtype:
+            raise TypeError(f"{name} must be {k.dtype} or float8_e4m3fn, got {t.dtype}")
+        shape, stride = _kv_tensor(t, name, t.dtype, 4)
+        if shape != (k_pages.shape[0], 64, H, D):
+            raise ValueError(f"{name} must be [P, 64, {H}, {D}], got {list(shape)}")
+        strides += stride[:3]
+    kind = types.get(k_pages.dtype)
+    cache = _KV_CACHE.pack(k_pages.data_ptr(), 0 if v is None else v_pages.data_ptr(), *strides, *([0] * (6 - len(strides))),
+                           k_pages.shape[0], H, D, kind, _f32(k_scale), _f32(v_scale))
+    _kv_append("mqa_kv_append", k, v, cache, block_table, seq_of_row, position, rotary_position, inv_freq, k_weight, eps,
+               weight_offset, rotary_offset, interleaved, q, q_out, q_weight, stream)
+
+
+def mqa_kv_append_fp4(k, v, k_pages, k_scale, v_pages, v_scale, block_table, seq_of_row, position, rotary_position=None,
+                      inv_freq=None, k_weight=None, eps=1e-6, weight_offset=0.0, rotary_offset=0, interleaved=False,
+                      q=None, q_out=None, q_weight=None, stream=None):
+    """mqa_kv_append into a cache in 4 bits (codes uint8 [P, 64, Hkv, D / 2], scales uint8 [P, 64, Hkv, D / 32]), by
+    the rule of mqa_fp4_quantize. With one key head of 128 dims, keys only, these are the indexer's own pages
+    (k_pages[:, :, None], k_scale[:, :, None]). Capturable."""
+    torch = _kv()[0]
+    if not isinstance(k, torch.Tensor) or k.dim() != 3:
+        raise (ValueError if isinstance(k, torch.Tensor) else TypeError)("k must be a tensor [T, Hkv, D]")
+    if (v is None) != (v_pages is None):
+        raise ValueError("v and v_pages go together")
+    cache, heads = _kv_cache_fp4(k.shape[2], k_pages, k_scale, v_pages, v_scale)
+    if heads != k.shape[1]:
+        raise ValueError(f"k_pages has {heads} key heads, k {k.shape[1]}")
+    _kv_append("mqa_kv_append_fp4", k, v, cache, block_table, seq_of_row, position, rotary_position, inv_freq, k_weight, eps,
+               weight_offset, rotary_offset, interleaved, q, q_out, q_weight, stream)

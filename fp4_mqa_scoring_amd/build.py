@@ -11,7 +11,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libmqa_fp4.so")
 SOURCES = [os.path.join(PKG, "csrc", f) for f in ("mqa_kernels.hip", "mqa_api.hip", "mqa_quant.hip", "mqa_decode.hip",
-                                               "mqa_kv_attn.hip", "mqa_kv_evict.hip", "mqa_kv_api.hip")]
+                                               "mqa_kv_attn.hip", "mqa_kv_fp4.hip", "mqa_kv_evict.hip", "mqa_kv_write.hip",
+                                               "mqa_kv_api.hip", "mqa_kv_write_api.hip")]
 # measurement probes (bench only), a library of their own beside the operator's
 PROBE_LIB = os.path.join(PKG, "libmqa_fp4_probe.so")
 PROBE_SOURCES = [os.path.join(PKG, "csrc", "mqa_probe.hip")]

@@ -109,4 +109,48 @@ struct KvCompactArgs {
 };
 hipError_t launch_kv_compact(const KvCompactArgs& a, hipStream_t st);
 
+// A cache in 4 bits: the codes are KvAttnArgs' k and v, these their scales. Strides in bytes.
+struct KvFp4Args : KvAttnArgs {
+  const char* ks;
+  const char* vs;
+  int64_t ks_page, ks_pos, ks_head;
+  int64_t vs_page, vs_pos, vs_head;
+};
+hipError_t launch_kv_decode_fp4(const KvFp4Args& a, hipStream_t st);
+hipError_t launch_kv_selected_fp4(const KvFp4Args& a, hipStream_t st);
+
+// New heads: norm, rotation, appending. Strides in bytes.
+struct KvHeads {
+  const char* x;
+  int64_t x_row;
+  char* out;
+  int64_t out_row;
+  const uint16_t* weight;    // null: no norm
+  float offset;
+  int32_t n;                 // 0: none
+};
+struct KvPages {
+  char* p;
+  int64_t page, pos, head;
+};
+enum KvStore : int32_t { kKvStoreRows, kKvStoreSame, kKvStoreE4m3, kKvStoreFp4 };
+struct KvWriteArgs {
+  KvHeads q, k, v;           // out of k and v: kKvStoreRows
+  int64_t T;
+  int32_t D, type;           // MQA_KV_*
+  int32_t store;             // KvStore
+  const float* inv_freq;     // null: no rotation
+  const int32_t* turn_pos;   // null: pos
+  int32_t half, offset, interleaved;   // pairs of dims, the first dim
+  float eps;
+  const int32_t* table;
+  int64_t n_seq, max_pages;
+  const int32_t *seq, *pos;
+  int64_t P_phys;
+  KvPages kc, vc, ks, vs;    // codes or numbers, and the scales of 4 bits
+  float k_scale, v_scale;    // of 8 bits
+  int32_t* status;
+};
+hipError_t launch_kv_write(const KvWriteArgs& a, hipStream_t st);
+
 }  // namespace mqa

@@ -1,9 +1,11 @@
-// Host side of the C ABI declared in include/mqa_kv_cache.h: argument checks,
+// Host side of the C ABI declared in include/mqa_kv_cache.h and include/mqa_kv_fp4.h: argument checks,
 // strides in bytes, workspace layout. Nothing here allocates or synchronises.
 #include "mqa_fp4_topk.h"
 #include "mqa_host.h"
 #include "mqa_kv.h"
 #include "mqa_kv_cache.h"
+#include "mqa_kv_fp4.h"
+#include "mqa_kv_host.h"
 #include "mqa_launch.h"
 
 #include <hip/hip_runtime.h>
@@ -15,72 +17,28 @@ namespace {
 using namespace mqa::host;
 using mqa::KvAttnArgs;
 
-// A launch's threads are counted in 32 bits: at most 2^24 - 1 workgroups of 256.
-constexpr int64_t kMaxItems = (1ll << 24) - 256;
-constexpr int64_t kMaxPages = 0x7FFFFFFFll / 64;
-constexpr int64_t kMaxLogical = (0x7FFFFFFFll - 512) / 64;
-
-int64_t align_up(int64_t x) { return (x + 255) & ~255ll; }
-
-int64_t element_bytes(int32_t type) { return type == MQA_KV_E4M3 ? 1 : 2; }
-
-int32_t check_heads(int64_t num_rows, int32_t H, int32_t Hkv, int32_t D) {
-  if (D != 64 && D != 128 && D != 256) return MQA_ERR_UNSUPPORTED;
-  if (num_rows < 0 || H < 1 || H > 65536 || Hkv < 1 || H % Hkv) return MQA_ERR_BAD_SIZE;
-  if (num_rows > kMaxItems / H) return MQA_ERR_BAD_SIZE;
-  return MQA_OK;
-}
-
-// Strides of one tensor of the cache, checked and in bytes. Those of one page or one head are never taken, and
-// may be anything (as torch's are): 0 in their place.
-int32_t cache_strides(const int64_t* strides, const mqa_kv_cache& c, int64_t* page, int64_t* pos, int64_t* head) {
-  const int64_t bytes = element_bytes(c.type), D = c.head_dim;
-  const int64_t stride[3] = {c.num_phys_pages > 1 ? strides[0] : 0, strides[1], c.num_kv_heads > 1 ? strides[2] : 0};
-  for (int i = 0; i < 3; ++i) {
-    if (stride[i] < 0 || stride[i] >= (1ll << 35)) return MQA_ERR_BAD_SIZE;
-    if (stride[i] * bytes % 16) return MQA_ERR_MISALIGNED;
-  }
-  // one page's extent, and every product of a stride in the kernels, fits
-  const int64_t span = 63 * stride[1] * bytes;
-  if (span >= 0x7FFFFFFFll - D * bytes) return MQA_ERR_BAD_SIZE;
-  if (stride[2] * bytes > (0x7FFFFFFFll - D * bytes - span) / c.num_kv_heads) return MQA_ERR_BAD_SIZE;
-  *page = stride[0] * bytes;
-  *pos = stride[1] * bytes;
-  *head = stride[2] * bytes;
-  return MQA_OK;
-}
-
-// Checks queries and cache and fills the kernels' arguments; `values`: the call reads values too.
-int32_t attn_args(const mqa_kv_query* q, const mqa_kv_cache* c, bool values, KvAttnArgs* a) {
-  if (q == nullptr || c == nullptr) return MQA_ERR_NULL_POINTER;
-  if (q->type != MQA_KV_BF16 && q->type != MQA_KV_FP16) return MQA_ERR_UNSUPPORTED;
-  if (c->type != q->type && c->type != MQA_KV_E4M3) return MQA_ERR_UNSUPPORTED;
-  int32_t rc = check_heads(q->num_rows, q->num_heads, c->num_kv_heads, c->head_dim);
+// Checks queries over a cache's heads and pages and fills the kernels' arguments.
+int32_t query_args(const mqa_kv_query* q, int32_t Hkv, int32_t D, int64_t P_phys, float k_scale, float v_scale,
+                   KvAttnArgs* a) {
+  const int32_t rc = check_heads(q->num_rows, q->num_heads, Hkv, D);
   if (rc != MQA_OK) return rc;
-  if (c->num_phys_pages < 0 || c->num_phys_pages > kMaxPages) return MQA_ERR_BAD_SIZE;
-  if (!std::isfinite(q->scale) || !std::isfinite(c->k_scale) || !std::isfinite(c->v_scale)) return MQA_ERR_BAD_SIZE;
-  const float scale = q->scale * c->k_scale;
+  if (P_phys < 0 || P_phys > kMaxPages) return MQA_ERR_BAD_SIZE;
+  if (!std::isfinite(q->scale) || !std::isfinite(k_scale) || !std::isfinite(v_scale)) return MQA_ERR_BAD_SIZE;
+  const float scale = q->scale * k_scale;
   const float log2e = 1.44269504088896340736f;
   if (!std::isfinite(scale * log2e)) return MQA_ERR_BAD_SIZE;
-  const int64_t row = static_cast<int64_t>(q->num_heads) * c->head_dim;
+  const int64_t row = static_cast<int64_t>(q->num_heads) * D;
   if (q->num_rows > 1 && (q->row_stride < row || q->row_stride > (1ll << 32))) return MQA_ERR_BAD_SIZE;
   if (q->num_rows > 1 && q->row_stride * 2 % 16) return MQA_ERR_MISALIGNED;
-  *a = KvAttnArgs{};
-  rc = cache_strides(c->k_stride, *c, &a->k_page, &a->k_pos, &a->k_head);
-  if (rc == MQA_OK && values) rc = cache_strides(c->v_stride, *c, &a->v_page, &a->v_pos, &a->v_head);
-  if (rc != MQA_OK) return rc;
   a->q = static_cast<const char*>(q->q);
   a->q_row = q->num_rows > 1 ? q->row_stride * 2 : 0;
   a->Q = q->num_rows;
-  a->k = static_cast<const char*>(c->k);
-  a->v = static_cast<const char*>(c->v);
-  a->P_phys = c->num_phys_pages;
+  a->P_phys = P_phys;
   a->H = q->num_heads;
-  a->Hkv = c->num_kv_heads;
+  a->Hkv = Hkv;
   a->G = a->H / a->Hkv;
-  a->D = c->head_dim;
+  a->D = D;
   a->q_type = q->type;
-  a->kv_type = c->type;
   // the running maximum is taken before the scale, which therefore must not be
   // negative: a negative one changes the queries' signs instead
   // and a zero one, so that -infinity times it stays that, clears the queries
@@ -89,7 +47,42 @@ int32_t attn_args(const mqa_kv_query* q, const mqa_kv_cache* c, bool values, KvA
   if (!(a->c > 0.0f)) a->c = 1.0f;
   a->q_flip = std::signbit(scale) ? 0x80008000u : 0u;
   a->score_scale = scale;
-  a->v_scale = c->v_scale;
+  a->v_scale = v_scale;
+  return MQA_OK;
+}
+
+// Checks queries and cache and fills the kernels' arguments; `values`: the call reads values too.
+int32_t attn_args(const mqa_kv_query* q, const mqa_kv_cache* c, bool values, KvAttnArgs* a) {
+  if (q == nullptr || c == nullptr) return MQA_ERR_NULL_POINTER;
+  if (q->type != MQA_KV_BF16 && q->type != MQA_KV_FP16) return MQA_ERR_UNSUPPORTED;
+  if (c->type != q->type && c->type != MQA_KV_E4M3) return MQA_ERR_UNSUPPORTED;
+  *a = KvAttnArgs{};
+  int32_t rc = query_args(q, c->num_kv_heads, c->head_dim, c->num_phys_pages, c->k_scale, c->v_scale, a);
+  if (rc == MQA_OK) rc = cache_strides(c->k_stride, *c, &a->k_page, &a->k_pos, &a->k_head);
+  if (rc == MQA_OK && values) rc = cache_strides(c->v_stride, *c, &a->v_page, &a->v_pos, &a->v_head);
+  if (rc != MQA_OK) return rc;
+  a->k = static_cast<const char*>(c->k);
+  a->v = static_cast<const char*>(c->v);
+  a->kv_type = c->type;
+  return MQA_OK;
+}
+
+// The same over a cache in 4 bits.
+int32_t fp4_args(const mqa_kv_query* q, const mqa_kv_cache_fp4* c, mqa::KvFp4Args* a) {
+  if (q == nullptr || c == nullptr) return MQA_ERR_NULL_POINTER;
+  if (q->type != MQA_KV_BF16 && q->type != MQA_KV_FP16) return MQA_ERR_UNSUPPORTED;
+  *a = mqa::KvFp4Args{};
+  int32_t rc = query_args(q, c->num_kv_heads, c->head_dim, c->num_phys_pages, 1.0f, 1.0f, a);
+  const int64_t codes = c->head_dim / 2, scales = c->head_dim / 32;
+  if (rc == MQA_OK) rc = fp4_strides(c->k_stride, *c, codes, 16, &a->k_page, &a->k_pos, &a->k_head);
+  if (rc == MQA_OK) rc = fp4_strides(c->v_stride, *c, codes, 16, &a->v_page, &a->v_pos, &a->v_head);
+  if (rc == MQA_OK) rc = fp4_strides(c->k_scale_stride, *c, scales, scales, &a->ks_page, &a->ks_pos, &a->ks_head);
+  if (rc == MQA_OK) rc = fp4_strides(c->v_scale_stride, *c, scales, scales, &a->vs_page, &a->vs_pos, &a->vs_head);
+  if (rc != MQA_OK) return rc;
+  a->k = static_cast<const char*>(c->k);
+  a->v = static_cast<const char*>(c->v);
+  a->ks = static_cast<const char*>(c->k_scale);
+  a->vs = static_cast<const char*>(c->v_scale);
   return MQA_OK;
 }
 
@@ -239,6 +232,81 @@ int32_t mqa_kv_attention_selected(const mqa_kv_query* q, const mqa_kv_cache* cac
   if (a.status == nullptr) return MQA_ERR_HIP;
   place(&a, lay, workspace);
   return hip_rc(mqa::launch_kv_selected(a, st));
+}
+
+int32_t mqa_kv_attention_decode_fp4(const mqa_kv_query* q, const mqa_kv_cache_fp4* cache, const int32_t* block_table,
+                                    int64_t num_seqs, int64_t max_pages, const int32_t* seq_of_row,
+                                    const int32_t* row_start, const int32_t* row_end, void* out, float* lse,
+                                    void* workspace, int64_t workspace_bytes, void* stream) {
+  mqa::KvFp4Args a;
+  int32_t rc = fp4_args(q, cache, &a);
+  if (rc == MQA_OK) rc = window_args(&a, block_table, num_seqs, max_pages, seq_of_row, row_start, row_end);
+  if (rc != MQA_OK) return rc;
+  const bool rows = a.Q > 0, pages = a.P_phys > 0;
+  const uintptr_t unit = a.D / 32;
+  const PartialLayout lay = decode_layout(a.Q, a.D, a.G);
+  if (rows && workspace_bytes < lay.total) return MQA_ERR_BAD_SIZE;
+  const PtrSpec specs[] = {
+      {a.q, rows, 16},        {a.k, pages, 16},    {a.v, pages, 16},   {block_table, num_seqs > 0 && max_pages > 0, 4},
+      {a.ks, pages, unit},    {a.vs, pages, unit},
+      {seq_of_row, rows, 4},  {row_start, rows, 4}, {row_end, rows, 4}, {out, rows, 16},
+      {lse, false, 4},        {workspace, rows, 256},
+  };
+  rc = check_ptrs_host(specs, sizeof(specs) / sizeof(specs[0]));
+  if (rc != MQA_OK) return rc;
+  const Span ints[] = {{block_table, 1, 0, num_seqs * max_pages * 4}, {seq_of_row, 1, 0, a.Q * 4},
+                       {row_start, 1, 0, a.Q * 4}, {row_end, 1, 0, a.Q * 4}};
+  rc = check_attn_apart(a, out, lse, workspace, lay.total, ints, 4);
+  if (rc != MQA_OK) return rc;
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  DeviceGuard guard;
+  DeviceInfo info;
+  rc = enter(st, specs, sizeof(specs) / sizeof(specs[0]), guard, &info, /*allow_capture=*/true);
+  if (rc != MQA_OK || !rows) return rc;
+  a.out = out;
+  a.lse = lse;
+  a.status = mqa::status_word();
+  if (a.status == nullptr) return MQA_ERR_HIP;
+  place(&a, lay, workspace);
+  return hip_rc(mqa::launch_kv_decode_fp4(a, st));
+}
+
+int32_t mqa_kv_attention_selected_fp4(const mqa_kv_query* q, const mqa_kv_cache_fp4* cache, const int32_t* slots,
+                                      const int32_t* count, int64_t K, void* out, float* lse, void* workspace,
+                                      int64_t workspace_bytes, void* stream) {
+  mqa::KvFp4Args a;
+  int32_t rc = fp4_args(q, cache, &a);
+  if (rc != MQA_OK) return rc;
+  if (K < 0 || K > 0x7FFFFFFFll) return MQA_ERR_BAD_SIZE;
+  const bool rows = a.Q > 0, pages = a.P_phys > 0;
+  const uintptr_t unit = a.D / 32;
+  a.splits = mqa::kv_selected_splits(a.Q, K, a.D, a.G, a.Hkv);
+  const PartialLayout lay = selected_layout(a.Q, a.D, a.G, a.Hkv, a.splits);
+  if (rows && workspace_bytes < lay.total) return MQA_ERR_BAD_SIZE;
+  const PtrSpec specs[] = {
+      {a.q, rows, 16},      {a.k, pages, 16},    {a.v, pages, 16}, {a.ks, pages, unit}, {a.vs, pages, unit},
+      {slots, rows && K > 0, 4}, {count, rows, 4}, {out, rows, 16},  {lse, false, 4},
+      {workspace, rows && lay.total > 0, 256},
+  };
+  rc = check_ptrs_host(specs, sizeof(specs) / sizeof(specs[0]));
+  if (rc != MQA_OK) return rc;
+  const Span ints[] = {{slots, 1, 0, a.Q * K * 4}, {count, 1, 0, a.Q * 4}};
+  rc = check_attn_apart(a, out, lse, workspace, lay.total, ints, 2);
+  if (rc != MQA_OK) return rc;
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  DeviceGuard guard;
+  DeviceInfo info;
+  rc = enter(st, specs, sizeof(specs) / sizeof(specs[0]), guard, &info, /*allow_capture=*/true);
+  if (rc != MQA_OK || !rows) return rc;
+  a.slots = slots;
+  a.count = count;
+  a.K = K;
+  a.out = out;
+  a.lse = lse;
+  a.status = mqa::status_word();
+  if (a.status == nullptr) return MQA_ERR_HIP;
+  place(&a, lay, workspace);
+  return hip_rc(mqa::launch_kv_selected_fp4(a, st));
 }
 
 int32_t mqa_kv_weights_accumulate(const mqa_kv_query* q, const float* lse, const mqa_kv_cache* cache,
