@@ -61,6 +61,15 @@ Span rows_span(const void* p, int64_t row, const KvHeads& h, const KvWriteArgs& 
   return Span(p, h.n > 0 ? a.T : 0, row, static_cast<int64_t>(h.n) * a.D * 2);
 }
 
+// check_apart of two; rows of different strides count as one piece from the first to the last.
+int32_t check_two_apart(Span x, Span y) {
+  if (x.rows > 1 && y.rows > 1 && x.stride != y.stride) {
+    x = Span(x.p, 1, 0, (x.rows - 1) * x.stride + x.bytes);
+    y = Span(y.p, 1, 0, (y.rows - 1) * y.stride + y.bytes);
+  }
+  return overlap(x, y) ? MQA_ERR_OVERLAP : MQA_OK;
+}
+
 // Outputs of queries and keys lie apart from each other and from what the call reads, but for one in its own
 // x's place: the lanes that write a head are the only ones that read it, and have read it before.
 int32_t check_rows_apart(const KvWriteArgs& a, const Span* more, int n_more) {
@@ -68,13 +77,16 @@ int32_t check_rows_apart(const KvWriteArgs& a, const Span* more, int n_more) {
   const Span small[] = {{a.q.weight, 1, 0, a.D * 2}, {a.k.weight, 1, 0, a.D * 2}, {a.inv_freq, 1, 0, a.half * 4},
                         {a.turn_pos, 1, 0, a.T * 4}};
   const Span outs[] = {rows_span(a.q.out, a.q.out_row, a.q, a), rows_span(a.k.out, a.k.out_row, a.k, a)};
-  int32_t rc = check_apart(outs, 2, small, 4);
-  if (rc == MQA_OK) rc = check_apart(outs, 2, more, n_more);
+  int32_t rc = check_two_apart(outs[0], outs[1]);
+  for (int o = 0; o < 2 && rc == MQA_OK; ++o) {
+    rc = check_apart(&outs[o], 1, small, 4);
+    if (rc == MQA_OK) rc = check_apart(&outs[o], 1, more, n_more);
+  }
   for (int o = 0; o < 2 && rc == MQA_OK; ++o)
     for (int i = 0; i < 3 && rc == MQA_OK; ++i) {
       const bool in_place = o == i && heads[i]->x == heads[o]->out && heads[i]->x_row == heads[o]->out_row;
       const Span in = rows_span(heads[i]->x, heads[i]->x_row, *heads[i], a);
-      if (!in_place) rc = check_apart(&outs[o], 1, &in, 1);
+      if (!in_place) rc = check_two_apart(outs[o], in);
     }
   return rc;
 }
