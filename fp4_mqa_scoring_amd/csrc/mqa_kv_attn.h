@@ -147,6 +147,7 @@ __device__ __forceinline__ void settle(v4f (&s)[N][2]) {
 template <class T, bool E4M3, int D, int NQ, int POS = 32, bool QL = false, int SLACK = 0>
 struct Wave {
   static constexpr int kPositions = POS;
+  static constexpr int kQueries = NQ;
   static constexpr int kBytes = E4M3 ? 1 : 2;
   static constexpr int kChunks = D / 32;                 // matrix steps over the dims
   static constexpr int kLoads = D * kBytes / 64;         // 16-byte key loads per lane and position
@@ -378,13 +379,13 @@ struct Merge {
   float2 ml[kWaves][16];
   float2 fin[16];
 
-  template <class W>
+  template <int N = 0, class W>   // N: which 16 heads
   __device__ __forceinline__ void run(W& w, bool bad, int rows, float v_scale, char* out, float* lse, float* part_o,
                                       float2* part_ml) {
     const int wave = threadIdx.x >> 6;
     __syncthreads();   // the previous use of this memory is over
-    const float mine = groups_sum(w.l[0]);
-    if (w.grp == 0) ml[wave][w.col] = make_float2(w.m[0], bad ? __builtin_nanf("") : mine);
+    const float mine = groups_sum(w.l[N]);
+    if (w.grp == 0) ml[wave][w.col] = make_float2(w.m[N], bad ? __builtin_nanf("") : mine);
     __syncthreads();
     float2 x[kWaves];
     float top = -__builtin_inff(), total = 0.0f;
@@ -396,7 +397,7 @@ struct Merge {
     const float ref = top == -__builtin_inff() ? 0.0f : top;
 #pragma unroll
     for (int i = 0; i < kWaves; ++i) total += x[i].y * __builtin_amdgcn_exp2f(x[i].x - ref);
-    const float f = __builtin_amdgcn_exp2f(w.m[0] - ref);
+    const float f = __builtin_amdgcn_exp2f(w.m[N] - ref);
     if (wave == 0 && w.grp == 0) fin[w.col] = make_float2(top, total);
     constexpr int kT = kPart / 16;   // matrix tiles of a part
 #pragma unroll
@@ -407,8 +408,8 @@ struct Merge {
 #pragma unroll
         for (int t = 0; t < kT; t += 4)
           *reinterpret_cast<v4f*>(&o[wave][w.col][(4 * w.grp + i) * kT + t]) =
-              v4f{w.o[0][t0 + t][i] * f, w.o[0][t0 + t + 1][i] * f, w.o[0][t0 + t + 2][i] * f,
-                  w.o[0][t0 + t + 3][i] * f};
+              v4f{w.o[N][t0 + t][i] * f, w.o[N][t0 + t + 1][i] * f, w.o[N][t0 + t + 2][i] * f,
+                  w.o[N][t0 + t + 3][i] * f};
       __syncthreads();
       for (int e = threadIdx.x; e < 16 * kPart / 4; e += kThreads) {
         const int head = e / (kPart / 4), at = 4 * (e % (kPart / 4));
@@ -451,8 +452,8 @@ __device__ __forceinline__ void run_tiles(W& w, int t, int t_hi, float c, KEYS&&
 #pragma unroll
       for (int j = 0; j < W::kMine; ++j) inside |= (w.mine(j) >= lo && w.mine(j) < hi ? 1u : 0u) << j;
     }
-    v4f s[1][W::kTiles];
-    typename W::P p[1];
+    v4f s[W::kQueries][W::kTiles];
+    typename W::P p[W::kQueries];
     w.scores(s);
     if (more) load_keys(tn);
     w.weights(s, c, edge, inside, p);

@@ -45,12 +45,13 @@ inline int32_t cache_strides(const int64_t* strides, const mqa_kv_cache& c, int6
   return MQA_OK;
 }
 
-// The same of one tensor of a cache in 4 bits: `row` bytes a head, strides multiples of `unit` bytes.
+// The same of one tensor of a cache in 4 bits: `row` bytes a head, strides multiples of `unit` bytes and below 2^36
+// (of scales, whose unit is their row, 2^32).
 inline int32_t fp4_strides(const int64_t* strides, const mqa_kv_cache_fp4& c, int64_t row, int64_t unit, int64_t* page,
                            int64_t* pos, int64_t* head) {
   const int64_t stride[3] = {c.num_phys_pages > 1 ? strides[0] : 0, strides[1], c.num_kv_heads > 1 ? strides[2] : 0};
   for (int i = 0; i < 3; ++i) {
-    if (stride[i] < 0 || stride[i] >= (1ll << 36)) return MQA_ERR_BAD_SIZE;
+    if (stride[i] < 0 || stride[i] >= (unit == row ? 1ll << 32 : 1ll << 36)) return MQA_ERR_BAD_SIZE;
     if (stride[i] % unit) return MQA_ERR_MISALIGNED;
   }
   const int64_t span = 63 * stride[1];

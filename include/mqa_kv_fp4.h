@@ -28,10 +28,11 @@ extern "C" {
  * Codes are tensors [P_phys, 64, Hkv, D / 2] and scales [P_phys, 64, Hkv, D / 32]
  * of bytes, given by a base and the strides in BYTES of page, position and head;
  * the bytes of one head are contiguous. Bases and strides of codes must be
- * multiples of 16, of scales of D / 32; strides not negative and below 2^36, and
- * one page must span less than 2 GiB; the page stride of one page and the head
- * stride of one head are not looked at. Nothing behind a page, position or head that
- * a call does not address is read. */
+ * multiples of 16, of scales of D / 32; strides not negative and below 2^36 (of
+ * scales 2^32), and one page must span less than 2 GiB; the page stride of one page
+ * and the head stride of one head are not looked at. A page that a window touches
+ * is read in tiles of 32 positions; what it holds outside the window does not
+ * matter. Nothing of other pages is read. */
 typedef struct mqa_kv_cache_fp4 {
   void* k;                        /* codes of keys and values (an attention only reads them) */
   void* v;
