@@ -2,52 +2,33 @@
 // operands' layout are those of mqa_kv_attn.hip; keys and values are made 16-bit numbers in
 // registers, exactly, right before their product: one instruction makes two numbers of a
 // byte and their block's power of two.
+//
+// Every wave streams its own tiles of 32 positions through LDS: asynchronous copies (memory to
+// LDS, no registers) fill a ring of kDepth tiles, keys and values apart, and as soon as a
+// tile's keys (values) are in registers the copies of the tile kDepth further go into their
+// place. Nothing is shared between waves, so there are no barriers, only a count of
+// copies to wait for. The reads are inline assembly, each block with its own wait: the
+// compiler would wait for every copy in flight before an LDS read that it cannot prove apart.
 #include "mqa_kv_attn.h"
 
 namespace mqa {
 namespace {
 
 template <int SEL>
-__device__ __forceinline__ uint32_t pair_of(Bf16, uint32_t w, float scale) {
-  return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, SEL));
+__device__ __forceinline__ uint32_t pair_of(Bf16, uint32_t w, uint32_t scale) {
+  return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, __uint_as_float(scale), SEL));
 }
 template <int SEL>
-__device__ __forceinline__ uint32_t pair_of(Fp16, uint32_t w, float scale) {
-  return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, scale, SEL));
+__device__ __forceinline__ uint32_t pair_of(Fp16, uint32_t w, uint32_t scale) {
+  return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, __uint_as_float(scale), SEL));
 }
 
-// 2^(byte - 127) as the conversions take it: they look at the exponent alone.
-__device__ __forceinline__ float power_of(uint32_t byte) { return __uint_as_float(byte << 23); }
-
-// Reads of one page: a scalar base, and 32-bit offsets of the lane and of what is read.
-struct PageReads {
-  __amdgpu_buffer_rsrc_t page;
-  uint32_t lane;
-  int at;   // added to the offsets below
-
-  __device__ __forceinline__ PageReads(const char* base, uint32_t lane_) : lane(lane_), at(0) {
-    page = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), 0, 0x7FFFFFFF, 0x00027000);
-  }
-  __device__ __forceinline__ PageReads& from(int at_) {
-    at = at_;
-    return *this;
-  }
-  __device__ __forceinline__ void operator()(int off, v4u& x) const { x = __builtin_amdgcn_raw_buffer_load_b128(page, lane + off, at, 0); }
-  __device__ __forceinline__ void operator()(int off, v2u& x) const { x = __builtin_amdgcn_raw_buffer_load_b64(page, lane + off, at, 0); }
-  __device__ __forceinline__ void operator()(int off, uint32_t& x) const { x = __builtin_amdgcn_raw_buffer_load_b32(page, lane + off, at, 0); }
-  __device__ __forceinline__ void operator()(int off, uint16_t& x) const { x = __builtin_amdgcn_raw_buffer_load_b16(page, lane + off, at, 0); }
-  __device__ __forceinline__ void operator()(int off, uint8_t& x) const { x = __builtin_amdgcn_raw_buffer_load_b8(page, lane + off, at, 0); }
-};
-
-// Reads behind a lane's own address.
-struct LaneReads {
-  const char* p;
-  template <class X>
-  __device__ __forceinline__ void operator()(int off, X& x) const { x = *reinterpret_cast<const X*>(p + off); }
-};
+// A word of scale bytes turned so that the wanted one lies at a 32-bit number's exponent, which is
+// all that the conversions look at. shift: 8 * byte + 9.
+__device__ __forceinline__ uint32_t scale_of(uint32_t word, uint32_t shift) { return __builtin_amdgcn_alignbit(word, word, shift); }
 
 // A wave's tile of 32 positions over a cache in 4 bits. Lane (col, grp) holds, of keys 16 a + col, the codes of
-// kKeyDims neighbouring dims (one block's, or a half of one with D = 64), and of values mine(j) those of D / 16.
+// D / 4 dims, 32 of a block at most, and of values mine(j) those of D / 16 neighbouring ones.
 //
 // More than 16 heads: the queries lie in LDS, and the running maximum may lag by 2^8.
 template <class T, int D, int NQ>
@@ -64,9 +45,10 @@ struct Wave4 : Wave<T, false, D, NQ, 32, (NQ > 1), (NQ > 1 ? 8 : 0)> {
   typedef typename Base::P P;
   static constexpr int kKeyBlocks = D == 256 ? 2 : 1;    // scales of a lane's key
   static constexpr int kKeyWords = D / 32;               // words of 8 codes of a lane's key
+  static constexpr int kSteps = kChunks < 4 ? kChunks : 4;   // matrix steps over the dims at once
   static constexpr int kWords4 = D == 256 ? 2 : 1;       // words of a lane's value (half of one with D = 64)
 
-  const __attribute__((address_space(3))) v4u* ql;       // the queries in LDS, from this lane's on
+  uint32_t q_at;                                         // LDS address of the queries, from this lane's on
   uint32_t kc[kTiles][kKeyWords], kb[kTiles][kKeyBlocks];
   uint32_t vc[kMine][kWords4], vb[kMine];
 
@@ -86,7 +68,7 @@ struct Wave4 : Wave<T, false, D, NQ, 32, (NQ > 1), (NQ > 1 ? 8 : 0)> {
   // Loads the queries: into registers, or by the whole workgroup into `lds` (NQ * kChunks * 64 of it), between barriers.
   __device__ __forceinline__ void load_q(const char* p, int rows, uint32_t keep, uint32_t flip, v4u* lds) {
     if constexpr (kShared) {
-      ql = (const __attribute__((address_space(3))) v4u*)lds + this->lane;
+      q_at = lds_address(lds) + 16 * this->lane;
       __syncthreads();
       for (int x = threadIdx.x >> 6; x < NQ * kChunks; x += kWaves)
         lds[64 * x + this->lane] = query(p, x / kChunks, x % kChunks, rows, keep, flip);
@@ -99,84 +81,114 @@ struct Wave4 : Wave<T, false, D, NQ, 32, (NQ > 1), (NQ > 1 ? 8 : 0)> {
     }
   }
 
-  // What a lane adds to the address of its key: of the codes and scales of position 16 a.
-  __device__ __forceinline__ uint32_t key_at() const { return D == 64 ? 8 * grp : 16 * grp; }
-  __device__ __forceinline__ uint32_t key_scale_at() const { return D == 64 ? grp >> 1 : grp; }
-  // And of its values.
-  __device__ __forceinline__ uint32_t value_at() const { return col * (D / 32); }
-  __device__ __forceinline__ uint32_t value_scale_at() const { return col * kDims / 32; }
-
-  // This lane's codes and scale of position 16 a + col; get(offset, x) reads x at that offset behind their place.
-  template <class CODES, class SCALES>
-  __device__ __forceinline__ void load_k(int a, CODES&& codes, SCALES&& scales) {
-    if constexpr (D == 64) {
-      v2u x;
-      codes(0, x);
-      kc[a][0] = x.x;
-      kc[a][1] = x.y;
+  // Steps 4 h .. of query tile N.
+  template <int N>
+  __device__ __forceinline__ void read_q(int h, v4u (&y)[4]) const {
+    constexpr int kOff = N * kChunks * 1024;
+    if constexpr (kChunks == 2) {
+      __asm__ __volatile__("ds_read_b128 %0, %2 offset:%3\n\tds_read_b128 %1, %2 offset:%4\n\ts_waitcnt lgkmcnt(0)"
+                           : "=&v"(y[0]), "=&v"(y[1])
+                           : "v"(q_at), "n"(kOff), "n"(kOff + 1024)
+                           : "memory");
     } else {
-#pragma unroll
-      for (int i = 0; i < D / 128; ++i) {
-        v4u x;
-        codes(64 * i, x);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) kc[a][4 * i + e] = x[e];
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < kKeyBlocks; ++i) {
-      uint8_t x;
-      scales(4 * i, x);
-      kb[a][i] = x;
+      __asm__ __volatile__(
+          "ds_read_b128 %0, %4 offset:%5\n\tds_read_b128 %1, %4 offset:%6\n\t"
+          "ds_read_b128 %2, %4 offset:%7\n\tds_read_b128 %3, %4 offset:%8\n\ts_waitcnt lgkmcnt(0)"
+          : "=&v"(y[0]), "=&v"(y[1]), "=&v"(y[2]), "=&v"(y[3])
+          : "v"(q_at + 4096 * h), "n"(kOff), "n"(kOff + 1024), "n"(kOff + 2048), "n"(kOff + 3072)
+          : "memory");
     }
   }
 
-  // Of position mine(j).
-  template <class CODES, class SCALES>
-  __device__ __forceinline__ void load_v(int j, CODES&& codes, SCALES&& scales) {
-    if constexpr (D == 64) {
-      uint16_t x;
-      codes(0, x);
-      vc[j][0] = x;
-    } else if constexpr (D == 128) {
-      codes(0, vc[j][0]);
-    } else {
-      v2u x;
-      codes(0, x);
-      vc[j][0] = x.x;
-      vc[j][1] = x.y;
+  __device__ __forceinline__ void keys_of(int c, v4u (&x)[kTiles]) const {
+#pragma unroll
+    for (int a = 0; a < kTiles; ++a) {
+      const uint32_t w = kc[a][c], by = kb[a][D == 256 ? c >> 2 : 0];
+      x[a] = v4u{pair_of<0>(T{}, w, by), pair_of<1>(T{}, w, by), pair_of<2>(T{}, w, by), pair_of<3>(T{}, w, by)};
     }
-    uint8_t x;
-    scales(0, x);
-    vb[j] = x;
   }
 
-  __device__ __forceinline__ void scores(v4f (&s)[NQ][kTiles]) {
-    auto queries = ql;
-    if constexpr (kShared) __asm__ __volatile__("" : "+v"(queries));   // read anew for every tile, not kept in registers
+  // Scores of query tile N over steps [4 h, 4 h + 4) of the keys x.
+  template <int N>
+  __device__ __forceinline__ void score_tile(v4f (&s)[kTiles], const v4u (&x)[kSteps][kTiles], int h) const {
+    v4u y[4];
+    if constexpr (kShared) {
+      read_q<N>(h, y);
+    } else {
 #pragma unroll
-    for (int n = 0; n < NQ; ++n)
-#pragma unroll
-      for (int a = 0; a < kTiles; ++a) s[n][a] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-    for (int c = 0; c < kChunks; ++c) {
-      v4u x[kTiles];
-#pragma unroll
-      for (int a = 0; a < kTiles; ++a) {
-        const uint32_t w = kc[a][c];
-        const float by = power_of(kb[a][D == 256 ? c >> 2 : 0]);
-        x[a] = v4u{pair_of<0>(T{}, w, by), pair_of<1>(T{}, w, by), pair_of<2>(T{}, w, by), pair_of<3>(T{}, w, by)};
-      }
-#pragma unroll
-      for (int n = 0; n < NQ; ++n) {
-        v4u y;
-        if constexpr (kShared) y = queries[(n * kChunks + c) * 64];
-        else y = q[n][c];
-#pragma unroll
-        for (int a = 0; a < kTiles; ++a) s[n][a] = T::mfma(x[a], y, s[n][a]);
-      }
+      for (int c = 0; c < kSteps; ++c) y[c] = q[N][4 * h + c];
     }
-    settle(s);
+    if (h == 0)
+#pragma unroll
+      for (int a = 0; a < kTiles; ++a) s[a] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int c = 0; c < kSteps; ++c)
+#pragma unroll
+      for (int a = 0; a < kTiles; ++a) s[a] = T::mfma(x[c][a], y[c], s[a]);
+  }
+
+  // Weights of query tile N while the scores of the next one are made.
+  template <int N>
+  __device__ __forceinline__ void weigh_tiles(v4f (&s)[kTiles], const v4u (&x)[kSteps][kTiles], float c, bool edge, uint32_t inside,
+                                              P (&p)[NQ]) {
+    v4f after[kTiles];
+    if constexpr (N + 1 < NQ) score_tile<N + 1>(after, x, 0);
+    weigh<N>(s, c, edge, inside, p[N]);
+    if constexpr (N + 1 < NQ) weigh_tiles<N + 1>(after, x, c, edge, inside, p);
+  }
+
+  // The weights of the tile that lies in kc and kb, packed as the second product's operand.
+  __device__ __forceinline__ void weights_of_tile(float c, bool edge, uint32_t inside, P (&p)[NQ]) {
+    v4u x[kSteps][kTiles];
+    if constexpr (kChunks <= 4) {
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) keys_of(i, x[i]);
+      v4f s[kTiles];
+      score_tile<0>(s, x, 0);
+      weigh_tiles<0>(s, x, c, edge, inside, p);
+    } else {   // D = 256: half of the dims at a time
+      static_assert(NQ <= 2, "two tiles of queries at most");
+      v4f s[2][kTiles];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) keys_of(4 * h + i, x[i]);
+        score_tile<0>(s[0], x, h);
+        if constexpr (NQ > 1) score_tile<NQ - 1>(s[1], x, h);
+      }
+      weigh<0>(s[0], c, edge, inside, p[0]);
+      if constexpr (NQ > 1) weigh<NQ - 1>(s[1], c, edge, inside, p[NQ - 1]);
+    }
+  }
+
+  // Scores of query tile N to weights, as Wave::weights, for itself alone.
+  template <int N>
+  __device__ __forceinline__ void weigh(v4f (&s)[kTiles], float c, bool edge, uint32_t inside, P& p) {
+    constexpr float kSlack = NQ > 1 ? 8.0f : 0.0f;
+    __asm__ __volatile__("s_nop 7" : "+v"(s[0]), "+v"(s[1]));   // as settle()
+    if (edge) {   // a score of -infinity is a weight of 0, as c > 0
+      const uint32_t in = Base::here(inside);
+#pragma unroll
+      for (int j = 0; j < kMine; ++j) s[j >> 2][j & 3] = (in >> j & 1) ? s[j >> 2][j & 3] : -__builtin_inff();
+    }
+    float top = max3(max3(max3(s[0][0], s[0][1], s[0][2]), s[0][3], s[1][0]), s[1][1], max2(s[1][2], s[1][3]));
+    top = Base::kBias == 0 ? groups_max(top) * c : __builtin_fmaf(groups_max(top), c, static_cast<float>(-Base::kBias));
+    float& m = this->m[N];
+    if (__any(top > m + kSlack)) {
+      const float to = fmaxf(m, top);
+      const float f = to == m ? 1.0f : __builtin_amdgcn_exp2f(m - to);
+      m = to;
+      this->l[N] *= f;
+#pragma unroll
+      for (int t = 0; t < kDims; ++t) this->o[N][t] *= f;
+    }
+    const float ref = m == -__builtin_inff() ? 0.0f : m;
+    float w[kMine];
+#pragma unroll
+    for (int j = 0; j < kMine; ++j) w[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j >> 2][j & 3], c, -ref));
+    this->l[N] += ((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7]));
+#pragma unroll
+    for (int j = 0; j < kMine / 2; ++j) p[j] = T::pack(w[2 * j], w[2 * j + 1]);
   }
 
   // Values outside the window: every code is a number, so a scale of nearly 0 will do.
@@ -187,15 +199,10 @@ struct Wave4 : Wave<T, false, D, NQ, 32, (NQ > 1), (NQ > 1 ? 8 : 0)> {
   }
 
   template <int E>
-  __device__ __forceinline__ uint32_t dims_pair(int j) const {
-    return pair_of<(E & 3)>(T{}, vc[j][E >> 2], power_of(vb[j]));
-  }
-
-  template <int E>
   __device__ __forceinline__ void add_pair(const P (&p)[NQ]) {
     uint32_t w[kMine];
 #pragma unroll
-    for (int j = 0; j < kMine; ++j) w[j] = dims_pair<E>(j);
+    for (int j = 0; j < kMine; ++j) w[j] = pair_of<(E & 3)>(T{}, vc[j][E >> 2], vb[j]);
     P even, odd;
 #pragma unroll
     for (int jj = 0; jj < kMine / 2; ++jj) {
@@ -225,6 +232,252 @@ struct Wave4 : Wave<T, false, D, NQ, 32, (NQ > 1), (NQ > 1 ? 8 : 0)> {
   }
 };
 
+// --- a wave's stream of tiles ---------------------------------------------------
+
+// LDS of the four waves' rings. A piece is a tile's keys or values: 32 rows of D / 2 bytes of codes, one after another,
+// and their scales, one word a row (two with D = 256; with D = 64 the upper half is empty).
+//
+// kDepth: as many tiles as LDS holds for two workgroups of a compute unit.
+template <class T, int D, int NQ>
+struct Ring4 {
+  typedef Wave4<T, D, NQ> W;
+  static constexpr int kRow = D / 2, kCodes = 32 * kRow, kScaleWords = D == 256 ? 2 : 1;
+  static constexpr int kPiece = kCodes + 32 * 4 * kScaleWords;
+  static constexpr int kDepth = D == 64 ? 4 : D == 128 ? (NQ == 1 ? 4 : 3) : (NQ == 1 ? 2 : 1);
+  static constexpr int kLanes = kRow / 16;                   // lanes that copy one row
+  static constexpr int kCopyRows = 64 / kLanes;              // rows of one copy of 1 KiB
+  static constexpr int kCodeCopies = kCodes / 1024, kCopies = kCodeCopies + 1;   // per piece
+  char piece[kWaves][kDepth][2][kPiece];
+
+  // Keys lie with the 16-byte parts of a row permuted by its number, so that the rows that one read takes fall on
+  // different banks. The same for every copy of a piece.
+  static __device__ __forceinline__ int swizzle(int row) { return D == 64 ? row >> 3 & 1 : D == 128 ? row >> 1 & 3 : row & 7; }
+
+  // This lane's row in the first copy of a piece, and its bytes of that row.
+  static __device__ __forceinline__ int code_row(int lane) { return lane / kLanes; }
+  static __device__ __forceinline__ int code_byte(int kv, int lane) {
+    return 16 * (kv == 0 ? lane % kLanes ^ swizzle(code_row(lane)) : lane % kLanes);
+  }
+  static __device__ __forceinline__ int scale_row(int lane) { return D == 256 ? lane >> 1 : lane & 31; }
+  static __device__ __forceinline__ int scale_byte(int lane) { return D == 256 ? 4 * (lane & 1) : 0; }
+
+  // Copy i of a piece's codes, and of its scales.
+  __device__ __forceinline__ void copy(int wave, int stage, int kv, int i, const char* src) {
+    __builtin_amdgcn_global_load_lds(src, &piece[wave][stage][kv][1024 * i], 16, 0, 0);
+  }
+  __device__ __forceinline__ void copy_scales(int wave, int stage, int kv, int lane, const char* src) {
+    if (D == 256 || lane < 32) __builtin_amdgcn_global_load_lds(src, &piece[wave][stage][kv][kCodes], D == 64 ? 2 : 4, 0, 0);
+  }
+
+  // The same from a scalar base, `off` bytes and a lane's own offset behind it (all together below 2^31).
+  static __device__ __forceinline__ __amdgpu_buffer_rsrc_t page_at(const char* base) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), 0, 0x7FFFFFFF, 0x00027000);
+  }
+  __device__ __forceinline__ void copy(int wave, int stage, int kv, int i, __amdgpu_buffer_rsrc_t page, int off, uint32_t lane_at) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(page, &piece[wave][stage][kv][1024 * i], 16, lane_at, off, 0, 0);
+  }
+  __device__ __forceinline__ void copy_scales(int wave, int stage, int kv, int lane, __amdgpu_buffer_rsrc_t page, int off, uint32_t lane_at) {
+    if (D == 256 || lane < 32)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(page, &piece[wave][stage][kv][kCodes], D == 64 ? 2 : 4, lane_at, off, 0, 0);
+  }
+
+  // Waits until the oldest piece in flight is there: `more` younger ones at least are on their way.
+  static __device__ __forceinline__ void arrived(int more) {
+    constexpr int kYounger = 2 * kDepth - 1;
+    if (more >= kYounger) __asm__ __volatile__("s_waitcnt vmcnt(%0)" ::"n"(kYounger * kCopies) : "memory");
+    else __asm__ __volatile__("s_waitcnt vmcnt(0)" ::: "memory");
+  }
+
+  // Keys 16 a + col of a piece into w.kc and w.kb.
+  static __device__ __forceinline__ void read_keys(W& w, uint32_t at, uint32_t shift) {
+    const uint32_t scales = at + kCodes + 4 * kScaleWords * w.col;
+    if constexpr (D == 64) {
+      const uint32_t codes = at + w.col * kRow + ((8 * w.grp) ^ (16 * swizzle(w.col)));
+      v2u x, y;
+      uint32_t sx, sy;
+      __asm__ __volatile__(
+          "ds_read_b64 %0, %4\n\tds_read_b64 %1, %4 offset:512\n\t"
+          "ds_read_b32 %2, %5\n\tds_read_b32 %3, %5 offset:64\n\ts_waitcnt lgkmcnt(0)"
+          : "=&v"(x), "=&v"(y), "=&v"(sx), "=&v"(sy)
+          : "v"(codes), "v"(scales)
+          : "memory");
+      w.kc[0][0] = x.x;
+      w.kc[0][1] = x.y;
+      w.kc[1][0] = y.x;
+      w.kc[1][1] = y.y;
+      w.kb[0][0] = scale_of(sx, shift);
+      w.kb[1][0] = scale_of(sy, shift);
+    } else if constexpr (D == 128) {
+      const uint32_t codes = at + w.col * kRow + 16 * (w.grp ^ swizzle(w.col));
+      v4u x, y;
+      uint32_t sx, sy;
+      __asm__ __volatile__(
+          "ds_read_b128 %0, %4\n\tds_read_b128 %1, %4 offset:1024\n\t"
+          "ds_read_b32 %2, %5\n\tds_read_b32 %3, %5 offset:64\n\ts_waitcnt lgkmcnt(0)"
+          : "=&v"(x), "=&v"(y), "=&v"(sx), "=&v"(sy)
+          : "v"(codes), "v"(scales)
+          : "memory");
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        w.kc[0][e] = x[e];
+        w.kc[1][e] = y[e];
+      }
+      w.kb[0][0] = scale_of(sx, shift);
+      w.kb[1][0] = scale_of(sy, shift);
+    } else {
+      const uint32_t row = at + w.col * kRow, part = w.grp ^ swizzle(w.col), codes = row + 16 * part, other = row + 16 * (part ^ 4);
+      v4u x[4];
+      v2u s[2];
+      __asm__ __volatile__(
+          "ds_read_b128 %0, %6\n\tds_read_b128 %1, %7\n\t"
+          "ds_read_b128 %2, %6 offset:2048\n\tds_read_b128 %3, %7 offset:2048\n\t"
+          "ds_read_b64 %4, %8\n\tds_read_b64 %5, %8 offset:128\n\ts_waitcnt lgkmcnt(0)"
+          : "=&v"(x[0]), "=&v"(x[1]), "=&v"(x[2]), "=&v"(x[3]), "=&v"(s[0]), "=&v"(s[1])
+          : "v"(codes), "v"(other), "v"(scales)
+          : "memory");
+#pragma unroll
+      for (int a = 0; a < 2; ++a)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) w.kc[a][4 * i + e] = x[2 * a + i][e];
+          w.kb[a][i] = scale_of(s[a][i], shift);
+        }
+    }
+  }
+
+  // Values mine(j) of a piece into w.vc and w.vb.
+  static __device__ __forceinline__ void read_values(W& w, uint32_t at, uint32_t shift) {
+    const uint32_t codes = at + 4 * w.grp * kRow + w.col * (D / 32);
+    const uint32_t scales = at + kCodes + 16 * kScaleWords * w.grp + (D == 256 ? 4 * (w.col >> 3) : 0);
+    if constexpr (D == 256) {
+      v2u x[8], s[4];
+      __asm__ __volatile__(
+          "ds_read_b64 %0, %12\n\tds_read_b64 %1, %12 offset:128\n\t"
+          "ds_read_b64 %2, %12 offset:256\n\tds_read_b64 %3, %12 offset:384\n\t"
+          "ds_read_b64 %4, %12 offset:2048\n\tds_read_b64 %5, %12 offset:2176\n\t"
+          "ds_read_b64 %6, %12 offset:2304\n\tds_read_b64 %7, %12 offset:2432\n\t"
+          "ds_read2_b32 %8, %13 offset0:0 offset1:2\n\tds_read2_b32 %9, %13 offset0:4 offset1:6\n\t"
+          "ds_read2_b32 %10, %13 offset0:32 offset1:34\n\tds_read2_b32 %11, %13 offset0:36 offset1:38\n\ts_waitcnt lgkmcnt(0)"
+          : "=&v"(x[0]), "=&v"(x[1]), "=&v"(x[2]), "=&v"(x[3]), "=&v"(x[4]), "=&v"(x[5]), "=&v"(x[6]), "=&v"(x[7]),
+            "=&v"(s[0]), "=&v"(s[1]), "=&v"(s[2]), "=&v"(s[3])
+          : "v"(codes), "v"(scales)
+          : "memory");
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        w.vc[j][0] = x[j].x;
+        w.vc[j][1] = x[j].y;
+        w.vb[j] = scale_of(s[j / 2][j & 1], shift);
+      }
+    } else {
+      v4u s[2];
+      if constexpr (D == 128) {
+        __asm__ __volatile__(
+            "ds_read_b32 %0, %10\n\tds_read_b32 %1, %10 offset:64\n\t"
+            "ds_read_b32 %2, %10 offset:128\n\tds_read_b32 %3, %10 offset:192\n\t"
+            "ds_read_b32 %4, %10 offset:1024\n\tds_read_b32 %5, %10 offset:1088\n\t"
+            "ds_read_b32 %6, %10 offset:1152\n\tds_read_b32 %7, %10 offset:1216\n\t"
+            "ds_read_b128 %8, %11\n\tds_read_b128 %9, %11 offset:64\n\ts_waitcnt lgkmcnt(0)"
+            : "=&v"(w.vc[0][0]), "=&v"(w.vc[1][0]), "=&v"(w.vc[2][0]), "=&v"(w.vc[3][0]), "=&v"(w.vc[4][0]),
+              "=&v"(w.vc[5][0]), "=&v"(w.vc[6][0]), "=&v"(w.vc[7][0]), "=&v"(s[0]), "=&v"(s[1])
+            : "v"(codes), "v"(scales)
+            : "memory");
+      } else {
+        __asm__ __volatile__(
+            "ds_read_u16 %0, %10\n\tds_read_u16 %1, %10 offset:32\n\t"
+            "ds_read_u16 %2, %10 offset:64\n\tds_read_u16 %3, %10 offset:96\n\t"
+            "ds_read_u16 %4, %10 offset:512\n\tds_read_u16 %5, %10 offset:544\n\t"
+            "ds_read_u16 %6, %10 offset:576\n\tds_read_u16 %7, %10 offset:608\n\t"
+            "ds_read_b128 %8, %11\n\tds_read_b128 %9, %11 offset:64\n\ts_waitcnt lgkmcnt(0)"
+            : "=&v"(w.vc[0][0]), "=&v"(w.vc[1][0]), "=&v"(w.vc[2][0]), "=&v"(w.vc[3][0]), "=&v"(w.vc[4][0]),
+              "=&v"(w.vc[5][0]), "=&v"(w.vc[6][0]), "=&v"(w.vc[7][0]), "=&v"(s[0]), "=&v"(s[1])
+            : "v"(codes), "v"(scales)
+            : "memory");
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w.vb[j] = scale_of(s[j / 4][j & 3], shift);
+    }
+  }
+
+  // This lane's slots of a tile: of the rows that it copies codes of, and scales.
+  static __device__ __forceinline__ void read_slots(int (&slot)[kCodeCopies], int* scale_slot, uint32_t codes, uint32_t scales) {
+    if constexpr (kCodeCopies == 4) {
+      __asm__ __volatile__(
+          "ds_read_b32 %0, %5\n\tds_read_b32 %1, %5 offset:32\n\tds_read_b32 %2, %5 offset:64\n\t"
+          "ds_read_b32 %3, %5 offset:96\n\tds_read_b32 %4, %6\n\ts_waitcnt lgkmcnt(0)"
+          : "=&v"(slot[0]), "=&v"(slot[1]), "=&v"(slot[2]), "=&v"(slot[3]), "=&v"(*scale_slot)
+          : "v"(codes), "v"(scales)
+          : "memory");
+    } else if constexpr (kCodeCopies == 2) {
+      __asm__ __volatile__("ds_read_b32 %0, %3\n\tds_read_b32 %1, %3 offset:64\n\tds_read_b32 %2, %4\n\ts_waitcnt lgkmcnt(0)"
+                           : "=&v"(slot[0]), "=&v"(slot[1]), "=&v"(*scale_slot)
+                           : "v"(codes), "v"(scales)
+                           : "memory");
+    } else {
+      static_assert(kCodeCopies == 1, "one, two or four");
+      __asm__ __volatile__("ds_read_b32 %0, %2\n\tds_read_b32 %1, %3\n\ts_waitcnt lgkmcnt(0)"
+                           : "=&v"(slot[0]), "=&v"(*scale_slot)
+                           : "v"(codes), "v"(scales)
+                           : "memory");
+    }
+    static_assert(kCopyRows * 4 == (kCodeCopies == 4 ? 32 : kCodeCopies == 2 ? 64 : 128), "the offsets above");
+  }
+
+  // This wave's tiles t, t + kWaves, ... below t_hi. keys(t, stage) and values(t, stage) issue the copies of one
+  // piece, values those of the tile that keys was last called for; range(t, &lo, &hi) gives the positions that count.
+  template <class KEYS, class VALUES, class RANGE>
+  __device__ __forceinline__ void run(W& w, int wave, int t, int t_hi, float c, KEYS&& keys, VALUES&& values, RANGE&& range) {
+    if (t >= t_hi) return;
+    const uint32_t ring = lds_address(&piece[wave][0][0][0]);
+    // byte of the word that holds the scale of this lane's keys, and of its values
+    const uint32_t k_shift = 8 * (D == 64 ? w.grp >> 1 : w.grp) + 9;
+    const uint32_t v_shift = 8 * (D == 64 ? w.col >> 3 : D == 128 ? w.col >> 2 : w.col >> 1 & 3) + 9;
+    // no other load or store of this wave is in flight when the copies are counted
+    __asm__ __volatile__("s_waitcnt vmcnt(0)" ::: "memory");
+    const int tiles = (t_hi - t + kWaves - 1) / kWaves;
+#pragma unroll
+    for (int i = 0; i < kDepth; ++i)
+      if (i < tiles) {
+        keys(t + kWaves * i, i);
+        __asm__ __volatile__("" ::: "memory");   // a piece's copies are counted before the next one's
+        values(t + kWaves * i, i);
+        __asm__ __volatile__("" ::: "memory");
+      }
+    int stage = 0;
+    for (int i = 0; i < tiles; ++i, t += kWaves) {
+      int lo, hi;
+      range(t, &lo, &hi);
+      const bool edge = lo > 0 || hi < 32;
+      uint32_t inside = 0xFFu;
+      if (edge) {
+        inside = 0;
+#pragma unroll
+        for (int j = 0; j < W::kMine; ++j) inside |= (w.mine(j) >= lo && w.mine(j) < hi ? 1u : 0u) << j;
+      }
+      const int left = 2 * (tiles - i) - 1;   // pieces behind this one
+      const uint32_t at = ring + 2 * kPiece * stage;
+      typename W::P p[NQ];
+      arrived(left);
+      read_keys(w, at, k_shift);
+      if (i + kDepth < tiles) {
+        keys(t + kWaves * kDepth, stage);
+        __asm__ __volatile__("" ::: "memory");
+      }
+      w.weights_of_tile(c, edge, inside, p);
+      // the keys that were just asked for are younger too
+      arrived(i + kDepth < tiles ? 2 * kDepth : 0);
+      read_values(w, at + kPiece, v_shift);
+      if (i + kDepth < tiles) {
+        values(t + kWaves * kDepth, stage);
+        __asm__ __volatile__("" ::: "memory");
+      }
+      if (edge) w.clear_outside(inside);
+      w.add_values(p);
+      stage = stage + 1 < kDepth ? stage + 1 : 0;
+    }
+  }
+};
+
 // Heads of one row and key head that a workgroup carries.
 template <int NQ>
 __device__ __forceinline__ int group_of(const KvFp4Args& a) { return a.G < 16 * NQ ? a.G : 16 * NQ; }
@@ -242,35 +495,71 @@ __device__ __forceinline__ void join_waves(Merge<T, D>& merge, W& w, bool bad, i
   }
 }
 
+// A workgroup's LDS: the rings, and when the last tile is done the memory that joins the waves.
+template <class T, int D, int NQ>
+union Space {
+  Ring4<T, D, NQ> ring;
+  Merge<T, D> merge;
+};
+
 // --- decode form --------------------------------------------------------------
+
+// A row's pages lie end to end with the others' and are cut into shares, and a workgroup takes one share of one of the `pairs`
+// of a key head and 16 NQ of its query heads. All pairs of a share go to one die, next to each other in the launch: the
+// 64 bytes of a position's key under 8 key heads are half of a cache line, its 4 bytes of scales an eighth of
+// one, and what one head's workgroup leaves of them the others find in the die's L2.
+// Shares of more pairs than that leaves room for: as many as there are workgroups for.
+__host__ __device__ __forceinline__ int decode_shares(int64_t pairs) {
+  if (pairs <= kKvDecodeGroups / 8) return static_cast<int>(kKvDecodeGroups / (8 * pairs) * 8);
+  return pairs < kKvDecodeGroups ? static_cast<int>(kKvDecodeGroups / pairs) : 1;
+}
+
+// x, which every lane holds, as a scalar: what hangs on it (pages' addresses) is then computed once for the wave.
+__device__ __forceinline__ int64_t uniform(int64_t x) {
+  const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(x));
+  const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(static_cast<uint64_t>(x) >> 32));
+  return static_cast<int64_t>(static_cast<uint64_t>(hi) << 32 | lo);
+}
 
 template <class T, int D, int NQ>
 __global__ void __launch_bounds__(kThreads, 2) kv_decode_fp4_kernel(KvFp4Args a) {
   typedef Wave4<T, D, NQ> W;
+  typedef Ring4<T, D, NQ> R;
   __shared__ Plan<kWaves> plan;
-  __shared__ Merge<T, D> merge;
+  __shared__ __align__(16) Space<T, D, NQ> lds;
   __shared__ v4u q_lds[W::kShared ? NQ * W::kChunks * 64 : 1];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t* prefix = plan.make(a);
   const int group = group_of<NQ>(a), qg = (a.G + 16 * NQ - 1) / (16 * NQ);
-  const int64_t gh = static_cast<int64_t>(a.Hkv) * qg;
-  const int64_t units = prefix[a.Q] * gh;
-  const int64_t share = unit_share(a, units, gridDim.x);
-  int64_t cur = blockIdx.x * share;
-  const int64_t stop = cur + share < units ? cur + share : units;
+  const int pairs = a.Hkv * qg, shares = decode_shares(pairs), at = blockIdx.x;
+  int pair = pairs < kKvDecodeGroups ? at % pairs : at, which = pairs < kKvDecodeGroups ? at / pairs : 0;
+  if (shares >= 8) {
+    pair = (at >> 3) % pairs;
+    which = (at >> 3) / pairs * 8 + (at & 7);
+  }
+  if (which >= shares) return;
+  const int64_t units = uniform(prefix[a.Q]);
+  const int64_t share = unit_share(a, units, shares);
+  const int64_t stop = which * share + share < units ? which * share + share : units;
   W w;
   w.init();
-  // strides inside a page, whose extent is below 2^31
+  // strides inside a page, whose extent is below 2^31, and what a lane adds to a piece's address
   const int k_pos = static_cast<int>(a.k_pos), v_pos = static_cast<int>(a.v_pos), ks_pos = static_cast<int>(a.ks_pos), vs_pos = static_cast<int>(a.vs_pos);
-  const uint32_t k_at = w.col * k_pos + w.key_at(), ks_at = w.col * ks_pos + w.key_scale_at();
-  const uint32_t v_at = 4 * w.grp * v_pos + w.value_at(), vs_at = 4 * w.grp * vs_pos + w.value_scale_at();
-  while (cur < stop) {
+  const uint32_t k_at = R::code_row(w.lane) * k_pos + R::code_byte(0, w.lane), v_at = R::code_row(w.lane) * v_pos + R::code_byte(1, w.lane);
+  const uint32_t ks_at = R::scale_row(w.lane) * ks_pos + R::scale_byte(w.lane), vs_at = R::scale_row(w.lane) * vs_pos + R::scale_byte(w.lane);
+  // (with more pairs than workgroups there is one share only)
+  for (int64_t cur = which * share; cur < stop || pair + kKvDecodeGroups < pairs;) {
+    if (cur >= stop) {
+      pair += kKvDecodeGroups;
+      cur = which * share;
+      continue;
+    }
     Segment sg;
-    sg.take(a, prefix, gh, &cur, stop);
+    sg.take(a, prefix, 1, &cur, stop);
     const int64_t r = sg.r;
-    const int kvh = sg.g / qg, first = (sg.g % qg) * 16 * NQ, rows = a.G - first < 16 * NQ ? a.G - first : 16 * NQ;
+    const int kvh = pair / qg, first = (pair % qg) * 16 * NQ, rows = a.G - first < 16 * NQ ? a.G - first : 16 * NQ;
     const int start = sg.start, end = sg.end;
-    const int32_t* table = a.table + static_cast<int64_t>(sg.seq) * a.max_pages;
+    const ScalarInts table = scalar_ints(a.table + static_cast<int64_t>(sg.seq) * a.max_pages);
     const int p0 = start >> 6;
     const int t_lo = max(2 * (p0 + sg.pa), start / 32);
     const int t_hi = min(2 * (p0 + sg.pb), (end + 31) / 32);
@@ -282,31 +571,29 @@ __global__ void __launch_bounds__(kThreads, 2) kv_decode_fp4_kernel(KvFp4Args a)
 
     bool bad = false;
     int next = t_lo + wave < t_hi ? table[(t_lo + wave) / 2] : 0;   // entry of the next tile's page, read early
-    int page = 0;
-    // Whole tiles are read: what a page holds outside the window is masked. A tile's page is the same for the wave, so
-    // that addresses are a scalar base and a lane's offset, which never changes.
-    run_tiles(
-        w, t_lo + wave, t_hi, a.c,
-        [&](int t) {
-          page = __builtin_amdgcn_readfirstlane(next);
+    int64_t page = 0;
+    // whole tiles are read: what a page holds outside the window is masked
+    lds.ring.run(
+        w, wave, t_lo + wave, t_hi, a.c,
+        [&](int t, int stage) {
+          page = next;
           if (t + kWaves < t_hi) next = table[(t + kWaves) / 2];
           if (page < 0 || page >= a.P_phys) {   // nothing of it is read; page 0 stands in
             bad = true;
             page = 0;
           }
-          const int first = 32 * (t & 1);
-          PageReads codes(kb + page * a.k_page, k_at), scales(ksb + page * a.ks_page, ks_at);
+          const int first_pos = 32 * (t & 1);
+          const auto codes = R::page_at(kb + page * a.k_page), scales = R::page_at(ksb + page * a.ks_page);
 #pragma unroll
-          for (int b = 0; b < W::kTiles; ++b) w.load_k(b, codes.from((first + 16 * b) * k_pos), scales.from((first + 16 * b) * ks_pos));
+          for (int i = 0; i < R::kCodeCopies; ++i) lds.ring.copy(wave, stage, 0, i, codes, (first_pos + i * R::kCopyRows) * k_pos, k_at);
+          lds.ring.copy_scales(wave, stage, 0, w.lane, scales, first_pos * ks_pos, ks_at);
         },
-        [&](int t) {
-          const int first = 32 * (t & 1);
-          PageReads codes(vb + page * a.v_page, v_at), scales(vsb + page * a.vs_page, vs_at);
+        [&](int t, int stage) {
+          const int first_pos = 32 * (t & 1);
+          const auto codes = R::page_at(vb + page * a.v_page), scales = R::page_at(vsb + page * a.vs_page);
 #pragma unroll
-          for (int j = 0; j < W::kMine; ++j) {
-            const int pos = first + 16 * (j >> 2) + (j & 3);
-            w.load_v(j, codes.from(pos * v_pos), scales.from(pos * vs_pos));
-          }
+          for (int i = 0; i < R::kCodeCopies; ++i) lds.ring.copy(wave, stage, 1, i, codes, (first_pos + i * R::kCopyRows) * v_pos, v_at);
+          lds.ring.copy_scales(wave, stage, 1, w.lane, scales, first_pos * vs_pos, vs_at);
         },
         [&](int t, int* lo, int* hi) {
           *lo = start - 32 * t;
@@ -314,31 +601,101 @@ __global__ void __launch_bounds__(kThreads, 2) kv_decode_fp4_kernel(KvFp4Args a)
         });
     if (bad && w.lane == 0) atomicOr(a.status, kStBadPage);
     const bool whole = sg.pa == 0 && sg.pb == sg.n;
-    const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (sg.pa == 0 ? 1 : 0);
-    join_waves<0, T, D>(merge, w, bad, rows, static_cast<char*>(a.out) + head0 * D * 2, a.lse == nullptr ? nullptr : a.lse + head0,
+    const int64_t slot = 2 * (static_cast<int64_t>(pair) * shares + which) + (sg.pa == 0 ? 1 : 0);
+    join_waves<0, T, D>(lds.merge, w, bad, rows, static_cast<char*>(a.out) + head0 * D * 2, a.lse == nullptr ? nullptr : a.lse + head0,
                         whole ? nullptr : a.part_o + slot * group * D, a.part_ml + slot * group);
+    __syncthreads();   // the rings may be filled again
   }
+}
+
+// Joins the parts of rows that several shares have a part of, and writes the rows that have no pages.
+template <class T, int D, int NQ, int WAVES>
+__global__ void __launch_bounds__(kThreads) kv_decode_fp4_join_kernel(KvFp4Args a) {
+  const int64_t head = join_head<WAVES>(a);
+  if (head < 0) return;
+  const int64_t r = head / a.H;
+  const int h = static_cast<int>(head - r * a.H);
+  const int64_t before = a.prefix[r], n = a.prefix[r + 1] - before;
+  if (n == 0) {
+    int code;
+    row_pages(a, r, &code);
+    fill_row<T, D>(a, head, code != 0, WAVES > 1 ? threadIdx.x : threadIdx.x & 63, 64 * WAVES);
+    return;
+  }
+  const int qg = (a.G + 16 * NQ - 1) / (16 * NQ), shares = decode_shares(static_cast<int64_t>(a.Hkv) * qg);
+  const int64_t share = unit_share(a, a.prefix[a.Q], shares);
+  const int64_t w0 = before / share, w1 = (before + n - 1) / share;
+  if (w0 == w1) return;   // one workgroup had all of it and wrote the output
+  const int kvh = h / a.G, in_kv = h - kvh * a.G;
+  const int64_t slot = 2 * ((static_cast<int64_t>(kvh) * qg + in_kv / (16 * NQ)) * shares + w0);
+  // the first part is its workgroup's last one (slot + 1), the others are first ones
+  join_row<T, D, WAVES>(a, head, in_kv % (16 * NQ), group_of<NQ>(a), w1 - w0 + 1, slot + 1, slot, 2);
 }
 
 // --- selected form ------------------------------------------------------------
 
-// Where a slot's codes and scales lie. A page's strides are below 2^36 (codes, multiples of 16) and 2^32.
-struct SlotAt {
-  uint64_t codes, scales;
-};
-__device__ __forceinline__ SlotAt slot_at(int slot, int64_t page, int64_t pos, int64_t s_page, int64_t s_pos) {
-  const uint32_t in = slot & 63;
-  return {slot_offset(slot, static_cast<uint32_t>(page >> 4), static_cast<uint32_t>(pos >> 4)) << 4,
-          static_cast<uint64_t>(static_cast<uint32_t>(slot) >> 6) * static_cast<uint32_t>(s_page) + in * static_cast<uint32_t>(s_pos)};
+// Offset of a slot's scales: a page's stride is below 2^32.
+__device__ __forceinline__ uint64_t scale_offset(int slot, int64_t page, int64_t pos) {
+  const uint32_t s = slot;
+  return static_cast<uint64_t>(s >> 6) * static_cast<uint32_t>(page) + static_cast<uint64_t>((s & 63) * static_cast<uint32_t>(pos));
 }
+
+// The tiles of a list of slots in LDS, filled up to whole tiles.
+template <class R>
+struct ListTiles {
+  const KvFp4Args& a;
+  const char *k, *v, *ks, *vs;
+  uint32_t k_page, v_page, k_pos, v_pos;   // in units of 16 bytes
+  bool alike;                              // keys and values lie at the same offsets
+  uint32_t codes, scales;                  // LDS addresses of this lane's slots
+  int wave, lane, len;
+  int slot[R::kCodeCopies], scale_slot;    // of the tile that keys() was last called for
+  uint64_t off[R::kCodeCopies], scale_off;
+
+  __device__ __forceinline__ ListTiles(const KvFp4Args& a_, int kvh, int wave_, int lane_, uint32_t list)
+      : a(a_), wave(wave_), lane(lane_), len(0), scale_slot(0), scale_off(0) {
+    k = a.k + kvh * a.k_head + R::code_byte(0, lane);
+    v = a.v + kvh * a.v_head + R::code_byte(1, lane);
+    ks = a.ks + kvh * a.ks_head + R::scale_byte(lane);
+    vs = a.vs + kvh * a.vs_head + R::scale_byte(lane);
+    k_page = static_cast<uint32_t>(a.k_page >> 4);
+    v_page = static_cast<uint32_t>(a.v_page >> 4);
+    k_pos = static_cast<uint32_t>(a.k_pos >> 4);
+    v_pos = static_cast<uint32_t>(a.v_pos >> 4);
+    alike = k_page == v_page && k_pos == v_pos && a.ks_page == a.vs_page && a.ks_pos == a.vs_pos;
+    codes = list + 4 * R::code_row(lane);
+    scales = list + 4 * R::scale_row(lane);
+  }
+
+  __device__ __forceinline__ void keys(R& ring, int t, int stage) {
+    R::read_slots(slot, &scale_slot, codes + 128 * t, scales + 128 * t);
+#pragma unroll
+    for (int i = 0; i < R::kCodeCopies; ++i) {
+      off[i] = slot_offset(slot[i], k_page, k_pos);
+      ring.copy(wave, stage, 0, i, k + (off[i] << 4));
+    }
+    scale_off = scale_offset(scale_slot, a.ks_page, a.ks_pos);
+    ring.copy_scales(wave, stage, 0, lane, ks + scale_off);
+  }
+
+  __device__ __forceinline__ void values(R& ring, int, int stage) {
+    if (!alike) {
+#pragma unroll
+      for (int i = 0; i < R::kCodeCopies; ++i) off[i] = slot_offset(slot[i], v_page, v_pos);
+      scale_off = scale_offset(scale_slot, a.vs_page, a.vs_pos);
+    }
+#pragma unroll
+    for (int i = 0; i < R::kCodeCopies; ++i) ring.copy(wave, stage, 1, i, v + (off[i] << 4));
+    ring.copy_scales(wave, stage, 1, lane, vs + scale_off);
+  }
+};
 
 template <class T, int D, int NQ>
 __global__ void __launch_bounds__(kThreads, 2) kv_selected_fp4_kernel(KvFp4Args a) {
   typedef Wave4<T, D, NQ> W;
-  __shared__ union {
-    SlotAt list[2][kKvSelBlock];   // of keys and values: made once by one lane, not by each that reads there
-    Merge<T, D> merge;
-  } lds;
+  typedef Ring4<T, D, NQ> R;
+  __shared__ int list[kKvSelBlock];
+  __shared__ __align__(16) Space<T, D, NQ> lds;
   __shared__ v4u q_lds[W::kShared ? NQ * W::kChunks * 64 : 1];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int qg = (a.G + 16 * NQ - 1) / (16 * NQ);
@@ -356,43 +713,29 @@ __global__ void __launch_bounds__(kThreads, 2) kv_selected_fp4_kernel(KvFp4Args 
   w.init();
   w.start();
   w.load_q(a.q + p.r * a.q_row + (static_cast<int64_t>(kvh) * a.G + first) * D * 2, rows, a.q_keep, a.q_flip, q_lds);
-  const char *kb = a.k + kvh * a.k_head + w.key_at(), *vb = a.v + kvh * a.v_head + w.value_at();
-  const char *ksb = a.ks + kvh * a.ks_head + w.key_scale_at(), *vsb = a.vs + kvh * a.vs_head + w.value_scale_at();
+  ListTiles<R> tiles_of(a, kvh, wave, w.lane, lds_address(list));
   bool bad = false;
   for (int64_t b0 = p.from; b0 < p.to; b0 += kKvSelBlock) {
     const int len = static_cast<int>(p.to - b0 < kKvSelBlock ? p.to - b0 : kKvSelBlock);
     if (b0 != p.from) __syncthreads();
     bool mine = false;
-    for (int i = threadIdx.x; i < len; i += kThreads) {
-      const int s = a.slots[p.r * a.K + b0 + i];
-      lds.list[0][i] = slot_at(s, a.k_page, a.k_pos, a.ks_page, a.ks_pos);
-      lds.list[1][i] = slot_at(s, a.v_page, a.v_pos, a.vs_page, a.vs_pos);
+    const int tiles = (len + 31) / 32;
+    for (int i = threadIdx.x; i < 32 * tiles; i += kThreads) {
+      const int s = a.slots[p.r * a.K + b0 + min(i, len - 1)];   // the last one again behind the end
+      list[i] = s;
       mine |= s < 0 || s >= 64 * a.P_phys;
     }
     if (__syncthreads_or(mine)) {   // nothing of the list is read
       bad = true;
       break;
     }
-    run_tiles(
-        w, wave, (len + 31) / 32, a.c,
-        [&](int t) {
-#pragma unroll
-          for (int b = 0; b < W::kTiles; ++b) {
-            const SlotAt at = lds.list[0][min(32 * t + 16 * b + w.col, len - 1)];
-            w.load_k(b, LaneReads{kb + at.codes}, LaneReads{ksb + at.scales});
-          }
-        },
-        [&](int t) {
-#pragma unroll
-          for (int j = 0; j < W::kMine; ++j) {
-            const SlotAt at = lds.list[1][min(32 * t + w.mine(j), len - 1)];
-            w.load_v(j, LaneReads{vb + at.codes}, LaneReads{vsb + at.scales});
-          }
-        },
-        [&](int t, int* lo, int* hi) {
-          *lo = 0;
-          *hi = len - 32 * t;
-        });
+    tiles_of.len = len;
+    lds.ring.run(w, wave, wave, tiles, a.c, [&](int t, int stage) { tiles_of.keys(lds.ring, t, stage); },
+                 [&](int t, int stage) { tiles_of.values(lds.ring, t, stage); },
+                 [&](int t, int* lo, int* hi) {
+                   *lo = 0;
+                   *hi = tiles_of.len - 32 * t;
+                 });
   }
   if (bad && threadIdx.x == 0) atomicOr(a.status, kStBadPage);
   const int64_t part = p.item * group_of<NQ>(a);
@@ -405,18 +748,19 @@ __global__ void __launch_bounds__(kThreads, 2) kv_selected_fp4_kernel(KvFp4Args 
 template <class T, int D, int NQ>
 void decode_on(KvFp4Args a, hipStream_t st) {
   const int groups = kKvDecodeGroups;
+  // what one more part costs (its sums' bytes, its turn in the joining of its heads) by what a page takes, both in ns
   const double page_ns = NQ > 1 ? 1000 : 100 + 2.75 * D;
+  const double pairs = static_cast<double>(a.Hkv) * kv_head_groups(D, a.G);
   const double sums_ns = kv_group_rows(D, a.G) * D * 4 * 0.8e-3, turn_ns = a.Q * a.H <= kJoinHeads ? 20 : 80;
-  const double pairs = static_cast<double>(a.Q) * a.Hkv * kv_head_groups(D, a.G);
-  a.join_cost = static_cast<uint32_t>((sums_ns + turn_ns / pairs) / page_ns * 65536.0);
+  const double cost = (sums_ns * pairs + turn_ns / static_cast<double>(a.Q)) / page_ns * 65536.0;
+  a.join_cost = cost < 8388608.0 ? static_cast<uint32_t>(cost) : 8388608u;
   if (a.Q > kKvPlanRows) kv_plan_kernel<<<dim3(1), dim3(1024), 0, st>>>(a);
   kv_decode_fp4_kernel<T, D, NQ><<<dim3(groups), dim3(kThreads), 0, st>>>(a);
   const int64_t heads = a.Q * a.H;
   if (heads <= kJoinHeads)
-    kv_decode_join_kernel<T, D, kWaves><<<dim3(static_cast<unsigned>(heads)), dim3(kThreads), 0, st>>>(a, 16 * NQ, groups);
+    kv_decode_fp4_join_kernel<T, D, NQ, kWaves><<<dim3(static_cast<unsigned>(heads)), dim3(kThreads), 0, st>>>(a);
   else
-    kv_decode_join_kernel<T, D, 1>
-        <<<dim3(static_cast<unsigned>((heads + kWaves - 1) / kWaves)), dim3(kThreads), 0, st>>>(a, 16 * NQ, groups);
+    kv_decode_fp4_join_kernel<T, D, NQ, 1><<<dim3(static_cast<unsigned>((heads + kWaves - 1) / kWaves)), dim3(kThreads), 0, st>>>(a);
 }
 
 template <class T, int D, int NQ>
