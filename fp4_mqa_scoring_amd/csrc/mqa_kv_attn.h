@@ -369,14 +369,14 @@ struct Wave {
 // tile's keys are loaded into the registers that the first product has just read,
 // its values into those that the second has.
 
-// Joins the four waves' results in LDS and writes the heads' outputs, or their partial
+// Joins a workgroup's waves' results in LDS and writes the heads' outputs, or their partial
 // sums where part_o is not null. `bad`: an invalid page or slot was met.
-template <class T, int D>
+template <class T, int D, int WAVES = kWaves>
 struct Merge {
   static constexpr int kPart = D < 128 ? D : 128;   // dims of a head at a time, so that LDS holds two workgroups or more
   static constexpr int kPitch = kPart + 4;
-  float o[kWaves][16][kPitch];
-  float2 ml[kWaves][16];
+  float o[WAVES][16][kPitch];
+  float2 ml[WAVES][16];
   float2 fin[16];
 
   template <int N = 0, class W>   // N: which 16 heads
@@ -387,16 +387,16 @@ struct Merge {
     const float mine = groups_sum(w.l[N]);
     if (w.grp == 0) ml[wave][w.col] = make_float2(w.m[N], bad ? __builtin_nanf("") : mine);
     __syncthreads();
-    float2 x[kWaves];
+    float2 x[WAVES];
     float top = -__builtin_inff(), total = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kWaves; ++i) {
+    for (int i = 0; i < WAVES; ++i) {
       x[i] = ml[i][w.col];
       top = fmaxf(top, x[i].x);
     }
     const float ref = top == -__builtin_inff() ? 0.0f : top;
 #pragma unroll
-    for (int i = 0; i < kWaves; ++i) total += x[i].y * __builtin_amdgcn_exp2f(x[i].x - ref);
+    for (int i = 0; i < WAVES; ++i) total += x[i].y * __builtin_amdgcn_exp2f(x[i].x - ref);
     const float f = __builtin_amdgcn_exp2f(w.m[N] - ref);
     if (wave == 0 && w.grp == 0) fin[w.col] = make_float2(top, total);
     constexpr int kT = kPart / 16;   // matrix tiles of a part
@@ -411,13 +411,13 @@ struct Merge {
               v4f{w.o[N][t0 + t][i] * f, w.o[N][t0 + t + 1][i] * f, w.o[N][t0 + t + 2][i] * f,
                   w.o[N][t0 + t + 3][i] * f};
       __syncthreads();
-      for (int e = threadIdx.x; e < 16 * kPart / 4; e += kThreads) {
+      for (int e = threadIdx.x; e < 16 * kPart / 4; e += 64 * WAVES) {
         const int head = e / (kPart / 4), at = 4 * (e % (kPart / 4));
         const int d = at / kT * W::kDims + t0 + at % kT;
         if (head >= rows) continue;
         v4f sum = *reinterpret_cast<const v4f*>(&o[0][head][at]);
 #pragma unroll
-        for (int i = 1; i < kWaves; ++i) sum += *reinterpret_cast<const v4f*>(&o[i][head][at]);
+        for (int i = 1; i < WAVES; ++i) sum += *reinterpret_cast<const v4f*>(&o[i][head][at]);
         const float2 e2 = fin[head];
         if (part_o != nullptr) {
           *reinterpret_cast<v4f*>(part_o + static_cast<int64_t>(head) * D + d) = sum;
@@ -614,8 +614,8 @@ struct Segment {
   int seq, start, end;
 
   // The segment at unit `cur`, which it advances.
-  __device__ __forceinline__ void take(const KvAttnArgs& a, const int64_t* prefix, int64_t gh, int64_t* cur,
-                                       int64_t stop) {
+  template <class ARGS>
+  __device__ __forceinline__ void take(ARGS& a, const int64_t* prefix, int64_t gh, int64_t* cur, int64_t stop) {
     // the row that the unit belongs to: the last one whose prefix is not above it
     int64_t lo = 0, hi = a.Q;
     const int64_t page_unit = *cur / gh;

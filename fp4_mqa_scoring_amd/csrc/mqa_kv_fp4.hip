@@ -11,6 +11,9 @@
 // compiler would wait for every copy in flight before an LDS read that it cannot prove apart.
 #include "mqa_kv_attn.h"
 
+#ifndef MIXV
+#define MIXV 5
+#endif
 namespace mqa {
 namespace {
 
@@ -70,7 +73,7 @@ struct Wave4 : Wave<T, false, D, NQ, 32, (NQ > 1), (NQ > 1 ? 8 : 0)> {
     if constexpr (kShared) {
       q_at = lds_address(lds) + 16 * this->lane;
       __syncthreads();
-      for (int x = threadIdx.x >> 6; x < NQ * kChunks; x += kWaves)
+      for (int x = threadIdx.x >> 6; x < NQ * kChunks; x += blockDim.x >> 6)
         lds[64 * x + this->lane] = query(p, x / kChunks, x % kChunks, rows, keep, flip);
       __syncthreads();
     } else {
@@ -127,68 +130,87 @@ struct Wave4 : Wave<T, false, D, NQ, 32, (NQ > 1), (NQ > 1 ? 8 : 0)> {
       for (int a = 0; a < kTiles; ++a) s[a] = T::mfma(x[c][a], y[c], s[a]);
   }
 
-  // Weights of query tile N while the scores of the next one are made.
   template <int N>
-  __device__ __forceinline__ void weigh_tiles(v4f (&s)[kTiles], const v4u (&x)[kSteps][kTiles], float c, bool edge, uint32_t inside,
-                                              P (&p)[NQ]) {
-    v4f after[kTiles];
-    if constexpr (N + 1 < NQ) score_tile<N + 1>(after, x, 0);
-    weigh<N>(s, c, edge, inside, p[N]);
-    if constexpr (N + 1 < NQ) weigh_tiles<N + 1>(after, x, c, edge, inside, p);
-  }
-
-  // The weights of the tile that lies in kc and kb, packed as the second product's operand.
-  __device__ __forceinline__ void weights_of_tile(float c, bool edge, uint32_t inside, P (&p)[NQ]) {
-    v4u x[kSteps][kTiles];
-    if constexpr (kChunks <= 4) {
-#pragma unroll
-      for (int i = 0; i < kSteps; ++i) keys_of(i, x[i]);
-      v4f s[kTiles];
-      score_tile<0>(s, x, 0);
-      weigh_tiles<0>(s, x, c, edge, inside, p);
-    } else {   // D = 256: half of the dims at a time
-      static_assert(NQ <= 2, "two tiles of queries at most");
-      v4f s[2][kTiles];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-#pragma unroll
-        for (int i = 0; i < kSteps; ++i) keys_of(4 * h + i, x[i]);
-        score_tile<0>(s[0], x, h);
-        if constexpr (NQ > 1) score_tile<NQ - 1>(s[1], x, h);
-      }
-      weigh<0>(s[0], c, edge, inside, p[0]);
-      if constexpr (NQ > 1) weigh<NQ - 1>(s[1], c, edge, inside, p[NQ - 1]);
+  __device__ __forceinline__ void score_tiles(v4f (&s)[NQ][kTiles], const v4u (&x)[kSteps][kTiles], int h) const {
+    if constexpr (N < NQ) {
+      score_tile<N>(s[N], x, h);
+      score_tiles<N + 1>(s, x, h);
     }
   }
 
-  // Scores of query tile N to weights, as Wave::weights, for itself alone.
-  template <int N>
-  __device__ __forceinline__ void weigh(v4f (&s)[kTiles], float c, bool edge, uint32_t inside, P& p) {
-    constexpr float kSlack = NQ > 1 ? 8.0f : 0.0f;
-    __asm__ __volatile__("s_nop 7" : "+v"(s[0]), "+v"(s[1]));   // as settle()
+  // Scores of the tile that lies in kc and kb, 128 dims at a time.
+  __device__ __forceinline__ void scores(v4f (&s)[NQ][kTiles]) const {
+#pragma unroll
+    for (int h = 0; h < (kChunks + 3) / 4; ++h) {
+      v4u x[kSteps][kTiles];
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) keys_of(4 * h + i, x[i]);
+      score_tiles<0>(s, x, h);
+    }
+    settle(s);
+  }
+
+  // First half of Wave::weights: the mask of a window's edge, and the running maximum.
+  __device__ __forceinline__ void follow_maximum(v4f (&s)[NQ][kTiles], float c, bool edge, uint32_t inside) {
     if (edge) {   // a score of -infinity is a weight of 0, as c > 0
       const uint32_t in = Base::here(inside);
 #pragma unroll
-      for (int j = 0; j < kMine; ++j) s[j >> 2][j & 3] = (in >> j & 1) ? s[j >> 2][j & 3] : -__builtin_inff();
+      for (int n = 0; n < NQ; ++n)
+#pragma unroll
+        for (int j = 0; j < kMine; ++j) s[n][j >> 2][j & 3] = (in >> j & 1) ? s[n][j >> 2][j & 3] : -__builtin_inff();
     }
-    float top = max3(max3(max3(s[0][0], s[0][1], s[0][2]), s[0][3], s[1][0]), s[1][1], max2(s[1][2], s[1][3]));
-    top = Base::kBias == 0 ? groups_max(top) * c : __builtin_fmaf(groups_max(top), c, static_cast<float>(-Base::kBias));
-    float& m = this->m[N];
-    if (__any(top > m + kSlack)) {
-      const float to = fmaxf(m, top);
-      const float f = to == m ? 1.0f : __builtin_amdgcn_exp2f(m - to);
-      m = to;
-      this->l[N] *= f;
+    // A lane's own scores tell whether the maximum moves; the other lanes' are asked for only if it does.
+    float top[NQ];
+    bool rise = false;
 #pragma unroll
-      for (int t = 0; t < kDims; ++t) this->o[N][t] *= f;
+    for (int n = 0; n < NQ; ++n) {
+      top[n] = max3(max3(max3(s[n][0][0], s[n][0][1], s[n][0][2]), s[n][0][3], s[n][1][0]), s[n][1][1], max2(s[n][1][2], s[n][1][3]));
+      const float least = static_cast<float>(Base::kBias + (NQ > 1 ? 8 : 0));
+      rise |= (least == 0.0f ? top[n] * c : __builtin_fmaf(top[n], c, -least)) > this->m[n];
     }
-    const float ref = m == -__builtin_inff() ? 0.0f : m;
-    float w[kMine];
+    if (__any(rise)) {
 #pragma unroll
-    for (int j = 0; j < kMine; ++j) w[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j >> 2][j & 3], c, -ref));
-    this->l[N] += ((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7]));
+      for (int n = 0; n < NQ; ++n) {
+        const float mine = groups_max(top[n]);
+        const float to = fmaxf(this->m[n], Base::kBias == 0 ? mine * c : __builtin_fmaf(mine, c, static_cast<float>(-Base::kBias)));
+        const float f = to == this->m[n] ? 1.0f : __builtin_amdgcn_exp2f(this->m[n] - to);
+        this->m[n] = to;
+        this->l[n] *= f;
 #pragma unroll
-    for (int j = 0; j < kMine / 2; ++j) p[j] = T::pack(w[2 * j], w[2 * j + 1]);
+        for (int t = 0; t < kDims; ++t) this->o[n][t] *= f;
+      }
+    }
+  }
+
+  // The running maximum begins at the least number: a score of -infinity under it weighs 0.
+  __device__ __forceinline__ void start() {
+    Base::start();
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) this->m[n] = -3.402823466e38f;
+  }
+
+  // Second half: weights, their sums and the weighted values, without a branch, so that vector and matrix
+  // instructions of the two products mix.
+  __device__ __forceinline__ void add_weighted(const v4f (&s)[NQ][kTiles], float c) {
+    P p[NQ];
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+      float w[kMine];
+#pragma unroll
+      for (int j = 0; j < kMine; ++j) w[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n][j >> 2][j & 3], c, -this->m[n]));
+      this->l[n] += ((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7]));
+#pragma unroll
+      for (int j = 0; j < kMine / 2; ++j) p[n][j] = T::pack(w[2 * j], w[2 * j + 1]);
+    }
+    add_values(p);
+    if constexpr (NQ > 1) {
+      __builtin_amdgcn_sched_group_barrier(0x2, 40, 0);
+#pragma unroll
+      for (int i = 0; i < NQ * kDims; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x2, MIXV, 0);
+      }
+    }
   }
 
   // Values outside the window: every code is a number, so a scale of nearly 0 will do.
@@ -234,7 +256,11 @@ struct Wave4 : Wave<T, false, D, NQ, 32, (NQ > 1), (NQ > 1 ? 8 : 0)> {
 
 // --- a wave's stream of tiles ---------------------------------------------------
 
-// LDS of the four waves' rings. A piece is a tile's keys or values: 32 rows of D / 2 bytes of codes, one after another,
+// Waves of a workgroup. Up to 16 heads per key head the vector unit waits for its own results much of the time, and
+// four waves to a SIMD find registers and LDS.
+constexpr int ring_waves(int D, int NQ) { return NQ == 1 && D <= 128 ? 8 : 4; }
+
+// LDS of the waves' rings. A piece is a tile's keys or values: 32 rows of D / 2 bytes of codes, one after another,
 // and their scales, one word a row (two with D = 256; with D = 64 the upper half is empty).
 //
 // kDepth: as many tiles as LDS holds for two workgroups of a compute unit.
@@ -243,7 +269,8 @@ struct Ring4 {
   typedef Wave4<T, D, NQ> W;
   static constexpr int kRow = D / 2, kCodes = 32 * kRow, kScaleWords = D == 256 ? 2 : 1;
   static constexpr int kPiece = kCodes + 32 * 4 * kScaleWords;
-  static constexpr int kDepth = D == 64 ? 4 : D == 128 ? (NQ == 1 ? 4 : 3) : (NQ == 1 ? 2 : 1);
+  static constexpr int kWaves = ring_waves(D, NQ);
+  static constexpr int kDepth = D == 64 ? (NQ == 1 ? 3 : 4) : D == 128 ? (NQ == 1 ? 2 : 3) : (NQ == 1 ? 2 : 1);
   static constexpr int kLanes = kRow / 16;                   // lanes that copy one row
   static constexpr int kCopyRows = 64 / kLanes;              // rows of one copy of 1 KiB
   static constexpr int kCodeCopies = kCodes / 1024, kCopies = kCodeCopies + 1;   // per piece
@@ -456,14 +483,15 @@ struct Ring4 {
       }
       const int left = 2 * (tiles - i) - 1;   // pieces behind this one
       const uint32_t at = ring + 2 * kPiece * stage;
-      typename W::P p[NQ];
       arrived(left);
       read_keys(w, at, k_shift);
       if (i + kDepth < tiles) {
         keys(t + kWaves * kDepth, stage);
         __asm__ __volatile__("" ::: "memory");
       }
-      w.weights_of_tile(c, edge, inside, p);
+      v4f s[NQ][2];
+      w.scores(s);
+      w.follow_maximum(s, c, edge, inside);
       // the keys that were just asked for are younger too
       arrived(i + kDepth < tiles ? 2 * kDepth : 0);
       read_values(w, at + kPiece, v_shift);
@@ -472,7 +500,7 @@ struct Ring4 {
         __asm__ __volatile__("" ::: "memory");
       }
       if (edge) w.clear_outside(inside);
-      w.add_values(p);
+      w.add_weighted(s, c);
       stage = stage + 1 < kDepth ? stage + 1 : 0;
     }
   }
@@ -483,8 +511,8 @@ template <int NQ>
 __device__ __forceinline__ int group_of(const KvFp4Args& a) { return a.G < 16 * NQ ? a.G : 16 * NQ; }
 
 // Joins the waves' results, 16 heads at a time.
-template <int N, class T, int D, class W>
-__device__ __forceinline__ void join_waves(Merge<T, D>& merge, W& w, bool bad, int rows, char* out, float* lse, float* part_o,
+template <int N, class T, int D, class MERGE, class W>
+__device__ __forceinline__ void join_waves(MERGE& merge, W& w, bool bad, int rows, char* out, float* lse, float* part_o,
                                            float2* part_ml) {
   if constexpr (N < W::kQueries) {
     if (16 * N >= rows) return;
@@ -499,7 +527,7 @@ __device__ __forceinline__ void join_waves(Merge<T, D>& merge, W& w, bool bad, i
 template <class T, int D, int NQ>
 union Space {
   Ring4<T, D, NQ> ring;
-  Merge<T, D> merge;
+  Merge<T, D, ring_waves(D, NQ)> merge;
 };
 
 // --- decode form --------------------------------------------------------------
@@ -521,11 +549,20 @@ __device__ __forceinline__ int64_t uniform(int64_t x) {
   return static_cast<int64_t>(static_cast<uint64_t>(hi) << 32 | lo);
 }
 
+// The kernel's arguments, read from memory anew: kept in scalar registers over a segment, those that only its beginning
+// and end need push the streaming loop's own out of them.
+typedef const __attribute__((address_space(4))) KvFp4Args ArgsInMemory;
+__device__ __forceinline__ ArgsInMemory& fresh_args() {
+  auto p = (ArgsInMemory*)__builtin_amdgcn_kernarg_segment_ptr();
+  __asm__ __volatile__("" : "+s"(p));
+  return *p;
+}
+
 template <class T, int D, int NQ>
-__global__ void __launch_bounds__(kThreads, 2) kv_decode_fp4_kernel(KvFp4Args a) {
+__global__ void __launch_bounds__(64 * ring_waves(D, NQ), ring_waves(D, NQ) / 2) kv_decode_fp4_kernel(KvFp4Args a) {
   typedef Wave4<T, D, NQ> W;
   typedef Ring4<T, D, NQ> R;
-  __shared__ Plan<kWaves> plan;
+  __shared__ Plan<R::kWaves> plan;
   __shared__ __align__(16) Space<T, D, NQ> lds;
   __shared__ v4u q_lds[W::kShared ? NQ * W::kChunks * 64 : 1];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -554,43 +591,46 @@ __global__ void __launch_bounds__(kThreads, 2) kv_decode_fp4_kernel(KvFp4Args a)
       cur = which * share;
       continue;
     }
+    ArgsInMemory& m = fresh_args();
     Segment sg;
-    sg.take(a, prefix, 1, &cur, stop);
+    sg.take(m, prefix, 1, &cur, stop);
     const int64_t r = sg.r;
-    const int kvh = pair / qg, first = (pair % qg) * 16 * NQ, rows = a.G - first < 16 * NQ ? a.G - first : 16 * NQ;
+    const int kvh = pair / qg, first = (pair % qg) * 16 * NQ, rows = m.G - first < 16 * NQ ? m.G - first : 16 * NQ;
     const int start = sg.start, end = sg.end;
-    const ScalarInts table = scalar_ints(a.table + static_cast<int64_t>(sg.seq) * a.max_pages);
+    const ScalarInts table = scalar_ints(m.table + static_cast<int64_t>(sg.seq) * m.max_pages);
     const int p0 = start >> 6;
     const int t_lo = max(2 * (p0 + sg.pa), start / 32);
     const int t_hi = min(2 * (p0 + sg.pb), (end + 31) / 32);
-    const char *kb = a.k + kvh * a.k_head, *vb = a.v + kvh * a.v_head;
-    const char *ksb = a.ks + kvh * a.ks_head, *vsb = a.vs + kvh * a.vs_head;
-    const int64_t head0 = r * a.H + static_cast<int64_t>(kvh) * a.G + first;
+    const char *kb = m.k + kvh * m.k_head, *vb = m.v + kvh * m.v_head;
+    const char *ksb = m.ks + kvh * m.ks_head, *vsb = m.vs + kvh * m.vs_head;
+    const int64_t head0 = r * m.H + static_cast<int64_t>(kvh) * m.G + first;
     w.start();
-    w.load_q(a.q + r * a.q_row + (static_cast<int64_t>(kvh) * a.G + first) * D * 2, rows, a.q_keep, a.q_flip, q_lds);
+    w.load_q(m.q + r * m.q_row + (static_cast<int64_t>(kvh) * m.G + first) * D * 2, rows, m.q_keep, m.q_flip, q_lds);
 
+    const int64_t k_page = m.k_page, v_page = m.v_page, ks_page = m.ks_page, vs_page = m.vs_page;
+    const int pages = static_cast<int>(m.P_phys);
     bool bad = false;
     int next = t_lo + wave < t_hi ? table[(t_lo + wave) / 2] : 0;   // entry of the next tile's page, read early
     int64_t page = 0;
     // whole tiles are read: what a page holds outside the window is masked
     lds.ring.run(
-        w, wave, t_lo + wave, t_hi, a.c,
+        w, wave, t_lo + wave, t_hi, m.c,
         [&](int t, int stage) {
           page = next;
-          if (t + kWaves < t_hi) next = table[(t + kWaves) / 2];
-          if (page < 0 || page >= a.P_phys) {   // nothing of it is read; page 0 stands in
+          if (t + R::kWaves < t_hi) next = table[(t + R::kWaves) / 2];
+          if (page < 0 || page >= pages) {   // nothing of it is read; page 0 stands in
             bad = true;
             page = 0;
           }
           const int first_pos = 32 * (t & 1);
-          const auto codes = R::page_at(kb + page * a.k_page), scales = R::page_at(ksb + page * a.ks_page);
+          const auto codes = R::page_at(kb + page * k_page), scales = R::page_at(ksb + page * ks_page);
 #pragma unroll
           for (int i = 0; i < R::kCodeCopies; ++i) lds.ring.copy(wave, stage, 0, i, codes, (first_pos + i * R::kCopyRows) * k_pos, k_at);
           lds.ring.copy_scales(wave, stage, 0, w.lane, scales, first_pos * ks_pos, ks_at);
         },
         [&](int t, int stage) {
           const int first_pos = 32 * (t & 1);
-          const auto codes = R::page_at(vb + page * a.v_page), scales = R::page_at(vsb + page * a.vs_page);
+          const auto codes = R::page_at(vb + page * v_page), scales = R::page_at(vsb + page * vs_page);
 #pragma unroll
           for (int i = 0; i < R::kCodeCopies; ++i) lds.ring.copy(wave, stage, 1, i, codes, (first_pos + i * R::kCopyRows) * v_pos, v_at);
           lds.ring.copy_scales(wave, stage, 1, w.lane, scales, first_pos * vs_pos, vs_at);
@@ -599,11 +639,12 @@ __global__ void __launch_bounds__(kThreads, 2) kv_decode_fp4_kernel(KvFp4Args a)
           *lo = start - 32 * t;
           *hi = end - 32 * t;
         });
-    if (bad && w.lane == 0) atomicOr(a.status, kStBadPage);
+    ArgsInMemory& e = fresh_args();
+    if (bad && w.lane == 0) atomicOr(e.status, kStBadPage);
     const bool whole = sg.pa == 0 && sg.pb == sg.n;
     const int64_t slot = 2 * (static_cast<int64_t>(pair) * shares + which) + (sg.pa == 0 ? 1 : 0);
-    join_waves<0, T, D>(lds.merge, w, bad, rows, static_cast<char*>(a.out) + head0 * D * 2, a.lse == nullptr ? nullptr : a.lse + head0,
-                        whole ? nullptr : a.part_o + slot * group * D, a.part_ml + slot * group);
+    join_waves<0, T, D>(lds.merge, w, bad, rows, static_cast<char*>(e.out) + head0 * D * 2, e.lse == nullptr ? nullptr : e.lse + head0,
+                        whole ? nullptr : e.part_o + slot * group * D, e.part_ml + slot * group);
     __syncthreads();   // the rings may be filled again
   }
 }
@@ -691,7 +732,7 @@ struct ListTiles {
 };
 
 template <class T, int D, int NQ>
-__global__ void __launch_bounds__(kThreads, 2) kv_selected_fp4_kernel(KvFp4Args a) {
+__global__ void __launch_bounds__(64 * ring_waves(D, NQ), ring_waves(D, NQ) / 2) kv_selected_fp4_kernel(KvFp4Args a) {
   typedef Wave4<T, D, NQ> W;
   typedef Ring4<T, D, NQ> R;
   __shared__ int list[kKvSelBlock];
@@ -706,7 +747,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv_selected_fp4_kernel(KvFp4Args 
   const int kvh = p.g / qg, first = (p.g % qg) * 16 * NQ, rows = a.G - first < 16 * NQ ? a.G - first : 16 * NQ;
   const int64_t head0 = p.r * a.H + static_cast<int64_t>(kvh) * a.G + first;
   if (!any) {
-    for (int h = 0; h < rows; ++h) fill_row<T, D>(a, head0 + h, p.n != 0, threadIdx.x, kThreads);
+    for (int h = 0; h < rows; ++h) fill_row<T, D>(a, head0 + h, p.n != 0, threadIdx.x, 64 * R::kWaves);
     return;
   }
   W w;
@@ -720,7 +761,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv_selected_fp4_kernel(KvFp4Args 
     if (b0 != p.from) __syncthreads();
     bool mine = false;
     const int tiles = (len + 31) / 32;
-    for (int i = threadIdx.x; i < 32 * tiles; i += kThreads) {
+    for (int i = threadIdx.x; i < 32 * tiles; i += 64 * R::kWaves) {
       const int s = a.slots[p.r * a.K + b0 + min(i, len - 1)];   // the last one again behind the end
       list[i] = s;
       mine |= s < 0 || s >= 64 * a.P_phys;
@@ -755,7 +796,7 @@ void decode_on(KvFp4Args a, hipStream_t st) {
   const double cost = (sums_ns * pairs + turn_ns / static_cast<double>(a.Q)) / page_ns * 65536.0;
   a.join_cost = cost < 8388608.0 ? static_cast<uint32_t>(cost) : 8388608u;
   if (a.Q > kKvPlanRows) kv_plan_kernel<<<dim3(1), dim3(1024), 0, st>>>(a);
-  kv_decode_fp4_kernel<T, D, NQ><<<dim3(groups), dim3(kThreads), 0, st>>>(a);
+  kv_decode_fp4_kernel<T, D, NQ><<<dim3(groups), dim3(64 * ring_waves(D, NQ)), 0, st>>>(a);
   const int64_t heads = a.Q * a.H;
   if (heads <= kJoinHeads)
     kv_decode_fp4_join_kernel<T, D, NQ, kWaves><<<dim3(static_cast<unsigned>(heads)), dim3(kThreads), 0, st>>>(a);
@@ -767,7 +808,7 @@ template <class T, int D, int NQ>
 void selected_on(const KvFp4Args& a, hipStream_t st) {
   const int64_t items = a.Q * a.Hkv * kv_head_groups(D, a.G) * a.splits;
   const unsigned grid = static_cast<unsigned>((items + 7) / 8 * 8);
-  kv_selected_fp4_kernel<T, D, NQ><<<dim3(grid), dim3(kThreads), 0, st>>>(a);
+  kv_selected_fp4_kernel<T, D, NQ><<<dim3(grid), dim3(64 * ring_waves(D, NQ)), 0, st>>>(a);
   if (a.splits > 1)
     kv_selected_join_kernel<T, D, 1>
         <<<dim3(static_cast<unsigned>((a.Q * a.H + kWaves - 1) / kWaves)), dim3(kThreads), 0, st>>>(a, 16 * NQ);
