@@ -11,9 +11,6 @@
 // compiler would wait for every copy in flight before an LDS read that it cannot prove apart.
 #include "mqa_kv_attn.h"
 
-#ifndef MIXV
-#define MIXV 5
-#endif
 namespace mqa {
 namespace {
 
@@ -51,7 +48,7 @@ struct Wave4 : Wave<T, false, D, NQ, 32, (NQ > 1), (NQ > 1 ? 8 : 0)> {
   static constexpr int kSteps = kChunks < 4 ? kChunks : 4;   // matrix steps over the dims at once
   static constexpr int kWords4 = D == 256 ? 2 : 1;       // words of a lane's value (half of one with D = 64)
 
-  uint32_t q_at;                                         // LDS address of the queries, from this lane's on
+  const v4u* q_lane;                                     // the queries in LDS, from this lane's on
   uint32_t kc[kTiles][kKeyWords], kb[kTiles][kKeyBlocks];
   uint32_t vc[kMine][kWords4], vb[kMine];
 
@@ -71,7 +68,7 @@ struct Wave4 : Wave<T, false, D, NQ, 32, (NQ > 1), (NQ > 1 ? 8 : 0)> {
   // Loads the queries: into registers, or by the whole workgroup into `lds` (NQ * kChunks * 64 of it), between barriers.
   __device__ __forceinline__ void load_q(const char* p, int rows, uint32_t keep, uint32_t flip, v4u* lds) {
     if constexpr (kShared) {
-      q_at = lds_address(lds) + 16 * this->lane;
+      q_lane = lds + this->lane;
       __syncthreads();
       for (int x = threadIdx.x >> 6; x < NQ * kChunks; x += blockDim.x >> 6)
         lds[64 * x + this->lane] = query(p, x / kChunks, x % kChunks, rows, keep, flip);
@@ -81,25 +78,6 @@ struct Wave4 : Wave<T, false, D, NQ, 32, (NQ > 1), (NQ > 1 ? 8 : 0)> {
       for (int n = 0; n < NQ; ++n)
 #pragma unroll
         for (int c = 0; c < kChunks; ++c) q[n][c] = query(p, n, c, rows, keep, flip);
-    }
-  }
-
-  // Steps 4 h .. of query tile N.
-  template <int N>
-  __device__ __forceinline__ void read_q(int h, v4u (&y)[4]) const {
-    constexpr int kOff = N * kChunks * 1024;
-    if constexpr (kChunks == 2) {
-      __asm__ __volatile__("ds_read_b128 %0, %2 offset:%3\n\tds_read_b128 %1, %2 offset:%4\n\ts_waitcnt lgkmcnt(0)"
-                           : "=&v"(y[0]), "=&v"(y[1])
-                           : "v"(q_at), "n"(kOff), "n"(kOff + 1024)
-                           : "memory");
-    } else {
-      __asm__ __volatile__(
-          "ds_read_b128 %0, %4 offset:%5\n\tds_read_b128 %1, %4 offset:%6\n\t"
-          "ds_read_b128 %2, %4 offset:%7\n\tds_read_b128 %3, %4 offset:%8\n\ts_waitcnt lgkmcnt(0)"
-          : "=&v"(y[0]), "=&v"(y[1]), "=&v"(y[2]), "=&v"(y[3])
-          : "v"(q_at + 4096 * h), "n"(kOff), "n"(kOff + 1024), "n"(kOff + 2048), "n"(kOff + 3072)
-          : "memory");
     }
   }
 
@@ -115,11 +93,10 @@ struct Wave4 : Wave<T, false, D, NQ, 32, (NQ > 1), (NQ > 1 ? 8 : 0)> {
   template <int N>
   __device__ __forceinline__ void score_tile(v4f (&s)[kTiles], const v4u (&x)[kSteps][kTiles], int h) const {
     v4u y[4];
-    if constexpr (kShared) {
-      read_q<N>(h, y);
-    } else {
 #pragma unroll
-      for (int c = 0; c < kSteps; ++c) y[c] = q[N][4 * h + c];
+    for (int c = 0; c < kSteps; ++c) {
+      if constexpr (kShared) y[c] = q_lane[(N * kChunks + 4 * h + c) * 64];
+      else y[c] = q[N][4 * h + c];
     }
     if (h == 0)
 #pragma unroll
@@ -189,8 +166,7 @@ struct Wave4 : Wave<T, false, D, NQ, 32, (NQ > 1), (NQ > 1 ? 8 : 0)> {
     for (int n = 0; n < NQ; ++n) this->m[n] = -3.402823466e38f;
   }
 
-  // Second half: weights, their sums and the weighted values, without a branch, so that vector and matrix
-  // instructions of the two products mix.
+  // Second half: weights, their sums and the weighted values.
   __device__ __forceinline__ void add_weighted(const v4f (&s)[NQ][kTiles], float c) {
     P p[NQ];
 #pragma unroll
@@ -203,14 +179,6 @@ struct Wave4 : Wave<T, false, D, NQ, 32, (NQ > 1), (NQ > 1 ? 8 : 0)> {
       for (int j = 0; j < kMine / 2; ++j) p[n][j] = T::pack(w[2 * j], w[2 * j + 1]);
     }
     add_values(p);
-    if constexpr (NQ > 1) {
-      __builtin_amdgcn_sched_group_barrier(0x2, 40, 0);
-#pragma unroll
-      for (int i = 0; i < NQ * kDims; ++i) {
-        __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(0x2, MIXV, 0);
-      }
-    }
   }
 
   // Values outside the window: every code is a number, so a scale of nearly 0 will do.
