@@ -224,36 +224,41 @@ struct Wave4 : Wave<T, false, D, NQ, 32, (NQ > 1), (NQ > 1 ? 8 : 0)> {
 
 // --- a wave's stream of tiles ---------------------------------------------------
 
-// Waves of a workgroup. Up to 16 heads per key head the vector unit waits for its own results much of the time, and
-// four waves to a SIMD find registers and LDS.
-constexpr int ring_waves(int D, int NQ) { return NQ == 1 && D <= 128 ? 8 : 4; }
+// Waves of a workgroup of NH key heads, and workgroups of a launch: four waves of it to a SIMD where registers and LDS
+// leave room for them, two otherwise.
+constexpr int ring_waves(int D, int NQ, int NH) { return NH > 1 || (NQ == 1 && D <= 128) ? 8 : 4; }
+constexpr int ring_groups(int NH) { return kKvDecodeGroups / NH; }
+constexpr int ring_waves_per_simd(int D, int NQ, int NH) { return NQ == 1 && NH == 1 && D <= 128 ? 4 : 2; }
 
-// LDS of the waves' rings. A piece is a tile's keys or values: 32 rows of D / 2 bytes of codes, one after another,
-// and their scales, one word a row (two with D = 256; with D = 64 the upper half is empty).
+// LDS of the waves' rings. A piece is the keys or values of a tile under NH neighbouring key heads: 32 rows of NH * D / 2
+// bytes of codes, one after another, and their scales, head by head, one word a row (two with D = 256; with D = 64 the
+// upper half is empty).
 //
-// kDepth: as many tiles as LDS holds for two workgroups of a compute unit.
-template <class T, int D, int NQ>
+// kDepth: as many tiles as LDS holds for all workgroups of a compute unit.
+template <class T, int D, int NQ, int NH>
 struct Ring4 {
   typedef Wave4<T, D, NQ> W;
-  static constexpr int kRow = D / 2, kCodes = 32 * kRow, kScaleWords = D == 256 ? 2 : 1;
-  static constexpr int kPiece = kCodes + 32 * 4 * kScaleWords;
-  static constexpr int kWaves = ring_waves(D, NQ);
-  static constexpr int kDepth = D == 64 ? (NQ == 1 ? 3 : 4) : D == 128 ? (NQ == 1 ? 2 : 3) : (NQ == 1 ? 2 : 1);
-  static constexpr int kLanes = kRow / 16;                   // lanes that copy one row
-  static constexpr int kCopyRows = 64 / kLanes;              // rows of one copy of 1 KiB
+  static constexpr int kHeadRow = D / 2, kRow = NH * kHeadRow, kCodes = 32 * kRow, kScaleWords = D == 256 ? 2 : 1;
+  static constexpr int kHeadScales = 32 * 4 * kScaleWords, kPiece = kCodes + NH * kHeadScales;
+  static constexpr int kWaves = ring_waves(D, NQ, NH);
+  static constexpr int kDepth = NH > 1 ? (D == 64 ? 3 : 2) : D == 64 ? (NQ == 1 ? 3 : 4) : D == 128 ? (NQ == 1 ? 2 : 3) : (NQ == 1 ? 2 : 1);
+  static constexpr int kParts = kRow / 16;                   // 16-byte parts of a row, and lanes that copy one
+  static constexpr int kCopyRows = 64 / kParts;              // rows of one copy of 1 KiB
   static constexpr int kCodeCopies = kCodes / 1024, kCopies = kCodeCopies + 1;   // per piece
+  static_assert(NH * kHeadScales <= 256, "one copy takes all scales of a piece");
   char piece[kWaves][kDepth][2][kPiece];
 
-  // Keys lie with the 16-byte parts of a row permuted by its number, so that the rows that one read takes fall on
+  // Keys lie with the parts of a row permuted by its number, so that the rows that one read takes fall on
   // different banks. The same for every copy of a piece.
-  static __device__ __forceinline__ int swizzle(int row) { return D == 64 ? row >> 3 & 1 : D == 128 ? row >> 1 & 3 : row & 7; }
+  static __device__ __forceinline__ int swizzle(int row) { return kParts == 2 ? row >> 3 & 1 : kParts == 4 ? row >> 1 & 3 : row & 7; }
 
-  // This lane's row in the first copy of a piece, and its bytes of that row.
-  static __device__ __forceinline__ int code_row(int lane) { return lane / kLanes; }
-  static __device__ __forceinline__ int code_byte(int kv, int lane) {
-    return 16 * (kv == 0 ? lane % kLanes ^ swizzle(code_row(lane)) : lane % kLanes);
-  }
+  // What this lane copies: its row in the first copy of a piece, its head and its bytes of that head's row.
+  static __device__ __forceinline__ int code_row(int lane) { return lane / kParts; }
+  static __device__ __forceinline__ int code_part(int kv, int lane) { return kv == 0 ? lane % kParts ^ swizzle(code_row(lane)) : lane % kParts; }
+  static __device__ __forceinline__ int code_head(int kv, int lane) { return code_part(kv, lane) / (kHeadRow / 16); }
+  static __device__ __forceinline__ int code_byte(int kv, int lane) { return 16 * (code_part(kv, lane) % (kHeadRow / 16)); }
   static __device__ __forceinline__ int scale_row(int lane) { return D == 256 ? lane >> 1 : lane & 31; }
+  static __device__ __forceinline__ int scale_head(int lane) { return NH > 1 ? lane >> 5 : 0; }
   static __device__ __forceinline__ int scale_byte(int lane) { return D == 256 ? 4 * (lane & 1) : 0; }
 
   // Copy i of a piece's codes, and of its scales.
@@ -261,7 +266,7 @@ struct Ring4 {
     __builtin_amdgcn_global_load_lds(src, &piece[wave][stage][kv][1024 * i], 16, 0, 0);
   }
   __device__ __forceinline__ void copy_scales(int wave, int stage, int kv, int lane, const char* src) {
-    if (D == 256 || lane < 32) __builtin_amdgcn_global_load_lds(src, &piece[wave][stage][kv][kCodes], D == 64 ? 2 : 4, 0, 0);
+    if (NH * kHeadScales == 256 || lane < 32) __builtin_amdgcn_global_load_lds(src, &piece[wave][stage][kv][kCodes], D == 64 ? 2 : 4, 0, 0);
   }
 
   // The same from a scalar base, `off` bytes and a lane's own offset behind it (all together below 2^31).
@@ -272,7 +277,7 @@ struct Ring4 {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(page, &piece[wave][stage][kv][1024 * i], 16, lane_at, off, 0, 0);
   }
   __device__ __forceinline__ void copy_scales(int wave, int stage, int kv, int lane, __amdgpu_buffer_rsrc_t page, int off, uint32_t lane_at) {
-    if (D == 256 || lane < 32)
+    if (NH * kHeadScales == 256 || lane < 32)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(page, &piece[wave][stage][kv][kCodes], D == 64 ? 2 : 4, lane_at, off, 0, 0);
   }
 
@@ -283,18 +288,19 @@ struct Ring4 {
     else __asm__ __volatile__("s_waitcnt vmcnt(0)" ::: "memory");
   }
 
-  // Keys 16 a + col of a piece into w.kc and w.kb.
-  static __device__ __forceinline__ void read_keys(W& w, uint32_t at, uint32_t shift) {
-    const uint32_t scales = at + kCodes + 4 * kScaleWords * w.col;
+  // Keys 16 a + col of head h of a piece into w.kc and w.kb.
+  static __device__ __forceinline__ void read_keys(W& w, uint32_t at, int h, uint32_t shift) {
+    const uint32_t row = at + w.col * kRow, scales = at + kCodes + h * kHeadScales + 4 * kScaleWords * w.col;
+    const int z = swizzle(w.col);
     if constexpr (D == 64) {
-      const uint32_t codes = at + w.col * kRow + ((8 * w.grp) ^ (16 * swizzle(w.col)));
+      const uint32_t codes = row + 16 * ((2 * h + (w.grp >> 1)) ^ z) + 8 * (w.grp & 1);
       v2u x, y;
       uint32_t sx, sy;
       __asm__ __volatile__(
-          "ds_read_b64 %0, %4\n\tds_read_b64 %1, %4 offset:512\n\t"
+          "ds_read_b64 %0, %4\n\tds_read_b64 %1, %4 offset:%6\n\t"
           "ds_read_b32 %2, %5\n\tds_read_b32 %3, %5 offset:64\n\ts_waitcnt lgkmcnt(0)"
           : "=&v"(x), "=&v"(y), "=&v"(sx), "=&v"(sy)
-          : "v"(codes), "v"(scales)
+          : "v"(codes), "v"(scales), "n"(16 * kRow)
           : "memory");
       w.kc[0][0] = x.x;
       w.kc[0][1] = x.y;
@@ -303,14 +309,14 @@ struct Ring4 {
       w.kb[0][0] = scale_of(sx, shift);
       w.kb[1][0] = scale_of(sy, shift);
     } else if constexpr (D == 128) {
-      const uint32_t codes = at + w.col * kRow + 16 * (w.grp ^ swizzle(w.col));
+      const uint32_t codes = row + 16 * ((4 * h + w.grp) ^ z);
       v4u x, y;
       uint32_t sx, sy;
       __asm__ __volatile__(
-          "ds_read_b128 %0, %4\n\tds_read_b128 %1, %4 offset:1024\n\t"
+          "ds_read_b128 %0, %4\n\tds_read_b128 %1, %4 offset:%6\n\t"
           "ds_read_b32 %2, %5\n\tds_read_b32 %3, %5 offset:64\n\ts_waitcnt lgkmcnt(0)"
           : "=&v"(x), "=&v"(y), "=&v"(sx), "=&v"(sy)
-          : "v"(codes), "v"(scales)
+          : "v"(codes), "v"(scales), "n"(16 * kRow)
           : "memory");
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -320,7 +326,7 @@ struct Ring4 {
       w.kb[0][0] = scale_of(sx, shift);
       w.kb[1][0] = scale_of(sy, shift);
     } else {
-      const uint32_t row = at + w.col * kRow, part = w.grp ^ swizzle(w.col), codes = row + 16 * part, other = row + 16 * (part ^ 4);
+      const uint32_t codes = row + 16 * (w.grp ^ z), other = row + 16 * (w.grp ^ z ^ 4);
       v4u x[4];
       v2u s[2];
       __asm__ __volatile__(
@@ -341,10 +347,10 @@ struct Ring4 {
     }
   }
 
-  // Values mine(j) of a piece into w.vc and w.vb.
-  static __device__ __forceinline__ void read_values(W& w, uint32_t at, uint32_t shift) {
-    const uint32_t codes = at + 4 * w.grp * kRow + w.col * (D / 32);
-    const uint32_t scales = at + kCodes + 16 * kScaleWords * w.grp + (D == 256 ? 4 * (w.col >> 3) : 0);
+  // Values mine(j) of head h of a piece into w.vc and w.vb.
+  static __device__ __forceinline__ void read_values(W& w, uint32_t at, int h, uint32_t shift) {
+    const uint32_t codes = at + 4 * w.grp * kRow + h * kHeadRow + w.col * (D / 32);
+    const uint32_t scales = at + kCodes + h * kHeadScales + 16 * kScaleWords * w.grp + (D == 256 ? 4 * (w.col >> 3) : 0);
     if constexpr (D == 256) {
       v2u x[8], s[4];
       __asm__ __volatile__(
@@ -368,25 +374,27 @@ struct Ring4 {
       v4u s[2];
       if constexpr (D == 128) {
         __asm__ __volatile__(
-            "ds_read_b32 %0, %10\n\tds_read_b32 %1, %10 offset:64\n\t"
-            "ds_read_b32 %2, %10 offset:128\n\tds_read_b32 %3, %10 offset:192\n\t"
-            "ds_read_b32 %4, %10 offset:1024\n\tds_read_b32 %5, %10 offset:1088\n\t"
-            "ds_read_b32 %6, %10 offset:1152\n\tds_read_b32 %7, %10 offset:1216\n\t"
+            "ds_read_b32 %0, %10\n\tds_read_b32 %1, %10 offset:%12\n\t"
+            "ds_read_b32 %2, %10 offset:%13\n\tds_read_b32 %3, %10 offset:%14\n\t"
+            "ds_read_b32 %4, %10 offset:%15\n\tds_read_b32 %5, %10 offset:%16\n\t"
+            "ds_read_b32 %6, %10 offset:%17\n\tds_read_b32 %7, %10 offset:%18\n\t"
             "ds_read_b128 %8, %11\n\tds_read_b128 %9, %11 offset:64\n\ts_waitcnt lgkmcnt(0)"
             : "=&v"(w.vc[0][0]), "=&v"(w.vc[1][0]), "=&v"(w.vc[2][0]), "=&v"(w.vc[3][0]), "=&v"(w.vc[4][0]),
               "=&v"(w.vc[5][0]), "=&v"(w.vc[6][0]), "=&v"(w.vc[7][0]), "=&v"(s[0]), "=&v"(s[1])
-            : "v"(codes), "v"(scales)
+            : "v"(codes), "v"(scales), "n"(kRow), "n"(2 * kRow), "n"(3 * kRow), "n"(16 * kRow), "n"(17 * kRow), "n"(18 * kRow),
+              "n"(19 * kRow)
             : "memory");
       } else {
         __asm__ __volatile__(
-            "ds_read_u16 %0, %10\n\tds_read_u16 %1, %10 offset:32\n\t"
-            "ds_read_u16 %2, %10 offset:64\n\tds_read_u16 %3, %10 offset:96\n\t"
-            "ds_read_u16 %4, %10 offset:512\n\tds_read_u16 %5, %10 offset:544\n\t"
-            "ds_read_u16 %6, %10 offset:576\n\tds_read_u16 %7, %10 offset:608\n\t"
+            "ds_read_u16 %0, %10\n\tds_read_u16 %1, %10 offset:%12\n\t"
+            "ds_read_u16 %2, %10 offset:%13\n\tds_read_u16 %3, %10 offset:%14\n\t"
+            "ds_read_u16 %4, %10 offset:%15\n\tds_read_u16 %5, %10 offset:%16\n\t"
+            "ds_read_u16 %6, %10 offset:%17\n\tds_read_u16 %7, %10 offset:%18\n\t"
             "ds_read_b128 %8, %11\n\tds_read_b128 %9, %11 offset:64\n\ts_waitcnt lgkmcnt(0)"
             : "=&v"(w.vc[0][0]), "=&v"(w.vc[1][0]), "=&v"(w.vc[2][0]), "=&v"(w.vc[3][0]), "=&v"(w.vc[4][0]),
               "=&v"(w.vc[5][0]), "=&v"(w.vc[6][0]), "=&v"(w.vc[7][0]), "=&v"(s[0]), "=&v"(s[1])
-            : "v"(codes), "v"(scales)
+            : "v"(codes), "v"(scales), "n"(kRow), "n"(2 * kRow), "n"(3 * kRow), "n"(16 * kRow), "n"(17 * kRow), "n"(18 * kRow),
+              "n"(19 * kRow)
             : "memory");
       }
 #pragma unroll
@@ -398,15 +406,15 @@ struct Ring4 {
   static __device__ __forceinline__ void read_slots(int (&slot)[kCodeCopies], int* scale_slot, uint32_t codes, uint32_t scales) {
     if constexpr (kCodeCopies == 4) {
       __asm__ __volatile__(
-          "ds_read_b32 %0, %5\n\tds_read_b32 %1, %5 offset:32\n\tds_read_b32 %2, %5 offset:64\n\t"
-          "ds_read_b32 %3, %5 offset:96\n\tds_read_b32 %4, %6\n\ts_waitcnt lgkmcnt(0)"
+          "ds_read_b32 %0, %5\n\tds_read_b32 %1, %5 offset:%7\n\tds_read_b32 %2, %5 offset:%8\n\t"
+          "ds_read_b32 %3, %5 offset:%9\n\tds_read_b32 %4, %6\n\ts_waitcnt lgkmcnt(0)"
           : "=&v"(slot[0]), "=&v"(slot[1]), "=&v"(slot[2]), "=&v"(slot[3]), "=&v"(*scale_slot)
-          : "v"(codes), "v"(scales)
+          : "v"(codes), "v"(scales), "n"(4 * kCopyRows), "n"(8 * kCopyRows), "n"(12 * kCopyRows)
           : "memory");
     } else if constexpr (kCodeCopies == 2) {
-      __asm__ __volatile__("ds_read_b32 %0, %3\n\tds_read_b32 %1, %3 offset:64\n\tds_read_b32 %2, %4\n\ts_waitcnt lgkmcnt(0)"
+      __asm__ __volatile__("ds_read_b32 %0, %3\n\tds_read_b32 %1, %3 offset:%5\n\tds_read_b32 %2, %4\n\ts_waitcnt lgkmcnt(0)"
                            : "=&v"(slot[0]), "=&v"(slot[1]), "=&v"(*scale_slot)
-                           : "v"(codes), "v"(scales)
+                           : "v"(codes), "v"(scales), "n"(4 * kCopyRows)
                            : "memory");
     } else {
       static_assert(kCodeCopies == 1, "one, two or four");
@@ -415,18 +423,18 @@ struct Ring4 {
                            : "v"(codes), "v"(scales)
                            : "memory");
     }
-    static_assert(kCopyRows * 4 == (kCodeCopies == 4 ? 32 : kCodeCopies == 2 ? 64 : 128), "the offsets above");
   }
 
   // This wave's tiles t, t + kWaves, ... below t_hi. keys(t, stage) and values(t, stage) issue the copies of one
   // piece, values those of the tile that keys was last called for; range(t, &lo, &hi) gives the positions that count.
   template <class KEYS, class VALUES, class RANGE>
-  __device__ __forceinline__ void run(W& w, int wave, int t, int t_hi, float c, KEYS&& keys, VALUES&& values, RANGE&& range) {
+  __device__ __forceinline__ void run(W (&w)[NH], int wave, int t, int t_hi, float c, KEYS&& keys, VALUES&& values, RANGE&& range) {
     if (t >= t_hi) return;
     const uint32_t ring = lds_address(&piece[wave][0][0][0]);
     // byte of the word that holds the scale of this lane's keys, and of its values
-    const uint32_t k_shift = 8 * (D == 64 ? w.grp >> 1 : w.grp) + 9;
-    const uint32_t v_shift = 8 * (D == 64 ? w.col >> 3 : D == 128 ? w.col >> 2 : w.col >> 1 & 3) + 9;
+    const int col = w[0].col, grp = w[0].grp;
+    const uint32_t k_shift = 8 * (D == 64 ? grp >> 1 : grp) + 9;
+    const uint32_t v_shift = 8 * (D == 64 ? col >> 3 : D == 128 ? col >> 2 : col >> 1 & 3) + 9;
     // no other load or store of this wave is in flight when the copies are counted
     __asm__ __volatile__("s_waitcnt vmcnt(0)" ::: "memory");
     const int tiles = (t_hi - t + kWaves - 1) / kWaves;
@@ -447,34 +455,39 @@ struct Ring4 {
       if (edge) {
         inside = 0;
 #pragma unroll
-        for (int j = 0; j < W::kMine; ++j) inside |= (w.mine(j) >= lo && w.mine(j) < hi ? 1u : 0u) << j;
+        for (int j = 0; j < W::kMine; ++j) inside |= (w[0].mine(j) >= lo && w[0].mine(j) < hi ? 1u : 0u) << j;
       }
-      const int left = 2 * (tiles - i) - 1;   // pieces behind this one
+      const bool more = i + kDepth < tiles;   // tiles to ask for
       const uint32_t at = ring + 2 * kPiece * stage;
-      arrived(left);
-      read_keys(w, at, k_shift);
-      if (i + kDepth < tiles) {
-        keys(t + kWaves * kDepth, stage);
-        __asm__ __volatile__("" ::: "memory");
+      v4f s[NH][NQ][2];
+      arrived(2 * (tiles - i) - 1);           // pieces behind this one
+#pragma unroll
+      for (int h = 0; h < NH; ++h) {
+        read_keys(w[h], at, h, k_shift);
+        if (h == NH - 1 && more) {
+          keys(t + kWaves * kDepth, stage);
+          __asm__ __volatile__("" ::: "memory");
+        }
+        w[h].scores(s[h]);
+        w[h].follow_maximum(s[h], c, edge, inside);
       }
-      v4f s[NQ][2];
-      w.scores(s);
-      w.follow_maximum(s, c, edge, inside);
-      // the keys that were just asked for are younger too
-      arrived(i + kDepth < tiles ? 2 * kDepth : 0);
-      read_values(w, at + kPiece, v_shift);
-      if (i + kDepth < tiles) {
-        values(t + kWaves * kDepth, stage);
-        __asm__ __volatile__("" ::: "memory");
+      arrived(more ? 2 * kDepth : 0);         // the keys that were just asked for are younger too
+#pragma unroll
+      for (int h = 0; h < NH; ++h) {
+        read_values(w[h], at + kPiece, h, v_shift);
+        if (h == NH - 1 && more) {
+          values(t + kWaves * kDepth, stage);
+          __asm__ __volatile__("" ::: "memory");
+        }
+        if (edge) w[h].clear_outside(inside);
+        w[h].add_weighted(s[h], c);
       }
-      if (edge) w.clear_outside(inside);
-      w.add_weighted(s, c);
       stage = stage + 1 < kDepth ? stage + 1 : 0;
     }
   }
 };
 
-// Heads of one row and key head that a workgroup carries.
+// Query heads of one row and key head that a workgroup carries.
 template <int NQ>
 __device__ __forceinline__ int group_of(const KvFp4Args& a) { return a.G < 16 * NQ ? a.G : 16 * NQ; }
 
@@ -492,22 +505,21 @@ __device__ __forceinline__ void join_waves(MERGE& merge, W& w, bool bad, int row
 }
 
 // A workgroup's LDS: the rings, and when the last tile is done the memory that joins the waves.
-template <class T, int D, int NQ>
+template <class T, int D, int NQ, int NH>
 union Space {
-  Ring4<T, D, NQ> ring;
-  Merge<T, D, ring_waves(D, NQ)> merge;
+  Ring4<T, D, NQ, NH> ring;
+  Merge<T, D, ring_waves(D, NQ, NH)> merge;
 };
 
 // --- decode form --------------------------------------------------------------
 
-// A row's pages lie end to end with the others' and are cut into shares, and a workgroup takes one share of one of the `pairs`
-// of a key head and 16 NQ of its query heads. All pairs of a share go to one die, next to each other in the launch: the
-// 64 bytes of a position's key under 8 key heads are half of a cache line, its 4 bytes of scales an eighth of
-// one, and what one head's workgroup leaves of them the others find in the die's L2.
-// Shares of more pairs than that leaves room for: as many as there are workgroups for.
-__host__ __device__ __forceinline__ int decode_shares(int64_t pairs) {
-  if (pairs <= kKvDecodeGroups / 8) return static_cast<int>(kKvDecodeGroups / (8 * pairs) * 8);
-  return pairs < kKvDecodeGroups ? static_cast<int>(kKvDecodeGroups / pairs) : 1;
+// A row's pages lie end to end with the others' and are cut into shares, and a workgroup takes one share of one of the `sets`
+// of NH key heads and 16 NQ query heads of each. All sets of a share go to one die, next to each other in the launch: what one
+// workgroup leaves of a cache line that it reads a part of, the others find in the die's L2. `groups` workgroups at most; more sets
+// than that leave one share only.
+__host__ __device__ __forceinline__ int decode_shares(int64_t sets, int groups) {
+  if (sets <= groups / 8) return static_cast<int>(groups / (8 * sets) * 8);
+  return sets < groups ? static_cast<int>(groups / sets) : 1;
 }
 
 // x, which every lane holds, as a scalar: what hangs on it (pages' addresses) is then computed once for the wave.
@@ -526,36 +538,41 @@ __device__ __forceinline__ ArgsInMemory& fresh_args() {
   return *p;
 }
 
-template <class T, int D, int NQ>
-__global__ void __launch_bounds__(64 * ring_waves(D, NQ), ring_waves(D, NQ) / 2) kv_decode_fp4_kernel(KvFp4Args a) {
+template <class T, int D, int NQ, int NH>
+__global__ void __launch_bounds__(64 * ring_waves(D, NQ, NH), ring_waves_per_simd(D, NQ, NH)) kv_decode_fp4_kernel(KvFp4Args a) {
   typedef Wave4<T, D, NQ> W;
-  typedef Ring4<T, D, NQ> R;
+  typedef Ring4<T, D, NQ, NH> R;
+  constexpr int kGroups = ring_groups(NH);
   __shared__ Plan<R::kWaves> plan;
-  __shared__ __align__(16) Space<T, D, NQ> lds;
+  __shared__ __align__(16) Space<T, D, NQ, NH> lds;
   __shared__ v4u q_lds[W::kShared ? NQ * W::kChunks * 64 : 1];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t* prefix = plan.make(a);
   const int group = group_of<NQ>(a), qg = (a.G + 16 * NQ - 1) / (16 * NQ);
-  const int pairs = a.Hkv * qg, shares = decode_shares(pairs), at = blockIdx.x;
-  int pair = pairs < kKvDecodeGroups ? at % pairs : at, which = pairs < kKvDecodeGroups ? at / pairs : 0;
+  const int sets = a.Hkv / NH * qg, shares = decode_shares(sets, kGroups), at = blockIdx.x;
+  int set = sets < kGroups ? at % sets : at, which = sets < kGroups ? at / sets : 0;
   if (shares >= 8) {
-    pair = (at >> 3) % pairs;
-    which = (at >> 3) / pairs * 8 + (at & 7);
+    set = (at >> 3) % sets;
+    which = (at >> 3) / sets * 8 + (at & 7);
   }
   if (which >= shares) return;
   const int64_t units = uniform(prefix[a.Q]);
   const int64_t share = unit_share(a, units, shares);
   const int64_t stop = which * share + share < units ? which * share + share : units;
-  W w;
-  w.init();
+  W w[NH];
+#pragma unroll
+  for (int h = 0; h < NH; ++h) w[h].init();
+  const int lane = w[0].lane;
   // strides inside a page, whose extent is below 2^31, and what a lane adds to a piece's address
   const int k_pos = static_cast<int>(a.k_pos), v_pos = static_cast<int>(a.v_pos), ks_pos = static_cast<int>(a.ks_pos), vs_pos = static_cast<int>(a.vs_pos);
-  const uint32_t k_at = R::code_row(w.lane) * k_pos + R::code_byte(0, w.lane), v_at = R::code_row(w.lane) * v_pos + R::code_byte(1, w.lane);
-  const uint32_t ks_at = R::scale_row(w.lane) * ks_pos + R::scale_byte(w.lane), vs_at = R::scale_row(w.lane) * vs_pos + R::scale_byte(w.lane);
-  // (with more pairs than workgroups there is one share only)
-  for (int64_t cur = which * share; cur < stop || pair + kKvDecodeGroups < pairs;) {
+  const uint32_t k_at = R::code_row(lane) * k_pos + R::code_head(0, lane) * static_cast<int>(a.k_head) + R::code_byte(0, lane);
+  const uint32_t v_at = R::code_row(lane) * v_pos + R::code_head(1, lane) * static_cast<int>(a.v_head) + R::code_byte(1, lane);
+  const uint32_t ks_at = R::scale_row(lane) * ks_pos + R::scale_head(lane) * static_cast<int>(a.ks_head) + R::scale_byte(lane);
+  const uint32_t vs_at = R::scale_row(lane) * vs_pos + R::scale_head(lane) * static_cast<int>(a.vs_head) + R::scale_byte(lane);
+  // (with more sets than workgroups there is one share only)
+  for (int64_t cur = which * share; cur < stop || set + kGroups < sets;) {
     if (cur >= stop) {
-      pair += kKvDecodeGroups;
+      set += kGroups;
       cur = which * share;
       continue;
     }
@@ -563,7 +580,7 @@ __global__ void __launch_bounds__(64 * ring_waves(D, NQ), ring_waves(D, NQ) / 2)
     Segment sg;
     sg.take(m, prefix, 1, &cur, stop);
     const int64_t r = sg.r;
-    const int kvh = pair / qg, first = (pair % qg) * 16 * NQ, rows = m.G - first < 16 * NQ ? m.G - first : 16 * NQ;
+    const int kvh = set / qg * NH, first = (set % qg) * 16 * NQ, rows = m.G - first < 16 * NQ ? m.G - first : 16 * NQ;
     const int start = sg.start, end = sg.end;
     const ScalarInts table = scalar_ints(m.table + static_cast<int64_t>(sg.seq) * m.max_pages);
     const int p0 = start >> 6;
@@ -572,8 +589,11 @@ __global__ void __launch_bounds__(64 * ring_waves(D, NQ), ring_waves(D, NQ) / 2)
     const char *kb = m.k + kvh * m.k_head, *vb = m.v + kvh * m.v_head;
     const char *ksb = m.ks + kvh * m.ks_head, *vsb = m.vs + kvh * m.vs_head;
     const int64_t head0 = r * m.H + static_cast<int64_t>(kvh) * m.G + first;
-    w.start();
-    w.load_q(m.q + r * m.q_row + (static_cast<int64_t>(kvh) * m.G + first) * D * 2, rows, m.q_keep, m.q_flip, q_lds);
+#pragma unroll
+    for (int h = 0; h < NH; ++h) {
+      w[h].start();
+      w[h].load_q(m.q + r * m.q_row + (static_cast<int64_t>(kvh + h) * m.G + first) * D * 2, rows, m.q_keep, m.q_flip, q_lds);
+    }
 
     const int64_t k_page = m.k_page, v_page = m.v_page, ks_page = m.ks_page, vs_page = m.vs_page;
     const int pages = static_cast<int>(m.P_phys);
@@ -594,31 +614,35 @@ __global__ void __launch_bounds__(64 * ring_waves(D, NQ), ring_waves(D, NQ) / 2)
           const auto codes = R::page_at(kb + page * k_page), scales = R::page_at(ksb + page * ks_page);
 #pragma unroll
           for (int i = 0; i < R::kCodeCopies; ++i) lds.ring.copy(wave, stage, 0, i, codes, (first_pos + i * R::kCopyRows) * k_pos, k_at);
-          lds.ring.copy_scales(wave, stage, 0, w.lane, scales, first_pos * ks_pos, ks_at);
+          lds.ring.copy_scales(wave, stage, 0, lane, scales, first_pos * ks_pos, ks_at);
         },
         [&](int t, int stage) {
           const int first_pos = 32 * (t & 1);
           const auto codes = R::page_at(vb + page * v_page), scales = R::page_at(vsb + page * vs_page);
 #pragma unroll
           for (int i = 0; i < R::kCodeCopies; ++i) lds.ring.copy(wave, stage, 1, i, codes, (first_pos + i * R::kCopyRows) * v_pos, v_at);
-          lds.ring.copy_scales(wave, stage, 1, w.lane, scales, first_pos * vs_pos, vs_at);
+          lds.ring.copy_scales(wave, stage, 1, lane, scales, first_pos * vs_pos, vs_at);
         },
         [&](int t, int* lo, int* hi) {
           *lo = start - 32 * t;
           *hi = end - 32 * t;
         });
     ArgsInMemory& e = fresh_args();
-    if (bad && w.lane == 0) atomicOr(e.status, kStBadPage);
+    if (bad && lane == 0) atomicOr(e.status, kStBadPage);
     const bool whole = sg.pa == 0 && sg.pb == sg.n;
-    const int64_t slot = 2 * (static_cast<int64_t>(pair) * shares + which) + (sg.pa == 0 ? 1 : 0);
-    join_waves<0, T, D>(lds.merge, w, bad, rows, static_cast<char*>(e.out) + head0 * D * 2, e.lse == nullptr ? nullptr : e.lse + head0,
-                        whole ? nullptr : e.part_o + slot * group * D, e.part_ml + slot * group);
+    const int64_t slot = 2 * (static_cast<int64_t>(set) * shares + which) + (sg.pa == 0 ? 1 : 0);
+#pragma unroll
+    for (int h = 0; h < NH; ++h) {
+      const int64_t head = head0 + static_cast<int64_t>(h) * e.G, part = (slot * NH + h) * group;
+      join_waves<0, T, D>(lds.merge, w[h], bad, rows, static_cast<char*>(e.out) + head * D * 2, e.lse == nullptr ? nullptr : e.lse + head,
+                          whole ? nullptr : e.part_o + part * D, e.part_ml + part);
+    }
     __syncthreads();   // the rings may be filled again
   }
 }
 
 // Joins the parts of rows that several shares have a part of, and writes the rows that have no pages.
-template <class T, int D, int NQ, int WAVES>
+template <class T, int D, int NQ, int NH, int WAVES>
 __global__ void __launch_bounds__(kThreads) kv_decode_fp4_join_kernel(KvFp4Args a) {
   const int64_t head = join_head<WAVES>(a);
   if (head < 0) return;
@@ -631,14 +655,14 @@ __global__ void __launch_bounds__(kThreads) kv_decode_fp4_join_kernel(KvFp4Args 
     fill_row<T, D>(a, head, code != 0, WAVES > 1 ? threadIdx.x : threadIdx.x & 63, 64 * WAVES);
     return;
   }
-  const int qg = (a.G + 16 * NQ - 1) / (16 * NQ), shares = decode_shares(static_cast<int64_t>(a.Hkv) * qg);
+  const int qg = (a.G + 16 * NQ - 1) / (16 * NQ), shares = decode_shares(static_cast<int64_t>(a.Hkv / NH) * qg, ring_groups(NH));
   const int64_t share = unit_share(a, a.prefix[a.Q], shares);
   const int64_t w0 = before / share, w1 = (before + n - 1) / share;
   if (w0 == w1) return;   // one workgroup had all of it and wrote the output
-  const int kvh = h / a.G, in_kv = h - kvh * a.G;
-  const int64_t slot = 2 * ((static_cast<int64_t>(kvh) * qg + in_kv / (16 * NQ)) * shares + w0);
+  const int kvh = h / a.G, in_kv = h - kvh * a.G, group = group_of<NQ>(a);
+  const int64_t slot = 2 * ((static_cast<int64_t>(kvh / NH) * qg + in_kv / (16 * NQ)) * shares + w0);
   // the first part is its workgroup's last one (slot + 1), the others are first ones
-  join_row<T, D, WAVES>(a, head, in_kv % (16 * NQ), group_of<NQ>(a), w1 - w0 + 1, slot + 1, slot, 2);
+  join_row<T, D, WAVES>(a, head, kvh % NH * group + in_kv % (16 * NQ), NH * group, w1 - w0 + 1, slot + 1, slot, 2);
 }
 
 // --- selected form ------------------------------------------------------------
@@ -663,10 +687,10 @@ struct ListTiles {
 
   __device__ __forceinline__ ListTiles(const KvFp4Args& a_, int kvh, int wave_, int lane_, uint32_t list)
       : a(a_), wave(wave_), lane(lane_), len(0), scale_slot(0), scale_off(0) {
-    k = a.k + kvh * a.k_head + R::code_byte(0, lane);
-    v = a.v + kvh * a.v_head + R::code_byte(1, lane);
-    ks = a.ks + kvh * a.ks_head + R::scale_byte(lane);
-    vs = a.vs + kvh * a.vs_head + R::scale_byte(lane);
+    k = a.k + (kvh + R::code_head(0, lane)) * a.k_head + R::code_byte(0, lane);
+    v = a.v + (kvh + R::code_head(1, lane)) * a.v_head + R::code_byte(1, lane);
+    ks = a.ks + (kvh + R::scale_head(lane)) * a.ks_head + R::scale_byte(lane);
+    vs = a.vs + (kvh + R::scale_head(lane)) * a.vs_head + R::scale_byte(lane);
     k_page = static_cast<uint32_t>(a.k_page >> 4);
     v_page = static_cast<uint32_t>(a.v_page >> 4);
     k_pos = static_cast<uint32_t>(a.k_pos >> 4);
@@ -699,30 +723,34 @@ struct ListTiles {
   }
 };
 
-template <class T, int D, int NQ>
-__global__ void __launch_bounds__(64 * ring_waves(D, NQ), ring_waves(D, NQ) / 2) kv_selected_fp4_kernel(KvFp4Args a) {
+template <class T, int D, int NQ, int NH>
+__global__ void __launch_bounds__(64 * ring_waves(D, NQ, NH), ring_waves_per_simd(D, NQ, NH)) kv_selected_fp4_kernel(KvFp4Args a) {
   typedef Wave4<T, D, NQ> W;
-  typedef Ring4<T, D, NQ> R;
+  typedef Ring4<T, D, NQ, NH> R;
   __shared__ int list[kKvSelBlock];
-  __shared__ __align__(16) Space<T, D, NQ> lds;
+  __shared__ __align__(16) Space<T, D, NQ, NH> lds;
   __shared__ v4u q_lds[W::kShared ? NQ * W::kChunks * 64 : 1];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int qg = (a.G + 16 * NQ - 1) / (16 * NQ);
   ListPart p;
   bool fill;
-  const bool any = p.take(a, static_cast<int64_t>(a.Hkv) * qg, &fill);
+  const bool any = p.take(a, static_cast<int64_t>(a.Hkv / NH) * qg, &fill);
   if (!any && !fill) return;
-  const int kvh = p.g / qg, first = (p.g % qg) * 16 * NQ, rows = a.G - first < 16 * NQ ? a.G - first : 16 * NQ;
+  const int kvh = p.g / qg * NH, first = (p.g % qg) * 16 * NQ, rows = a.G - first < 16 * NQ ? a.G - first : 16 * NQ;
   const int64_t head0 = p.r * a.H + static_cast<int64_t>(kvh) * a.G + first;
   if (!any) {
-    for (int h = 0; h < rows; ++h) fill_row<T, D>(a, head0 + h, p.n != 0, threadIdx.x, 64 * R::kWaves);
+    for (int h = 0; h < NH * rows; ++h)
+      fill_row<T, D>(a, head0 + h / rows * a.G + h % rows, p.n != 0, threadIdx.x, 64 * R::kWaves);
     return;
   }
-  W w;
-  w.init();
-  w.start();
-  w.load_q(a.q + p.r * a.q_row + (static_cast<int64_t>(kvh) * a.G + first) * D * 2, rows, a.q_keep, a.q_flip, q_lds);
-  ListTiles<R> tiles_of(a, kvh, wave, w.lane, lds_address(list));
+  W w[NH];
+#pragma unroll
+  for (int h = 0; h < NH; ++h) {
+    w[h].init();
+    w[h].start();
+    w[h].load_q(a.q + p.r * a.q_row + (static_cast<int64_t>(kvh + h) * a.G + first) * D * 2, rows, a.q_keep, a.q_flip, q_lds);
+  }
+  ListTiles<R> tiles_of(a, kvh, wave, w[0].lane, lds_address(list));
   bool bad = false;
   for (int64_t b0 = p.from; b0 < p.to; b0 += kKvSelBlock) {
     const int len = static_cast<int>(p.to - b0 < kKvSelBlock ? p.to - b0 : kKvSelBlock);
@@ -747,16 +775,33 @@ __global__ void __launch_bounds__(64 * ring_waves(D, NQ), ring_waves(D, NQ) / 2)
                  });
   }
   if (bad && threadIdx.x == 0) atomicOr(a.status, kStBadPage);
-  const int64_t part = p.item * group_of<NQ>(a);
-  join_waves<0, T, D>(lds.merge, w, bad, rows, static_cast<char*>(a.out) + head0 * D * 2, a.lse == nullptr ? nullptr : a.lse + head0,
-                      a.splits == 1 ? nullptr : a.part_o + part * D, a.part_ml + part);
+  const int group = group_of<NQ>(a);
+#pragma unroll
+  for (int h = 0; h < NH; ++h) {
+    const int64_t head = head0 + static_cast<int64_t>(h) * a.G, part = (p.item * NH + h) * group;
+    join_waves<0, T, D>(lds.merge, w[h], bad, rows, static_cast<char*>(a.out) + head * D * 2, a.lse == nullptr ? nullptr : a.lse + head,
+                        a.splits == 1 ? nullptr : a.part_o + part * D, a.part_ml + part);
+  }
+}
+
+template <class T, int D, int NQ, int NH, int WAVES>
+__global__ void __launch_bounds__(kThreads) kv_selected_fp4_join_kernel(KvFp4Args a) {
+  const int64_t head = join_head<WAVES>(a);
+  if (head < 0) return;
+  const int64_t r = head / a.H;
+  const int h = static_cast<int>(head - r * a.H);
+  const int64_t n = a.count[r];
+  if (n <= 0 || n > a.K) return;   // written already
+  const int qg = (a.G + 16 * NQ - 1) / (16 * NQ), kvh = h / a.G, in_kv = h - kvh * a.G, group = group_of<NQ>(a);
+  const int64_t share = split_share(n, a.splits);
+  const int64_t slot = ((r * (a.Hkv / NH) + kvh / NH) * qg + in_kv / (16 * NQ)) * a.splits;
+  join_row<T, D, WAVES>(a, head, kvh % NH * group + in_kv % (16 * NQ), NH * group, (n + share - 1) / share, slot, slot, 1);
 }
 
 // --- dispatch -----------------------------------------------------------------
 
-template <class T, int D, int NQ>
+template <class T, int D, int NQ, int NH>
 void decode_on(KvFp4Args a, hipStream_t st) {
-  const int groups = kKvDecodeGroups;
   // what one more part costs (its sums' bytes, its turn in the joining of its heads) by what a page takes, both in ns
   const double page_ns = NQ > 1 ? 1000 : 100 + 2.75 * D;
   const double pairs = static_cast<double>(a.Hkv) * kv_head_groups(D, a.G);
@@ -764,52 +809,57 @@ void decode_on(KvFp4Args a, hipStream_t st) {
   const double cost = (sums_ns * pairs + turn_ns / static_cast<double>(a.Q)) / page_ns * 65536.0;
   a.join_cost = cost < 8388608.0 ? static_cast<uint32_t>(cost) : 8388608u;
   if (a.Q > kKvPlanRows) kv_plan_kernel<<<dim3(1), dim3(1024), 0, st>>>(a);
-  kv_decode_fp4_kernel<T, D, NQ><<<dim3(groups), dim3(64 * ring_waves(D, NQ)), 0, st>>>(a);
+  kv_decode_fp4_kernel<T, D, NQ, NH><<<dim3(ring_groups(NH)), dim3(64 * ring_waves(D, NQ, NH)), 0, st>>>(a);
   const int64_t heads = a.Q * a.H;
   if (heads <= kJoinHeads)
-    kv_decode_fp4_join_kernel<T, D, NQ, kWaves><<<dim3(static_cast<unsigned>(heads)), dim3(kThreads), 0, st>>>(a);
+    kv_decode_fp4_join_kernel<T, D, NQ, NH, kWaves><<<dim3(static_cast<unsigned>(heads)), dim3(kThreads), 0, st>>>(a);
   else
-    kv_decode_fp4_join_kernel<T, D, NQ, 1><<<dim3(static_cast<unsigned>((heads + kWaves - 1) / kWaves)), dim3(kThreads), 0, st>>>(a);
+    kv_decode_fp4_join_kernel<T, D, NQ, NH, 1>
+        <<<dim3(static_cast<unsigned>((heads + kWaves - 1) / kWaves)), dim3(kThreads), 0, st>>>(a);
 }
 
-template <class T, int D, int NQ>
+template <class T, int D, int NQ, int NH>
 void selected_on(const KvFp4Args& a, hipStream_t st) {
-  const int64_t items = a.Q * a.Hkv * kv_head_groups(D, a.G) * a.splits;
+  const int64_t items = a.Q * (a.Hkv / NH) * kv_head_groups(D, a.G) * a.splits;
   const unsigned grid = static_cast<unsigned>((items + 7) / 8 * 8);
-  kv_selected_fp4_kernel<T, D, NQ><<<dim3(grid), dim3(64 * ring_waves(D, NQ)), 0, st>>>(a);
+  kv_selected_fp4_kernel<T, D, NQ, NH><<<dim3(grid), dim3(64 * ring_waves(D, NQ, NH)), 0, st>>>(a);
   if (a.splits > 1)
-    kv_selected_join_kernel<T, D, 1>
-        <<<dim3(static_cast<unsigned>((a.Q * a.H + kWaves - 1) / kWaves)), dim3(kThreads), 0, st>>>(a, 16 * NQ);
+    kv_selected_fp4_join_kernel<T, D, NQ, NH, 1>
+        <<<dim3(static_cast<unsigned>((a.Q * a.H + kWaves - 1) / kWaves)), dim3(kThreads), 0, st>>>(a);
 }
 
 struct DecodeOn {
   const KvFp4Args& a;
   hipStream_t st;
-  template <class T, int D, int NQ>
-  void operator()() const { decode_on<T, D, NQ>(a, st); }
+  template <class T, int D, int NQ, int NH>
+  void operator()() const { decode_on<T, D, NQ, NH>(a, st); }
 };
 struct SelectedOn {
   const KvFp4Args& a;
   hipStream_t st;
-  template <class T, int D, int NQ>
-  void operator()() const { selected_on<T, D, NQ>(a, st); }
+  template <class T, int D, int NQ, int NH>
+  void operator()() const { selected_on<T, D, NQ, NH>(a, st); }
 };
 
-// Calls f<type, dim, query tiles>() for the call's type and sizes.
+// Calls f<type, dim, query tiles, key heads at once>() for the call's type and sizes. Two key heads at once, where there
+// are two and a head's row is less than a cache line of 128 bytes.
 template <class T, class F>
 void by_size(const KvFp4Args& a, F&& f) {
   const int nq = kv_tiles(a.D, a.G);
+  const bool two = a.Hkv % 2 == 0;
   if (a.D == 64) {
-    if (nq == 1) f.template operator()<T, 64, 1>();
-    else if (nq == 2) f.template operator()<T, 64, 2>();
-    else f.template operator()<T, 64, 4>();
+    if (nq == 1 && two) f.template operator()<T, 64, 1, 2>();
+    else if (nq == 1) f.template operator()<T, 64, 1, 1>();
+    else if (nq == 2) f.template operator()<T, 64, 2, 1>();
+    else f.template operator()<T, 64, 4, 1>();
   } else if (a.D == 128) {
-    if (nq == 1) f.template operator()<T, 128, 1>();
-    else if (nq == 2) f.template operator()<T, 128, 2>();
-    else f.template operator()<T, 128, 4>();
+    if (nq == 1 && two) f.template operator()<T, 128, 1, 2>();
+    else if (nq == 1) f.template operator()<T, 128, 1, 1>();
+    else if (nq == 2) f.template operator()<T, 128, 2, 1>();
+    else f.template operator()<T, 128, 4, 1>();
   } else {
-    if (nq == 1) f.template operator()<T, 256, 1>();
-    else f.template operator()<T, 256, 2>();
+    if (nq == 1) f.template operator()<T, 256, 1, 1>();
+    else f.template operator()<T, 256, 2, 1>();
   }
 }
 
