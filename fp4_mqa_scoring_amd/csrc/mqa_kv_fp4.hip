@@ -30,25 +30,27 @@ __device__ __forceinline__ uint32_t scale_of(uint32_t word, uint32_t shift) { re
 // A wave's tile of 32 positions over a cache in 4 bits. Lane (col, grp) holds, of keys 16 a + col, the codes of
 // D / 4 dims, 32 of a block at most, and of values mine(j) those of D / 16 neighbouring ones.
 //
-// More than 16 heads: the queries lie in LDS, and the running maximum may lag by 2^8.
+// More than 16 heads: the running maximum may lag by 2^8.
 template <class T, int D, int NQ>
-struct Wave4 : Wave<T, false, D, NQ, 32, (NQ > 1), (NQ > 1 ? 8 : 0)> {
-  typedef Wave<T, false, D, NQ, 32, (NQ > 1), (NQ > 1 ? 8 : 0)> Base;
+struct Wave4 : Wave<T, false, D, NQ, 32, true, (NQ > 1 ? 8 : 0)> {
+  typedef Wave<T, false, D, NQ, 32, true, (NQ > 1 ? 8 : 0)> Base;   // (queries and loads are this one's own)
   using Base::kChunks;
   using Base::kDims;
   using Base::kMine;
-  using Base::kShared;
   using Base::kTiles;
   using Base::col;
   using Base::grp;
-  using Base::q;
   typedef typename Base::P P;
   static constexpr int kKeyBlocks = D == 256 ? 2 : 1;    // scales of a lane's key
   static constexpr int kKeyWords = D / 32;               // words of 8 codes of a lane's key
-  static constexpr int kSteps = kChunks < 4 ? kChunks : 4;   // matrix steps over the dims at once
+  // Tiles of 16 heads whose queries stay in registers, as many as there is room for (64 heads, D = 128: 1, 2 and 3 of the four
+  // 238, 277 and 350 us, from the second on with spills); those of the others lie in LDS.
+  static constexpr int kHeld = D == 64 || NQ == 1 || (D == 128 && NQ == 2) ? NQ : D == 128 ? 1 : 0;
+  static constexpr int kInLds = NQ - kHeld;
   static constexpr int kWords4 = D == 256 ? 2 : 1;       // words of a lane's value (half of one with D = 64)
 
-  const v4u* q_lane;                                     // the queries in LDS, from this lane's on
+  v4u q[kHeld > 0 ? kHeld : 1][kChunks];
+  const v4u* q_lane;                                     // those in LDS, from this lane's on
   uint32_t kc[kTiles][kKeyWords], kb[kTiles][kKeyBlocks];
   uint32_t vc[kMine][kWords4], vb[kMine];
 
@@ -65,19 +67,18 @@ struct Wave4 : Wave<T, false, D, NQ, 32, (NQ > 1), (NQ > 1 ? 8 : 0)> {
     return (x & v4u{keep, keep, keep, keep}) ^ v4u{flip, flip, flip, flip};
   }
 
-  // Loads the queries: into registers, or by the whole workgroup into `lds` (NQ * kChunks * 64 of it), between barriers.
+  // Loads the queries: into registers, and by the whole workgroup into `lds` (kInLds * kChunks * 64 of it), between barriers.
   __device__ __forceinline__ void load_q(const char* p, int rows, uint32_t keep, uint32_t flip, v4u* lds) {
-    if constexpr (kShared) {
+#pragma unroll
+    for (int n = 0; n < kHeld; ++n)
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c) q[n][c] = query(p, n, c, rows, keep, flip);
+    if constexpr (kInLds > 0) {
       q_lane = lds + this->lane;
       __syncthreads();
-      for (int x = threadIdx.x >> 6; x < NQ * kChunks; x += blockDim.x >> 6)
-        lds[64 * x + this->lane] = query(p, x / kChunks, x % kChunks, rows, keep, flip);
+      for (int x = threadIdx.x >> 6; x < kInLds * kChunks; x += blockDim.x >> 6)
+        lds[64 * x + this->lane] = query(p, kHeld + x / kChunks, x % kChunks, rows, keep, flip);
       __syncthreads();
-    } else {
-#pragma unroll
-      for (int n = 0; n < NQ; ++n)
-#pragma unroll
-        for (int c = 0; c < kChunks; ++c) q[n][c] = query(p, n, c, rows, keep, flip);
     }
   }
 
@@ -89,40 +90,24 @@ struct Wave4 : Wave<T, false, D, NQ, 32, (NQ > 1), (NQ > 1 ? 8 : 0)> {
     }
   }
 
-  // Scores of query tile N over steps [4 h, 4 h + 4) of the keys x.
-  template <int N>
-  __device__ __forceinline__ void score_tile(v4f (&s)[kTiles], const v4u (&x)[kSteps][kTiles], int h) const {
-    v4u y[4];
-#pragma unroll
-    for (int c = 0; c < kSteps; ++c) {
-      if constexpr (kShared) y[c] = q_lane[(N * kChunks + 4 * h + c) * 64];
-      else y[c] = q[N][4 * h + c];
-    }
-    if (h == 0)
-#pragma unroll
-      for (int a = 0; a < kTiles; ++a) s[a] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-    for (int c = 0; c < kSteps; ++c)
-#pragma unroll
-      for (int a = 0; a < kTiles; ++a) s[a] = T::mfma(x[c][a], y[c], s[a]);
-  }
-
-  template <int N>
-  __device__ __forceinline__ void score_tiles(v4f (&s)[NQ][kTiles], const v4u (&x)[kSteps][kTiles], int h) const {
-    if constexpr (N < NQ) {
-      score_tile<N>(s[N], x, h);
-      score_tiles<N + 1>(s, x, h);
-    }
-  }
-
-  // Scores of the tile that lies in kc and kb, 128 dims at a time.
+  // Scores of the tile that lies in kc and kb: 32 dims of every key at a time, under all queries.
   __device__ __forceinline__ void scores(v4f (&s)[NQ][kTiles]) const {
 #pragma unroll
-    for (int h = 0; h < (kChunks + 3) / 4; ++h) {
-      v4u x[kSteps][kTiles];
+    for (int n = 0; n < NQ; ++n)
 #pragma unroll
-      for (int i = 0; i < kSteps; ++i) keys_of(4 * h + i, x[i]);
-      score_tiles<0>(s, x, h);
+      for (int a = 0; a < kTiles; ++a) s[n][a] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+      v4u x[kTiles];
+      keys_of(c, x);
+#pragma unroll
+      for (int n = 0; n < NQ; ++n) {
+        v4u y;
+        if (n < kHeld) y = q[n < kHeld ? n : 0][c];
+        else y = q_lane[((n - kHeld) * kChunks + c) * 64];
+#pragma unroll
+        for (int a = 0; a < kTiles; ++a) s[n][a] = T::mfma(x[a], y, s[n][a]);
+      }
     }
     settle(s);
   }
@@ -545,7 +530,7 @@ __global__ void __launch_bounds__(64 * ring_waves(D, NQ, NH), ring_waves_per_sim
   constexpr int kGroups = ring_groups(NH);
   __shared__ Plan<R::kWaves> plan;
   __shared__ __align__(16) Space<T, D, NQ, NH> lds;
-  __shared__ v4u q_lds[W::kShared ? NQ * W::kChunks * 64 : 1];
+  __shared__ v4u q_lds[W::kInLds > 0 ? W::kInLds * W::kChunks * 64 : 1];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t* prefix = plan.make(a);
   const int group = group_of<NQ>(a), qg = (a.G + 16 * NQ - 1) / (16 * NQ);
@@ -729,7 +714,7 @@ __global__ void __launch_bounds__(64 * ring_waves(D, NQ, NH), ring_waves_per_sim
   typedef Ring4<T, D, NQ, NH> R;
   __shared__ int list[kKvSelBlock];
   __shared__ __align__(16) Space<T, D, NQ, NH> lds;
-  __shared__ v4u q_lds[W::kShared ? NQ * W::kChunks * 64 : 1];
+  __shared__ v4u q_lds[W::kInLds > 0 ? W::kInLds * W::kChunks * 64 : 1];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int qg = (a.G + 16 * NQ - 1) / (16 * NQ);
   ListPart p;
