@@ -687,14 +687,15 @@ def mqa_kv_compact(keep, kept, src_table, dst_table, arrays, stream=None):
 
 def _kv_tensor(t, name, dtype, dims):
     """t is a tensor of this type and number of dimensions (its last one contiguous); its shape and strides."""
-    if not isinstance(t, _kv()[0].Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    shape, stride = t.shape, t.stride()
+    try:
+        if t.dtype is not dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        shape, stride = t.shape, t.stride()
+    except AttributeError:
+        raise TypeError(f"{name} must be a torch.Tensor") from None
     if len(shape) != dims:
         raise ValueError(f"{name} must have {dims} dimensions, got {list(shape)}")
-    if shape[-1] > 1 and stride[-1] != 1 and t.numel():
+    if stride[-1] != 1 and shape[-1] > 1 and t.numel():
         raise ValueError(f"{name}: the elements of one head must be contiguous")
     return shape, stride
 
@@ -759,48 +760,67 @@ def mqa_kv_attention_selected_fp4(q, k_pages, k_scale, v_pages, v_scale, slots, 
 
 
 # --- new heads: norm, rotation, appending (include/mqa_kv_append.h) ---------------------
+#
+# A decode step's launch takes the device three to four microseconds, and a call names up to fifteen tensors: the checks
+# look at as few of a tensor's attributes as will do (a tenth of a microsecond each).
 
 _KV_NO_ROWS = _KV_ROWS.pack(0, 0, 0, 0, 0, 0.0, 0)
 
 
-def _kv_rows(x, name, weight, weight_offset, out=None, like=None, outputs=False):
-    """mqa_kv_rows of x [T, H, D] (of `like`'s type, rows and D, if given) and its output."""
+def _kv_heads(t, name, kind, T, D, H=None):
+    """Address, row stride and number of heads of t, of this type and [T, H (any if None), D], the heads of a row contiguous."""
+    try:
+        if t.dtype is kind:
+            n, heads, dim = t.shape
+            if n == T and dim == D and (H is None or heads == H):
+                if t.is_contiguous():
+                    return t.data_ptr(), heads * D, heads
+                row, head, element = t.stride()
+                if (element == 1 or D == 1) and (head == D or heads <= 1):
+                    return t.data_ptr(), row if T > 1 else heads * D, heads
+                raise ValueError(f"the heads of one row of {name} must be contiguous")
+    except (AttributeError, ValueError) as e:
+        if not hasattr(t, "dtype"):
+            raise TypeError(f"{name} must be a torch.Tensor") from None
+        if "contiguous" in str(e):
+            raise
+    raise ValueError(f"{name} must be {kind} [{T}, {'H' if H is None else H}, {D}], got {t.dtype} {list(t.shape)}")
+
+
+def _kv_rows_of(x, name):
+    """Type, T and D of rows of heads."""
+    try:
+        kind, (T, _, D) = x.dtype, x.shape
+    except (AttributeError, ValueError):
+        if not hasattr(x, "shape"):
+            raise TypeError(f"{name} must be a torch.Tensor") from None
+        raise ValueError(f"{name} must be [T, H, D], got {list(x.shape)}") from None
     torch = _kv()[0]
-    if not isinstance(x, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    kind, shape = x.dtype, x.shape
-    if kind != torch.bfloat16 and kind != torch.float16:
+    if kind is not torch.bfloat16 and kind is not torch.float16:
         raise TypeError(f"{name} must be bfloat16 or float16, got {kind}")
-    if len(shape) != 3:
-        raise ValueError(f"{name} must be [T, H, D], got {list(shape)}")
-    T, H, D = shape
-    if like is not None and (kind != like.dtype or T != like.shape[0] or D != like.shape[2]):
-        raise ValueError(f"{name} must be {like.dtype} [{like.shape[0]}, H, {like.shape[2]}], got {kind} {list(shape)}")
-    rows = []
-    for t, what in ((x, name), (out, name + "_out"))[: 2 if outputs else 1]:
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{what} must be a torch.Tensor")
-        if t.dtype != kind or t.shape != shape:
-            raise ValueError(f"{what} must be {kind} {list(shape)}, got {t.dtype} {list(t.shape)}")
-        row, head, element = t.stride()
-        if T > 0 and ((D > 1 and element != 1) or (H > 1 and head != D)):
-            raise ValueError(f"the heads of one row of {what} must be contiguous")
-        rows += [t.data_ptr(), row if T > 1 else H * D]
-    if not outputs:
-        rows += [0, 0]
-    if weight is not None:
-        weight = _kv_check(weight, name + "_weight", kind, (D,))
-    return _KV_ROWS.pack(*rows, weight or 0, _f32(weight_offset), H)
+    return kind, T, D
 
 
-def _kv_turn(D, T, position, inv_freq, eps, rotary_offset, interleaved):
+def _kv_turned(x, out, name, kind, T, D, weight, weight_offset):
+    """mqa_kv_rows of x and of where its rows go."""
+    at, row, heads = _kv_heads(x, name, kind, T, D)
+    to, to_row, _ = _kv_heads(out, name + "_out", kind, T, D, heads)
+    return _KV_ROWS.pack(at, row, to, to_row, 0 if weight is None else _kv_check(weight, name + "_weight", kind, (D,)),
+                         weight_offset, heads)
+
+
+def _kv_turn(T, position, inv_freq, eps, rotary_offset, interleaved):
     """mqa_kv_turn; position may be None."""
-    torch = _kv()[0]
     if inv_freq is None:
-        return _KV_TURN.pack(0, 0, 0, 0, 0, _f32(eps))
-    freq = _kv_check(inv_freq, "inv_freq", torch.float32, (getattr(inv_freq, "shape", (0,)) or (0,))[:1])
-    at = 0 if position is None else _kv_check(position, "position", torch.int32, (T,))
-    return _KV_TURN.pack(freq, at or 0, 2 * inv_freq.shape[0], int(rotary_offset), int(bool(interleaved)), _f32(eps))
+        return _KV_TURN.pack(0, 0, 0, 0, 0, eps)
+    torch = _kv()[0]
+    try:
+        half, = inv_freq.shape
+    except (AttributeError, ValueError):
+        raise (ValueError if hasattr(inv_freq, "shape") else TypeError)("inv_freq must be a tensor of one dimension") from None
+    return _KV_TURN.pack(_kv_check(inv_freq, "inv_freq", torch.float32, (half,)),
+                         0 if position is None else _kv_check(position, "position", torch.int32, (T,)), 2 * half,
+                         int(rotary_offset), 1 if interleaved else 0, eps)
 
 
 def mqa_kv_norm_rotate(q, q_out, position=None, k=None, k_out=None, inv_freq=None, q_weight=None, k_weight=None, eps=1e-6,
@@ -810,31 +830,44 @@ def mqa_kv_norm_rotate(q, q_out, position=None, k=None, k_out=None, inv_freq=Non
     on by position int32 [T] times inv_freq float32 [R / 2] (halves i and i + R / 2, or with `interleaved` dims 2 i and
     2 i + 1), and writes q_out (q's shape; q itself, or apart from it); the same with k, k_out and k_weight in one
     launch. Without a weight there is no norm, without inv_freq no rotation. Capturable."""
-    rows = _kv_rows(q, "q", q_weight, weight_offset, q_out, outputs=True)
-    T, _, D = q.shape
-    keys = None if k is None else _kv_rows(k, "k", k_weight, weight_offset, k_out, like=q, outputs=True)
-    if k is None and (k_weight is not None or k_out is not None):
+    kind, T, D = _kv_rows_of(q, "q")
+    eps, weight_offset = _f32(eps), _f32(weight_offset)
+    rows = _kv_turned(q, q_out, "q", kind, T, D, q_weight, weight_offset)
+    if k is not None:
+        keys = _kv_turned(k, k_out, "k", kind, T, D, k_weight, weight_offset)
+    elif k_weight is not None or k_out is not None:
         raise ValueError("k_weight and k_out go with k")
-    turn = _kv_turn(D, T, position, inv_freq, eps, rotary_offset, interleaved)
-    rc = lib().mqa_kv_norm_rotate(rows, keys, turn, T, D, _kv()[1][q.dtype], _kv_stream(stream, q.device))
-    _rc(rc, "mqa_kv_norm_rotate")
+    else:
+        keys = None
+    rc = (_lib or lib()).mqa_kv_norm_rotate(rows, keys, _kv_turn(T, position, inv_freq, eps, rotary_offset, interleaved), T, D,
+                                            _kv()[1][kind], _kv_stream(stream, q.device))
+    if rc:
+        _rc(rc, "mqa_kv_norm_rotate")
 
 
-def _kv_append(what, k, v, cache, block_table, seq_of_row, position, rotary_position, inv_freq, k_weight, eps, weight_offset,
-               rotary_offset, interleaved, q, q_out, q_weight, stream):
+def _kv_append(what, kind, T, D, heads, k, v, cache, block_table, seq_of_row, position, rotary_position, inv_freq, k_weight, eps,
+               weight_offset, rotary_offset, interleaved, q, q_out, q_weight, stream):
     i32 = _kv()[0].int32
-    keys = _kv_rows(k, "k", k_weight, weight_offset)
-    T, _, D = k.shape
-    values = _KV_NO_ROWS if v is None else _kv_rows(v, "v", None, 0.0, like=k)
-    queries = None if q is None else _kv_rows(q, "q", q_weight, weight_offset, q_out, like=k, outputs=True)
-    if q is None and (q_weight is not None or q_out is not None):
+    eps, weight_offset = _f32(eps), _f32(weight_offset)
+    at, row, _ = _kv_heads(k, "k", kind, T, D, heads)
+    keys = _KV_ROWS.pack(at, row, 0, 0, 0 if k_weight is None else _kv_check(k_weight, "k_weight", kind, (D,)), weight_offset, heads)
+    values = _KV_NO_ROWS
+    if v is not None:
+        at, row, _ = _kv_heads(v, "v", kind, T, D, heads)
+        values = _KV_ROWS.pack(at, row, 0, 0, 0, 0.0, heads)
+    if q is not None:
+        queries = _kv_turned(q, q_out, "q", kind, T, D, q_weight, weight_offset)
+    elif q_weight is not None or q_out is not None:
         raise ValueError("q_weight and q_out go with q")
-    turn = _kv_turn(D, T, rotary_position, inv_freq, eps, rotary_offset, interleaved)
+    else:
+        queries = None
     table, n_seq, pages = _kv_table(block_table, "block_table", None)
-    new = _KV_NEW.pack(T, _kv()[1][k.dtype], table, n_seq, pages, _kv_check(seq_of_row, "seq_of_row", i32, (T,)),
+    new = _KV_NEW.pack(T, _kv()[1][kind], table, n_seq, pages, _kv_check(seq_of_row, "seq_of_row", i32, (T,)),
                        _kv_check(position, "position", i32, (T,)))
-    rc = getattr(lib(), what)(keys + values + new + turn, queries, cache, _kv_stream(stream, k.device))
-    _rc(rc, what)
+    turn = _kv_turn(T, rotary_position, inv_freq, eps, rotary_offset, interleaved)
+    rc = getattr(_lib or lib(), what)(keys + values + new + turn, queries, cache, _kv_stream(stream, k.device))
+    if rc:
+        _rc(rc, what)
 
 
 def mqa_kv_append(k, v, k_pages, v_pages, block_table, seq_of_row, position, k_scale=1.0, v_scale=1.0,
@@ -846,26 +879,29 @@ def mqa_kv_append(k, v, k_pages, v_pages, block_table, seq_of_row, position, k_s
     -1 is padding. Keys are normed by k_weight and rotated by rotary_position (position if None) times inv_freq on
     the way, and in the same launch queries q into q_out, as in mqa_kv_norm_rotate. Capturable."""
     torch, types, _ = _kv()
-    if not isinstance(k, torch.Tensor) or k.dim() != 3:
-        raise (ValueError if isinstance(k, torch.Tensor) else TypeError)("k must be a tensor [T, Hkv, D]")
+    kind, T, D = _kv_rows_of(k, "k")
     if (v is None) != (v_pages is None):
         raise ValueError("v and v_pages go together")
-    _, H, D = k.shape
-    tensors, strides = (k_pages,) if v is None else (k_pages, v_pages), []
-    for t, name in zip(tensors, ("k_pages", "v_pages")):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
-        if t.dtype != k.dtype and t.dtype != torch.float8_e4m3fn or t.dtype != k_pages.dtype:
-            raise TypeError(f"{name} must be {k.dtype} or float8_e4m3fn, got {t.dtype}")
-        shape, stride = _kv_tensor(t, name, t.dtype, 4)
-        if shape != (k_pages.shape[0], 64, H, D):
-            raise ValueError(f"{name} must be [P, 64, {H}, {D}], got {list(shape)}")
-        strides += stride[:3]
-    kind = types.get(k_pages.dtype)
-    cache = _KV_CACHE.pack(k_pages.data_ptr(), 0 if v is None else v_pages.data_ptr(), *strides, *([0] * (6 - len(strides))),
-                           k_pages.shape[0], H, D, kind, _f32(k_scale), _f32(v_scale))
-    _kv_append("mqa_kv_append", k, v, cache, block_table, seq_of_row, position, rotary_position, inv_freq, k_weight, eps,
-               weight_offset, rotary_offset, interleaved, q, q_out, q_weight, stream)
+    H = k.shape[1]
+    held = getattr(k_pages, "dtype", None)
+    if held is not kind and held is not torch.float8_e4m3fn:
+        raise TypeError(f"k_pages must be {kind} or float8_e4m3fn, got {held}")
+    shape, stride = _kv_tensor(k_pages, "k_pages", held, 4)
+    P, page, heads, dim = shape
+    if page != 64 or heads != H or dim != D:
+        raise ValueError(f"k_pages must be [P, 64, {H}, {D}], got {list(shape)}")
+    k_page, k_pos, k_head, _ = stride
+    v_ptr = v_page = v_pos = v_head = 0
+    if v_pages is not None:
+        got, stride = _kv_tensor(v_pages, "v_pages", held, 4)
+        if got != shape:
+            raise ValueError(f"v_pages must be {list(shape)}, got {list(got)}")
+        v_page, v_pos, v_head, _ = stride
+        v_ptr = v_pages.data_ptr()
+    cache = _KV_CACHE.pack(k_pages.data_ptr(), v_ptr, k_page, k_pos, k_head, v_page, v_pos, v_head, P, H, D, types[held],
+                           _f32(k_scale), _f32(v_scale))
+    _kv_append("mqa_kv_append", kind, T, D, H, k, v, cache, block_table, seq_of_row, position, rotary_position, inv_freq, k_weight,
+               eps, weight_offset, rotary_offset, interleaved, q, q_out, q_weight, stream)
 
 
 def mqa_kv_append_fp4(k, v, k_pages, k_scale, v_pages, v_scale, block_table, seq_of_row, position, rotary_position=None,
@@ -874,13 +910,11 @@ def mqa_kv_append_fp4(k, v, k_pages, k_scale, v_pages, v_scale, block_table, seq
     """mqa_kv_append into a cache in 4 bits (codes uint8 [P, 64, Hkv, D / 2], scales uint8 [P, 64, Hkv, D / 32]), by
     the rule of mqa_fp4_quantize. With one key head of 128 dims, keys only, these are the indexer's own pages
     (k_pages[:, :, None], k_scale[:, :, None]). Capturable."""
-    torch = _kv()[0]
-    if not isinstance(k, torch.Tensor) or k.dim() != 3:
-        raise (ValueError if isinstance(k, torch.Tensor) else TypeError)("k must be a tensor [T, Hkv, D]")
+    kind, T, D = _kv_rows_of(k, "k")
     if (v is None) != (v_pages is None):
         raise ValueError("v and v_pages go together")
-    cache, heads = _kv_cache_fp4(k.shape[2], k_pages, k_scale, v_pages, v_scale)
+    cache, heads = _kv_cache_fp4(D, k_pages, k_scale, v_pages, v_scale)
     if heads != k.shape[1]:
         raise ValueError(f"k_pages has {heads} key heads, k {k.shape[1]}")
-    _kv_append("mqa_kv_append_fp4", k, v, cache, block_table, seq_of_row, position, rotary_position, inv_freq, k_weight, eps,
-               weight_offset, rotary_offset, interleaved, q, q_out, q_weight, stream)
+    _kv_append("mqa_kv_append_fp4", kind, T, D, heads, k, v, cache, block_table, seq_of_row, position, rotary_position, inv_freq,
+               k_weight, eps, weight_offset, rotary_offset, interleaved, q, q_out, q_weight, stream)
