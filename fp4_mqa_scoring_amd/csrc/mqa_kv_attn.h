@@ -369,6 +369,9 @@ struct Wave {
 // tile's keys are loaded into the registers that the first product has just read,
 // its values into those that the second has.
 
+// A barrier for what lies in LDS alone: loads from memory and stores to it that are on their way stay so.
+__device__ __forceinline__ void lds_barrier() { __asm__ __volatile__("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
 // Joins a workgroup's waves' results in LDS and writes the heads' outputs, or their partial
 // sums where part_o is not null. `bad`: an invalid page or slot was met.
 template <class T, int D, int WAVES = kWaves>
@@ -379,13 +382,13 @@ struct Merge {
   float2 ml[WAVES][16];
   float2 fin[16];
 
-  template <int N = 0, class W>   // N: which 16 heads
+  template <class W>
   __device__ __forceinline__ void run(W& w, bool bad, int rows, float v_scale, char* out, float* lse, float* part_o,
                                       float2* part_ml) {
     const int wave = threadIdx.x >> 6;
     __syncthreads();   // the previous use of this memory is over
-    const float mine = groups_sum(w.l[N]);
-    if (w.grp == 0) ml[wave][w.col] = make_float2(w.m[N], bad ? __builtin_nanf("") : mine);
+    const float mine = groups_sum(w.l[0]);
+    if (w.grp == 0) ml[wave][w.col] = make_float2(w.m[0], bad ? __builtin_nanf("") : mine);
     __syncthreads();
     float2 x[WAVES];
     float top = -__builtin_inff(), total = 0.0f;
@@ -397,7 +400,7 @@ struct Merge {
     const float ref = top == -__builtin_inff() ? 0.0f : top;
 #pragma unroll
     for (int i = 0; i < WAVES; ++i) total += x[i].y * __builtin_amdgcn_exp2f(x[i].x - ref);
-    const float f = __builtin_amdgcn_exp2f(w.m[N] - ref);
+    const float f = __builtin_amdgcn_exp2f(w.m[0] - ref);
     if (wave == 0 && w.grp == 0) fin[w.col] = make_float2(top, total);
     constexpr int kT = kPart / 16;   // matrix tiles of a part
 #pragma unroll
@@ -408,8 +411,8 @@ struct Merge {
 #pragma unroll
         for (int t = 0; t < kT; t += 4)
           *reinterpret_cast<v4f*>(&o[wave][w.col][(4 * w.grp + i) * kT + t]) =
-              v4f{w.o[N][t0 + t][i] * f, w.o[N][t0 + t + 1][i] * f, w.o[N][t0 + t + 2][i] * f,
-                  w.o[N][t0 + t + 3][i] * f};
+              v4f{w.o[0][t0 + t][i] * f, w.o[0][t0 + t + 1][i] * f, w.o[0][t0 + t + 2][i] * f,
+                  w.o[0][t0 + t + 3][i] * f};
       __syncthreads();
       for (int e = threadIdx.x; e < 16 * kPart / 4; e += 64 * WAVES) {
         const int head = e / (kPart / 4), at = 4 * (e % (kPart / 4));
@@ -627,7 +630,7 @@ struct Segment {
     r = __builtin_amdgcn_readfirstlane(static_cast<int>(lo));   // Q < 2^24
     n = prefix[r + 1] - prefix[r];
     const int64_t in_row = *cur - prefix[r] * gh;
-    g = __builtin_amdgcn_readfirstlane(static_cast<int>(in_row / n));
+    g = __builtin_amdgcn_readfirstlane(static_cast<int>(gh == 1 ? 0 : in_row / n));
     pa = __builtin_amdgcn_readfirstlane(static_cast<int>(in_row - g * n));
     const int64_t left = stop - *cur;
     pb = __builtin_amdgcn_readfirstlane(static_cast<int>(n - pa < left ? n : pa + left));

@@ -60,26 +60,46 @@ struct Wave4 : Wave<T, false, D, NQ, 32, true, (NQ > 1 ? 8 : 0)> {
   }
 
   // This lane's part of step c of query tile n, of heads [0, rows) at `p`.
-  __device__ __forceinline__ v4u query(const char* p, int n, int c, int rows, uint32_t keep, uint32_t flip) const {
+  __device__ __forceinline__ v4u query(const char* p, int n, int c, int rows) const {
     const int h = 16 * n + col;
     v4u x = {0, 0, 0, 0};
     if (h < rows) x = *reinterpret_cast<const v4u*>(p + (static_cast<int64_t>(h) * D + step_dim(c)) * 2);
-    return (x & v4u{keep, keep, keep, keep}) ^ v4u{flip, flip, flip, flip};
+    return x;
   }
 
-  // Loads the queries: into registers, and by the whole workgroup into `lds` (kInLds * kChunks * 64 of it), between barriers.
+  // Asks for the queries that stay in registers, and loads the others, by the whole workgroup, into `lds` (kInLds *
+  // kChunks * 64 of it, which nobody reads any more).
+  template <int WAVES>
   __device__ __forceinline__ void load_q(const char* p, int rows, uint32_t keep, uint32_t flip, v4u* lds) {
 #pragma unroll
     for (int n = 0; n < kHeld; ++n)
 #pragma unroll
-      for (int c = 0; c < kChunks; ++c) q[n][c] = query(p, n, c, rows, keep, flip);
+      for (int c = 0; c < kChunks; ++c) q[n][c] = query(p, n, c, rows);
     if constexpr (kInLds > 0) {
       q_lane = lds + this->lane;
-      __syncthreads();
-      for (int x = threadIdx.x >> 6; x < kInLds * kChunks; x += blockDim.x >> 6)
-        lds[64 * x + this->lane] = query(p, kHeld + x / kChunks, x % kChunks, rows, keep, flip);
-      __syncthreads();
+      constexpr int kPer = (kInLds * kChunks + WAVES - 1) / WAVES;
+      v4u x[kPer];   // all asked for before the first is waited for
+      const int first = threadIdx.x >> 6;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int at = first + WAVES * i;
+        x[i] = query(p, kHeld + at / kChunks, at % kChunks, at < kInLds * kChunks ? rows : 0);
+      }
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int at = first + WAVES * i;
+        if (at < kInLds * kChunks) lds[64 * at + this->lane] = (x[i] & v4u{keep, keep, keep, keep}) ^ v4u{flip, flip, flip, flip};
+      }
+      lds_barrier();
     }
+  }
+
+  // Takes those in registers, once their tiles' first copies are on their way.
+  __device__ __forceinline__ void take_q(uint32_t keep, uint32_t flip) {
+#pragma unroll
+    for (int n = 0; n < kHeld; ++n)
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c) q[n][c] = (q[n][c] & v4u{keep, keep, keep, keep}) ^ v4u{flip, flip, flip, flip};
   }
 
   __device__ __forceinline__ void keys_of(int c, v4u (&x)[kTiles]) const {
@@ -412,17 +432,17 @@ struct Ring4 {
 
   // This wave's tiles t, t + kWaves, ... below t_hi. keys(t, stage) and values(t, stage) issue the copies of one
   // piece, values those of the tile that keys was last called for; range(t, &lo, &hi) gives the positions that count.
-  template <class KEYS, class VALUES, class RANGE>
-  __device__ __forceinline__ void run(W (&w)[NH], int wave, int t, int t_hi, float c, KEYS&& keys, VALUES&& values, RANGE&& range) {
-    if (t >= t_hi) return;
+  // ready() is called by every wave once its first copies are on their way. Other loads and stores may be in flight
+  // when the copies are counted: loads arrive in order, so one more of either only makes a wait longer.
+  template <class KEYS, class VALUES, class RANGE, class READY>
+  __device__ __forceinline__ void run(W (&w)[NH], int wave, int t, int t_hi, float c, KEYS&& keys, VALUES&& values, RANGE&& range,
+                                      READY&& ready) {
     const uint32_t ring = lds_address(&piece[wave][0][0][0]);
     // byte of the word that holds the scale of this lane's keys, and of its values
     const int col = w[0].col, grp = w[0].grp;
     const uint32_t k_shift = 8 * (D == 64 ? grp >> 1 : grp) + 9;
     const uint32_t v_shift = 8 * (D == 64 ? col >> 3 : D == 128 ? col >> 2 : col >> 1 & 3) + 9;
-    // no other load or store of this wave is in flight when the copies are counted
-    __asm__ __volatile__("s_waitcnt vmcnt(0)" ::: "memory");
-    const int tiles = (t_hi - t + kWaves - 1) / kWaves;
+    const int tiles = t < t_hi ? (t_hi - t + kWaves - 1) / kWaves : 0;
 #pragma unroll
     for (int i = 0; i < kDepth; ++i)
       if (i < tiles) {
@@ -431,6 +451,7 @@ struct Ring4 {
         values(t + kWaves * i, i);
         __asm__ __volatile__("" ::: "memory");
       }
+    ready();
     int stage = 0;
     for (int i = 0; i < tiles; ++i, t += kWaves) {
       int lo, hi;
@@ -476,24 +497,110 @@ struct Ring4 {
 template <int NQ>
 __device__ __forceinline__ int group_of(const KvFp4Args& a) { return a.G < 16 * NQ ? a.G : 16 * NQ; }
 
-// Joins the waves' results, 16 heads at a time.
-template <int N, class T, int D, class MERGE, class W>
-__device__ __forceinline__ void join_waves(MERGE& merge, W& w, bool bad, int rows, char* out, float* lse, float* part_o,
-                                           float2* part_ml) {
-  if constexpr (N < W::kQueries) {
-    if (16 * N >= rows) return;
-    constexpr int64_t at = 16 * N;
-    merge.template run<N>(w, bad, rows - 16 * N < 16 ? rows - 16 * N : 16, 1.0f, out + at * D * 2, lse == nullptr ? nullptr : lse + at,
-                          part_o == nullptr ? nullptr : part_o + at * D, part_ml + at);
-    join_waves<N + 1, T, D>(merge, w, bad, rows, out, lse, part_o, part_ml);
+// Joins a workgroup's waves' results in LDS and writes the heads' outputs, or their partial sums where part_o is not
+// null. Each wave ends up with 16 heads, or where there are more waves than tiles of 16 heads with some dims of them,
+// and adds up what all of them have of those: a lane reads what the same lane of each wave has written, so that the
+// numbers cross LDS in the order of the registers. All tiles at once, in up to four rounds. (One tile of 16 heads after
+// another, every thread adding up four dims and a wait for the stores between them, took 64 heads 15,000 of a short
+// sequence's 35,000 cycles; so 7,400. One sequence of 1,500 positions 18.0 -> 15.4 us, 8 of 16,000 36 -> 31 us; up to 16
+// heads the same but for 0.2 us more for one short sequence.)
+template <class T, int D, int NQ, int NH>
+struct Merge4 {
+  typedef Wave4<T, D, NQ> W;
+  static constexpr int kWaves = ring_waves(D, NQ, NH), kSets = NQ * NH, kDims = D / 16;
+  // waves of a tile of 16 heads: four matrix tiles of dims each at least, so that 16 bytes are stored at a time
+  static constexpr int kShares = kWaves / kSets < kDims / 4 ? kWaves / kSets : kDims / 4;
+  static constexpr int kOwn = kDims / kShares;            // matrix tiles of dims of a wave
+  // of which a round takes so many: less beside queries in LDS, which have to lie apart from everything that copies write
+  static constexpr int kStep = W::kInLds > 0 ? 2 : 4;
+  static_assert(kShares >= 1 && kOwn * kShares == kDims && kOwn % kStep == 0, "every tile has its wave");
+  v4f part[kSets * kShares][kStep][kWaves][64];
+  float2 ml[kWaves][kSets][16];
+
+  // The largest of the waves' maxima of a tile's head, and the sum that goes with it.
+  __device__ __forceinline__ float top_of(int set, int col) const {
+    float top = ml[0][set][col].x;
+#pragma unroll
+    for (int i = 1; i < kWaves; ++i) top = fmaxf(top, ml[i][set][col].x);
+    return top;
   }
-}
+
+  // out, lse, part_o, part_ml: of the first head; those of the next key head lie `heads` and `parts` rows behind.
+  __device__ __forceinline__ void run(W (&w)[NH], int wave, bool bad, int rows, int64_t heads, int64_t parts, char* out, float* lse,
+                                      float* part_o, float2* part_ml) {
+    const int col = w[0].col, grp = w[0].grp, lane = w[0].lane;
+    lds_barrier();   // every wave has its tiles behind it
+#pragma unroll
+    for (int set = 0; set < kSets; ++set) {
+      const float l = groups_sum(w[set / NQ].l[set % NQ]);
+      if (grp == 0) ml[wave][set][col] = make_float2(w[set / NQ].m[set % NQ], bad ? __builtin_nanf("") : l);
+    }
+    lds_barrier();
+    float f[kSets];
+#pragma unroll
+    for (int set = 0; set < kSets; ++set) f[set] = __builtin_amdgcn_exp2f(w[set / NQ].m[set % NQ] - top_of(set, col));
+    const int mine = wave / kShares, piece = wave % kShares;   // this wave's tile of heads, its dims
+    const bool owner = mine < kSets && 16 * (mine % NQ) < rows;
+    v4f sum[kOwn];
+#pragma unroll
+    for (int at = 0; at < kOwn; at += kStep) {
+      if (at > 0) lds_barrier();
+#pragma unroll
+      for (int set = 0; set < kSets; ++set)
+        if (16 * (set % NQ) < rows) {
+#pragma unroll
+          for (int s = 0; s < kShares; ++s)
+#pragma unroll
+            for (int j = 0; j < kStep; ++j) part[set * kShares + s][j][wave][lane] = w[set / NQ].o[set % NQ][s * kOwn + at + j] * f[set];
+        }
+      lds_barrier();
+      if (owner) {
+#pragma unroll
+        for (int j = 0; j < kStep; ++j) {
+          sum[at + j] = part[wave][j][0][lane];
+#pragma unroll
+          for (int i = 1; i < kWaves; ++i) sum[at + j] += part[wave][j][i][lane];
+        }
+      }
+    }
+    const int row = 16 * (mine % NQ) + col;
+    if (!owner || row >= rows) return;
+    const float top = top_of(mine, col);
+    float total = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i) total += ml[i][mine][col].y * __builtin_amdgcn_exp2f(ml[i][mine][col].x - top);
+    const int dim = 4 * grp * kDims + piece * kOwn;   // of sum[t][i]: dim + i * kDims + t
+    if (part_o != nullptr) {
+      const int64_t to = (mine / NQ) * parts + row;
+      if (piece == 0 && grp == 0) part_ml[to] = make_float2(top, total);
+      float* p = part_o + to * D + dim;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+#pragma unroll
+        for (int t = 0; t < kOwn; t += 4)
+          *reinterpret_cast<v4f*>(p + i * kDims + t) = v4f{sum[t][i], sum[t + 1][i], sum[t + 2][i], sum[t + 3][i]};
+      }
+      return;
+    }
+    const int64_t to = (mine / NQ) * heads + row;
+    if (piece == 0 && grp == 0 && lse != nullptr) lse[to] = lse_of<T>(top, total);
+    const float by = 1.0f / total;
+    char* p = out + (to * D + dim) * 2;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+      for (int t = 0; t < kOwn; t += 4)
+        *reinterpret_cast<v2u*>(p + 2 * (i * kDims + t)) =
+            v2u{T::pack(sum[t][i] * by, sum[t + 1][i] * by), T::pack(sum[t + 2][i] * by, sum[t + 3][i] * by)};
+    }
+  }
+};
 
 // A workgroup's LDS: the rings, and when the last tile is done the memory that joins the waves.
 template <class T, int D, int NQ, int NH>
 union Space {
   Ring4<T, D, NQ, NH> ring;
-  Merge<T, D, ring_waves(D, NQ, NH)> merge;
+  Merge4<T, D, NQ, NH> merge;
 };
 
 // --- decode form --------------------------------------------------------------
@@ -502,9 +609,9 @@ union Space {
 // of NH key heads and 16 NQ query heads of each. All sets of a share go to one die, next to each other in the launch: what one
 // workgroup leaves of a cache line that it reads a part of, the others find in the die's L2. `groups` workgroups at most; more sets
 // than that leave one share only.
-__host__ __device__ __forceinline__ int decode_shares(int64_t sets, int groups) {
-  if (sets <= groups / 8) return static_cast<int>(groups / (8 * sets) * 8);
-  return sets < groups ? static_cast<int>(groups / sets) : 1;
+__device__ __forceinline__ int decode_shares(uint32_t sets, uint32_t groups) {
+  if (sets <= groups / 8) return groups / (8 * sets) * 8;
+  return sets < groups ? groups / sets : 1;
 }
 
 // x, which every lane holds, as a scalar: what hangs on it (pages' addresses) is then computed once for the wave.
@@ -574,16 +681,16 @@ __global__ void __launch_bounds__(64 * ring_waves(D, NQ, NH), ring_waves_per_sim
     const char *kb = m.k + kvh * m.k_head, *vb = m.v + kvh * m.v_head;
     const char *ksb = m.ks + kvh * m.ks_head, *vsb = m.vs + kvh * m.vs_head;
     const int64_t head0 = r * m.H + static_cast<int64_t>(kvh) * m.G + first;
+    int next = t_lo + wave < t_hi ? table[(t_lo + wave) / 2] : 0;   // entry of the next tile's page, read early
 #pragma unroll
     for (int h = 0; h < NH; ++h) {
       w[h].start();
-      w[h].load_q(m.q + r * m.q_row + (static_cast<int64_t>(kvh + h) * m.G + first) * D * 2, rows, m.q_keep, m.q_flip, q_lds);
+      w[h].template load_q<R::kWaves>(m.q + r * m.q_row + (static_cast<int64_t>(kvh + h) * m.G + first) * D * 2, rows, m.q_keep, m.q_flip, q_lds);
     }
 
     const int64_t k_page = m.k_page, v_page = m.v_page, ks_page = m.ks_page, vs_page = m.vs_page;
     const int pages = static_cast<int>(m.P_phys);
     bool bad = false;
-    int next = t_lo + wave < t_hi ? table[(t_lo + wave) / 2] : 0;   // entry of the next tile's page, read early
     int64_t page = 0;
     // whole tiles are read: what a page holds outside the window is masked
     lds.ring.run(
@@ -611,18 +718,19 @@ __global__ void __launch_bounds__(64 * ring_waves(D, NQ, NH), ring_waves_per_sim
         [&](int t, int* lo, int* hi) {
           *lo = start - 32 * t;
           *hi = end - 32 * t;
+        },
+        [&]() {
+#pragma unroll
+          for (int h = 0; h < NH; ++h) w[h].take_q(m.q_keep, m.q_flip);
         });
     ArgsInMemory& e = fresh_args();
     if (bad && lane == 0) atomicOr(e.status, kStBadPage);
     const bool whole = sg.pa == 0 && sg.pb == sg.n;
     const int64_t slot = 2 * (static_cast<int64_t>(set) * shares + which) + (sg.pa == 0 ? 1 : 0);
-#pragma unroll
-    for (int h = 0; h < NH; ++h) {
-      const int64_t head = head0 + static_cast<int64_t>(h) * e.G, part = (slot * NH + h) * group;
-      join_waves<0, T, D>(lds.merge, w[h], bad, rows, static_cast<char*>(e.out) + head * D * 2, e.lse == nullptr ? nullptr : e.lse + head,
-                          whole ? nullptr : e.part_o + part * D, e.part_ml + part);
-    }
-    __syncthreads();   // the rings may be filled again
+    const int64_t part = slot * NH * group;
+    lds.merge.run(w, wave, bad, rows, e.G, group, static_cast<char*>(e.out) + head0 * D * 2, e.lse == nullptr ? nullptr : e.lse + head0,
+                  whole ? nullptr : e.part_o + part * D, e.part_ml + part);
+    lds_barrier();   // the rings may be filled again
   }
 }
 
@@ -640,7 +748,7 @@ __global__ void __launch_bounds__(kThreads) kv_decode_fp4_join_kernel(KvFp4Args 
     fill_row<T, D>(a, head, code != 0, WAVES > 1 ? threadIdx.x : threadIdx.x & 63, 64 * WAVES);
     return;
   }
-  const int qg = (a.G + 16 * NQ - 1) / (16 * NQ), shares = decode_shares(static_cast<int64_t>(a.Hkv / NH) * qg, ring_groups(NH));
+  const int qg = (a.G + 16 * NQ - 1) / (16 * NQ), shares = decode_shares(a.Hkv / NH * qg, ring_groups(NH));
   const int64_t share = unit_share(a, a.prefix[a.Q], shares);
   const int64_t w0 = before / share, w1 = (before + n - 1) / share;
   if (w0 == w1) return;   // one workgroup had all of it and wrote the output
@@ -733,7 +841,7 @@ __global__ void __launch_bounds__(64 * ring_waves(D, NQ, NH), ring_waves_per_sim
   for (int h = 0; h < NH; ++h) {
     w[h].init();
     w[h].start();
-    w[h].load_q(a.q + p.r * a.q_row + (static_cast<int64_t>(kvh + h) * a.G + first) * D * 2, rows, a.q_keep, a.q_flip, q_lds);
+    w[h].template load_q<R::kWaves>(a.q + p.r * a.q_row + (static_cast<int64_t>(kvh + h) * a.G + first) * D * 2, rows, a.q_keep, a.q_flip, q_lds);
   }
   ListTiles<R> tiles_of(a, kvh, wave, w[0].lane, lds_address(list));
   bool bad = false;
@@ -757,16 +865,18 @@ __global__ void __launch_bounds__(64 * ring_waves(D, NQ, NH), ring_waves_per_sim
                  [&](int t, int* lo, int* hi) {
                    *lo = 0;
                    *hi = tiles_of.len - 32 * t;
+                 },
+                 [&]() {
+                   if (b0 != p.from) return;
+#pragma unroll
+                   for (int h = 0; h < NH; ++h) w[h].take_q(a.q_keep, a.q_flip);
                  });
   }
   if (bad && threadIdx.x == 0) atomicOr(a.status, kStBadPage);
   const int group = group_of<NQ>(a);
-#pragma unroll
-  for (int h = 0; h < NH; ++h) {
-    const int64_t head = head0 + static_cast<int64_t>(h) * a.G, part = (p.item * NH + h) * group;
-    join_waves<0, T, D>(lds.merge, w[h], bad, rows, static_cast<char*>(a.out) + head * D * 2, a.lse == nullptr ? nullptr : a.lse + head,
-                        a.splits == 1 ? nullptr : a.part_o + part * D, a.part_ml + part);
-  }
+  const int64_t part = p.item * NH * group;
+  lds.merge.run(w, wave, bad, rows, a.G, group, static_cast<char*>(a.out) + head0 * D * 2, a.lse == nullptr ? nullptr : a.lse + head0,
+                a.splits == 1 ? nullptr : a.part_o + part * D, a.part_ml + part);
 }
 
 template <class T, int D, int NQ, int NH, int WAVES>
