@@ -11,8 +11,8 @@
 // compiler would wait for every copy in flight before an LDS read that it cannot prove apart.
 //
 // Few heads on a key head are bound by memory (32 sequences of 2K-16K positions, 32 heads on 8 of 128 dims: 82 us, 4.0
-// TB/s of codes and scales), 64 by the vector and matrix units together (64 sequences of 32K-131K on one key head: 227 us,
-// 54 and 38 % of the clocks; 2,048 lists of 1,024 slots 106 us, 53 and 27 %), short sequences by code that runs
+// TB/s of codes and scales), 64 by the vector and matrix units, which hardly run beside each other (64 sequences of
+// 32K-131K on one key head: 227 us, 54 and 38 % of the clocks; 2,048 lists of 1,024 slots 106 us, 53 and 27 %), short sequences by code that runs
 // once from a cold instruction cache (1,500 positions: 10.6 us, and 4.0 for the joining launch).
 #include "mqa_kv_attn.h"
 

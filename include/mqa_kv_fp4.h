@@ -32,7 +32,9 @@ extern "C" {
  * scales 2^32), and one page must span less than 2 GiB; the page stride of one page
  * and the head stride of one head are not looked at. A page that a window touches
  * is read in tiles of 32 positions; what it holds outside the window does not
- * matter. Nothing of other pages is read. */
+ * matter. Nothing of other pages is read.
+ * mqa_kv_compact moves such a cache as four arrays, one row of all heads to a position where
+ * those are contiguous; with D = 64 the scales need an even Hkv for that (whole words). */
 typedef struct mqa_kv_cache_fp4 {
   void* k;                        /* codes of keys and values (an attention only reads them) */
   void* v;
