@@ -300,6 +300,31 @@ def test_more_key_heads_than_shares():
     check_decode(c, q, *args, out, lse)
 
 
+@pytest.mark.parametrize("Hkv", [100, 131, 600])
+def test_many_key_heads_share_the_workgroups_unevenly(Hkv):
+    """50 pairs of 256 workgroups, 131 heads of 512, and one share only."""
+    c = Case([2500, 300, 65], Hkv, Hkv, 64, "bf16", seed=Hkv)
+    q = c.queries(4)
+    args = ([0, 1, 2, 0], [0, 3, 64, 1000], [2500, 300, 65, 2431])
+    out, lse = run_decode(c, q, *args)
+    check_decode(c, q, *args, out, lse)
+    slots, count = lists(c, 4, 130, 5, [130, 1, 0, 77])
+    out, lse = run_selected(c, q, slots, count)
+    check_selected(c, q, slots, count, out, lse)
+
+
+@pytest.mark.parametrize("rows", [1, 300])
+def test_lists_longer_than_lds_holds(rows):
+    """More slots than a workgroup has in LDS at once, 64 heads with queries in LDS and 16 with all in registers."""
+    for H, Hkv in ((64, 1), (32, 2)):
+        c = Case([4000], H, Hkv, 128, "bf16", seed=3 + H)
+        slots, count = lists(c, rows, 2700, 9, [2700, 1025, 2048, 1])
+        q = c.queries(rows)
+        out, lse = run_selected(c, q, slots, count)
+        some = list(range(min(rows, 6)))
+        check_selected(c, q[some], slots[some], count[some], out[some], lse[some])
+
+
 # --- the written example ---------------------------------------------------------------
 
 
