@@ -438,7 +438,7 @@ def _kv_stream(stream, device):
 def _kv_check(t, name, dtype, shape):
     """t is a contiguous tensor of this type and shape; its address."""
     try:
-        if t.dtype == dtype and t.shape == shape and t.is_contiguous():
+        if t.dtype is dtype and t.shape == shape and t.is_contiguous():
             return t.data_ptr()
     except AttributeError:
         raise TypeError(f"{name} must be a torch.Tensor") from None
@@ -451,18 +451,27 @@ def _kv_check(t, name, dtype, shape):
 
 def _kv_table(t, name, rows):
     """t is a contiguous int32 table [rows (or any), X]; its address and sizes."""
+    i32 = _kv()[0].int32
     try:
         n, width = t.shape
+        if t.dtype is i32 and (rows is None or n == rows) and t.is_contiguous():
+            return t.data_ptr(), n, width
     except (AttributeError, ValueError):
         raise (ValueError if hasattr(t, "shape") else TypeError)(f"{name} must be a tensor of two dimensions") from None
-    return _kv_check(t, name, _kv()[0].int32, (n if rows is None else rows, width)), n, width
+    return _kv_check(t, name, i32, (n if rows is None else rows, width)), n, width
 
 
 def _kv_workspace(t):
     """Address and bytes of a workspace (None: none)."""
     if t is None:
         return None, 0
-    return _kv_check(t, "workspace", _kv()[0].uint8, getattr(t, "shape", None)), t.numel()
+    u8 = _kv()[0].uint8
+    try:
+        if t.dtype is u8 and t.is_contiguous():
+            return t.data_ptr(), t.numel()
+    except AttributeError:
+        pass
+    return _kv_check(t, "workspace", u8, getattr(t, "shape", None)), t.numel()
 
 
 def _f32(x):
@@ -531,7 +540,7 @@ def _kv_windows(rows, block_table, seq_of_row, row_start, row_end):
 def _kv_outputs(q, shape, out, lse):
     """Addresses of out and lse (None: none)."""
     return (_kv_check(out, "out", q.dtype, shape),
-            None if lse is None else _kv_check(lse, "lse", _kv()[0].float32, shape[:2]))
+            None if lse is None else _kv_check(lse, "lse", _kv()[0].float32, (shape[0], shape[1])))
 
 
 def mqa_kv_attention_decode(q, k_pages, v_pages, block_table, seq_of_row, row_start, row_end, out, workspace,
@@ -700,29 +709,38 @@ def _kv_tensor(t, name, dtype, dims):
     return shape, stride
 
 
+def _kv_bytes(t, name, u8, shape):
+    """Address and strides of page, position and head of uint8 t of this shape, a head's bytes contiguous."""
+    try:
+        if t.dtype is u8 and t.shape == shape:
+            page, pos, head, element = t.stride()
+            if element == 1 or not t.numel():
+                return t.data_ptr(), page, pos, head
+    except AttributeError:
+        pass
+    got, _ = _kv_tensor(t, name, u8, 4)
+    raise ValueError(f"{name} must be {list(shape)}, got {list(got)}")
+
+
 def _kv_cache_fp4(D, k_pages, k_scale, v_pages, v_scale):
     """mqa_kv_cache_fp4 of codes [P, 64, Hkv, D / 2] and scales [P, 64, Hkv, D / 32] (v_pages None: keys only), and Hkv."""
     u8 = _kv()[0].uint8
-    shape, k = _kv_tensor(k_pages, "k_pages", u8, 4)
-    P, page, heads, _ = shape
-    if page != 64 or shape[3] != D // 2 or heads < 1:
+    try:
+        P, page, heads, half = shape = k_pages.shape
+    except (AttributeError, ValueError):
+        shape, _ = _kv_tensor(k_pages, "k_pages", u8, 4)
+        P, page, heads, half = shape
+    if page != 64 or half != D // 2 or heads < 1:
+        _kv_tensor(k_pages, "k_pages", u8, 4)
         raise ValueError(f"k_pages must be [P, 64, Hkv, {D // 2}], got {list(shape)}")
     scales = (P, 64, heads, D // 32)
-    got, ks = _kv_tensor(k_scale, "k_scale", u8, 4)
-    if got != scales:
-        raise ValueError(f"k_scale must be {list(scales)}, got {list(got)}")
-    v = vs = (0, 0, 0)
-    v_ptr = vs_ptr = 0
-    if v_pages is not None:
-        got, v = _kv_tensor(v_pages, "v_pages", u8, 4)
-        if got != shape:
-            raise ValueError(f"v_pages must be {list(shape)}, got {list(got)}")
-        got, vs = _kv_tensor(v_scale, "v_scale", u8, 4)
-        if got != scales:
-            raise ValueError(f"v_scale must be {list(scales)}, got {list(got)}")
-        v_ptr, vs_ptr = v_pages.data_ptr(), v_scale.data_ptr()
-    return _KV_CACHE_FP4.pack(k_pages.data_ptr(), v_ptr, k_scale.data_ptr(), vs_ptr, *k[:3], *v[:3], *ks[:3], *vs[:3], P,
-                              heads, D), heads
+    k, k0, k1, k2 = _kv_bytes(k_pages, "k_pages", u8, shape)
+    ks, ks0, ks1, ks2 = _kv_bytes(k_scale, "k_scale", u8, scales)
+    if v_pages is None:
+        return _KV_CACHE_FP4.pack(k, 0, ks, 0, k0, k1, k2, 0, 0, 0, ks0, ks1, ks2, 0, 0, 0, P, heads, D), heads
+    v, v0, v1, v2 = _kv_bytes(v_pages, "v_pages", u8, shape)
+    vs, vs0, vs1, vs2 = _kv_bytes(v_scale, "v_scale", u8, scales)
+    return _KV_CACHE_FP4.pack(k, v, ks, vs, k0, k1, k2, v0, v1, v2, ks0, ks1, ks2, vs0, vs1, vs2, P, heads, D), heads
 
 
 def _kv_query_fp4(q, scale, k_pages, k_scale, v_pages, v_scale):
@@ -742,7 +760,7 @@ def mqa_kv_attention_decode_fp4(q, k_pages, k_scale, v_pages, v_scale, block_tab
     D / 2] (two E2M1 codes to a byte, the even dim low), k_scale and v_scale uint8 [P, 64, Hkv, D / 32] (UE8M0);
     page, position and head strides are free. The other arguments, and the workspace, as there. Capturable."""
     query, shape, cache = _kv_query_fp4(q, scale, k_pages, k_scale, v_pages, v_scale)
-    rc = lib().mqa_kv_attention_decode_fp4(
+    rc = (_lib or lib()).mqa_kv_attention_decode_fp4(
         query, cache, *_kv_windows(shape[:1], block_table, seq_of_row, row_start, row_end), *_kv_outputs(q, shape, out, lse),
         *_kv_workspace(workspace), _kv_stream(stream, q.device))
     _rc(rc, "mqa_kv_attention_decode_fp4")
@@ -753,7 +771,7 @@ def mqa_kv_attention_selected_fp4(q, k_pages, k_scale, v_pages, v_scale, slots, 
     """mqa_kv_attention_selected over a cache in 4 bits (as in mqa_kv_attention_decode_fp4). Capturable."""
     query, shape, cache = _kv_query_fp4(q, scale, k_pages, k_scale, v_pages, v_scale)
     lists, _, K = _kv_table(slots, "slots", shape[0])
-    rc = lib().mqa_kv_attention_selected_fp4(
+    rc = (_lib or lib()).mqa_kv_attention_selected_fp4(
         query, cache, lists, _kv_check(count, "count", _kv()[0].int32, shape[:1]), K, *_kv_outputs(q, shape, out, lse),
         *_kv_workspace(workspace), _kv_stream(stream, q.device))
     _rc(rc, "mqa_kv_attention_selected_fp4")
