@@ -50,7 +50,9 @@ typedef struct mqa_kv_cache_fp4 {
 } mqa_kv_cache_fp4;
 
 /* mqa_kv_attention_decode over a cache in 4 bits (the same workspace:
- * mqa_kv_attention_decode_workspace_bytes). */
+ * mqa_kv_attention_decode_workspace_bytes). Its contents need not outlive the call,
+ * but calls that may run at the same time (on two streams, or in two captured
+ * graphs that are replayed side by side) need one each. */
 int32_t mqa_kv_attention_decode_fp4(const mqa_kv_query* q, const mqa_kv_cache_fp4* cache, const int32_t* block_table,
                                     int64_t num_seqs, int64_t max_pages, const int32_t* seq_of_row,
                                     const int32_t* row_start, const int32_t* row_end, void* out, float* lse,
