@@ -922,9 +922,22 @@ void decode_on(KvFp4Args a, hipStream_t st) {
 
 template <class T, int D, int NQ, int NH>
 void selected_on(const KvFp4Args& a, hipStream_t st) {
-  const int64_t items = a.Q * (a.Hkv / NH) * kv_head_groups(D, a.G) * a.splits;
-  const unsigned grid = static_cast<unsigned>((items + 7) / 8 * 8);
-  kv_selected_fp4_kernel<T, D, NQ, NH><<<dim3(grid), dim3(64 * ring_waves(D, NQ, NH)), 0, st>>>(a);
+  // A launch's threads are counted in 32 bits, and workgroups have up to 512: where one query head has a key head to itself, rows
+  // beyond 2^23 go in a second launch. (Lists in several parts have 512 workgroups in all, and one launch.)
+  constexpr int kGroupThreads = 64 * ring_waves(D, NQ, NH);
+  const int64_t of_row = static_cast<int64_t>(a.Hkv / NH) * kv_head_groups(D, a.G) * a.splits;
+  const int64_t most = 0xFFFFFFFFll / kGroupThreads / 8 * 8 / of_row;
+  KvFp4Args part = a;
+  for (int64_t at = 0; at < a.Q; at += most) {
+    part.Q = a.Q - at < most ? a.Q - at : most;
+    part.q = a.q + at * a.q_row;
+    part.slots = a.K == 0 ? a.slots : a.slots + at * a.K;
+    part.count = a.count + at;
+    part.out = static_cast<char*>(a.out) + at * a.H * D * 2;
+    part.lse = a.lse == nullptr ? nullptr : a.lse + at * a.H;
+    const unsigned grid = static_cast<unsigned>((part.Q * of_row + 7) / 8 * 8);
+    kv_selected_fp4_kernel<T, D, NQ, NH><<<dim3(grid), dim3(kGroupThreads), 0, st>>>(part);
+  }
   if (a.splits > 1)
     kv_selected_fp4_join_kernel<T, D, NQ, NH, 1>
         <<<dim3(static_cast<unsigned>((a.Q * a.H + kWaves - 1) / kWaves)), dim3(kThreads), 0, st>>>(a);
