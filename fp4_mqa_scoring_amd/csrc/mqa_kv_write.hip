@@ -305,8 +305,11 @@ void write_on(const KvWriteArgs& a, hipStream_t st) {
   // what comes before the first block (position, angles, block table) is then paid once for them (8192 rows of 48
   // heads: 47.5 us by one row, 46.3 by two, 50.2 by four, whose workgroups end too unevenly).
   int64_t rows = 1;
-  // (A group's rows lie within 32 bits of each other: at least 256 times as many rows fit the card's memory.)
   while (rows < kWriteRows && a.T >= 512 * rows && (rows < 2 || blocks_of(rows) < 2 * kWaves)) rows *= 2;
+  // The kernel's offsets inside a group are held in 32 bits. Managed memory may be larger than the card's, and rows of it farther apart.
+  int64_t widest = 0;
+  for (const int64_t row : {a.q.x_row, a.q.out_row, a.k.x_row, a.k.out_row, a.v.x_row}) widest = row > widest ? row : widest;
+  while (rows > 1 && rows * widest > 0x7FFFFFFF) rows /= 2;
   // few rows: their heads over several workgroups, four to a compute unit (1001 rows of 18 heads of 256 dims: 8.1 us,
   // 9.9 with eight: workgroups start at about one in a nanosecond)
   const int64_t passes = (blocks_of(rows) + kWaves - 1) / kWaves, groups = (a.T + rows - 1) / rows;
