@@ -1,5 +1,5 @@
 // What the attention kernels over the paged key-value cache share (gfx950): matrix operands and a wave's running
-// sums, the joining of waves and of partial results, the plan that cuts a batch into shares. The mathematics
+// sums, the joining of partial results, the plan that cuts a batch into shares. The mathematics
 // stands at the head of mqa_kv_attn.hip (16- and 8-bit caches); mqa_kv_fp4.hip has the caches in 4 bits.
 #pragma once
 
@@ -147,7 +147,6 @@ __device__ __forceinline__ void settle(v4f (&s)[N][2]) {
 template <class T, bool E4M3, int D, int NQ, int POS = 32, bool QL = false, int SLACK = 0>
 struct Wave {
   static constexpr int kPositions = POS;
-  static constexpr int kQueries = NQ;
   static constexpr int kBytes = E4M3 ? 1 : 2;
   static constexpr int kChunks = D / 32;                 // matrix steps over the dims
   static constexpr int kLoads = D * kBytes / 64;         // 16-byte key loads per lane and position
@@ -363,114 +362,8 @@ struct Wave {
   }
 };
 
-// --- up to 16 heads: keys and values in registers ---------------------------------
-//
-// The four waves of a workgroup take every fourth tile of 32 positions. The next
-// tile's keys are loaded into the registers that the first product has just read,
-// its values into those that the second has.
-
 // A barrier for what lies in LDS alone: loads from memory and stores to it that are on their way stay so.
 __device__ __forceinline__ void lds_barrier() { __asm__ __volatile__("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
-
-// Joins a workgroup's waves' results in LDS and writes the heads' outputs, or their partial
-// sums where part_o is not null. `bad`: an invalid page or slot was met.
-template <class T, int D, int WAVES = kWaves>
-struct Merge {
-  static constexpr int kPart = D < 128 ? D : 128;   // dims of a head at a time, so that LDS holds two workgroups or more
-  static constexpr int kPitch = kPart + 4;
-  float o[WAVES][16][kPitch];
-  float2 ml[WAVES][16];
-  float2 fin[16];
-
-  template <class W>
-  __device__ __forceinline__ void run(W& w, bool bad, int rows, float v_scale, char* out, float* lse, float* part_o,
-                                      float2* part_ml) {
-    const int wave = threadIdx.x >> 6;
-    __syncthreads();   // the previous use of this memory is over
-    const float mine = groups_sum(w.l[0]);
-    if (w.grp == 0) ml[wave][w.col] = make_float2(w.m[0], bad ? __builtin_nanf("") : mine);
-    __syncthreads();
-    float2 x[WAVES];
-    float top = -__builtin_inff(), total = 0.0f;
-#pragma unroll
-    for (int i = 0; i < WAVES; ++i) {
-      x[i] = ml[i][w.col];
-      top = fmaxf(top, x[i].x);
-    }
-    const float ref = top == -__builtin_inff() ? 0.0f : top;
-#pragma unroll
-    for (int i = 0; i < WAVES; ++i) total += x[i].y * __builtin_amdgcn_exp2f(x[i].x - ref);
-    const float f = __builtin_amdgcn_exp2f(w.m[0] - ref);
-    if (wave == 0 && w.grp == 0) fin[w.col] = make_float2(top, total);
-    constexpr int kT = kPart / 16;   // matrix tiles of a part
-#pragma unroll
-    for (int t0 = 0; t0 < W::kDims; t0 += kT) {
-      if (t0 > 0) __syncthreads();
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int t = 0; t < kT; t += 4)
-          *reinterpret_cast<v4f*>(&o[wave][w.col][(4 * w.grp + i) * kT + t]) =
-              v4f{w.o[0][t0 + t][i] * f, w.o[0][t0 + t + 1][i] * f, w.o[0][t0 + t + 2][i] * f,
-                  w.o[0][t0 + t + 3][i] * f};
-      __syncthreads();
-      for (int e = threadIdx.x; e < 16 * kPart / 4; e += 64 * WAVES) {
-        const int head = e / (kPart / 4), at = 4 * (e % (kPart / 4));
-        const int d = at / kT * W::kDims + t0 + at % kT;
-        if (head >= rows) continue;
-        v4f sum = *reinterpret_cast<const v4f*>(&o[0][head][at]);
-#pragma unroll
-        for (int i = 1; i < WAVES; ++i) sum += *reinterpret_cast<const v4f*>(&o[i][head][at]);
-        const float2 e2 = fin[head];
-        if (part_o != nullptr) {
-          *reinterpret_cast<v4f*>(part_o + static_cast<int64_t>(head) * D + d) = sum;
-          if (d == 0) part_ml[head] = e2;
-        } else {
-          const float inv = v_scale / e2.y;
-          const v2u y = {T::pack(sum[0] * inv, sum[1] * inv), T::pack(sum[2] * inv, sum[3] * inv)};
-          *reinterpret_cast<v2u*>(out + (static_cast<int64_t>(head) * D + d) * 2) = y;
-          if (d == 0 && lse != nullptr) lse[head] = lse_of<T>(e2.x, e2.y);
-        }
-      }
-    }
-  }
-};
-
-// This wave's tiles t, t + kWaves, ... below t_hi; range(t, &lo, &hi) gives the positions of a tile that count.
-template <class W, class KEYS, class VALUES, class RANGE>
-__device__ __forceinline__ void run_tiles(W& w, int t, int t_hi, float c, KEYS&& load_keys, VALUES&& load_values,
-                                          RANGE&& range) {
-  if (t >= t_hi) return;
-  load_keys(t);
-  load_values(t);
-  while (true) {
-    const int tn = t + kWaves;
-    const bool more = tn < t_hi;
-    int lo, hi;
-    range(t, &lo, &hi);
-    const bool edge = lo > 0 || hi < W::kPositions;
-    uint32_t inside = 0xFFu;
-    if (edge) {
-      inside = 0;
-#pragma unroll
-      for (int j = 0; j < W::kMine; ++j) inside |= (w.mine(j) >= lo && w.mine(j) < hi ? 1u : 0u) << j;
-    }
-    v4f s[W::kQueries][W::kTiles];
-    typename W::P p[W::kQueries];
-    w.scores(s);
-    if (more) load_keys(tn);
-    w.weights(s, c, edge, inside, p);
-    if (edge) w.clear_outside(inside);
-    w.add_values(p);
-    if (!more) break;
-    load_values(tn);
-    t = tn;
-  }
-}
-
-// Positions of a register tile: 32, or 16 where D = 256 in 16 bits would need more registers than
-// two waves per SIMD leave.
-constexpr int register_tile(int D, bool e4m3) { return D == 256 && !e4m3 ? 16 : 32; }
 
 // Offset of a slot in units of 16 bytes, of which the strides are multiples. A page's is below 2^36 bytes, 63
 // positions' below 2^31: one 32-bit multiplication and one of 24 bits.
@@ -740,30 +633,6 @@ __device__ __forceinline__ int64_t join_head(const KvAttnArgs& a) {
   return head < a.Q * a.H ? head : -1;
 }
 
-template <class T, int D, int WAVES>
-__global__ void __launch_bounds__(kThreads) kv_decode_join_kernel(KvAttnArgs a, int per, int groups) {
-  const int64_t head = join_head<WAVES>(a);
-  if (head < 0) return;
-  const int64_t r = head / a.H;
-  const int h = static_cast<int>(head - r * a.H);
-  const int64_t before = a.prefix[r], n = a.prefix[r + 1] - before, all = a.prefix[a.Q];
-  if (n == 0) {
-    int code;
-    row_pages(a, r, &code);
-    fill_row<T, D>(a, head, code != 0, WAVES > 1 ? threadIdx.x : threadIdx.x & 63, 64 * WAVES);
-    return;
-  }
-  const int qg = (a.G + per - 1) / per;
-  const int64_t gh = static_cast<int64_t>(a.Hkv) * qg;
-  const int64_t share = unit_share(a, all * gh, groups);
-  const int kvh = h / a.G, in_kv = h - kvh * a.G;
-  const int64_t from = before * gh + (static_cast<int64_t>(kvh) * qg + in_kv / per) * n;
-  const int64_t w0 = from / share, w1 = (from + n - 1) / share;
-  if (w0 == w1) return;   // one workgroup had all of it and wrote the output
-  // the first part is its workgroup's last one (slot 2 w + 1), the others are first ones (slot 2 w)
-  join_row<T, D, WAVES>(a, head, in_kv % per, a.G < per ? a.G : per, w1 - w0 + 1, 2 * w0 + 1, 2 * w0, 2);
-}
-
 // --- selected form ------------------------------------------------------------
 
 // Slots of one split of a row with n of them: whole tiles, the same for every split.
@@ -802,21 +671,6 @@ struct ListPart {
     return from < to;
   }
 };
-
-template <class T, int D, int WAVES>
-__global__ void __launch_bounds__(kThreads) kv_selected_join_kernel(KvAttnArgs a, int per) {
-  const int64_t head = join_head<WAVES>(a);
-  if (head < 0) return;
-  const int64_t r = head / a.H;
-  const int h = static_cast<int>(head - r * a.H);
-  const int64_t n = a.count[r];
-  if (n <= 0 || n > a.K) return;   // written already
-  const int qg = (a.G + per - 1) / per;
-  const int kvh = h / a.G, in_kv = h - kvh * a.G;
-  const int64_t share = split_share(n, a.splits);
-  const int64_t slot = ((r * a.Hkv + kvh) * qg + in_kv / per) * a.splits;
-  join_row<T, D, WAVES>(a, head, in_kv % per, a.G < per ? a.G : per, (n + share - 1) / share, slot, slot, 1);
-}
 
 // Heads up to which a whole workgroup joins one (a long sequence has hundreds of parts); beyond, there are
 // few parts each and a wave does.
