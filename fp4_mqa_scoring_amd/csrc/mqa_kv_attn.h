@@ -446,7 +446,8 @@ __global__ void __launch_bounds__(1024) kv_plan_kernel(KvAttnArgs a) {
 __device__ __forceinline__ int64_t unit_share(const KvAttnArgs& a, int64_t units, int64_t groups) {
   const int64_t equal = (units + groups - 1) / groups;
   const uint32_t some = static_cast<uint32_t>(units < 1 << 24 ? units : 1 << 24);
-  const uint32_t x = static_cast<uint32_t>(static_cast<uint64_t>(some) * a.join_cost >> 16);   // below 2^23
+  // At most 2^24 times a cost of 2^23 at most (4 bits, many key heads): x is at most 2^31, and s at most 2^15.
+  const uint32_t x = static_cast<uint32_t>(static_cast<uint64_t>(some) * a.join_cost >> 16);
   const int64_t s = x < 2 ? 1 : 1 << ((32 - __builtin_clz(x - 1)) >> 1);   // the least with 2 s^2 >= x
   return equal > s ? equal : s;
 }
@@ -469,7 +470,8 @@ struct Plan {
   // Returns the prefix (in LDS, or the one that kv_plan_kernel left in the workspace).
   __device__ __forceinline__ const int64_t* make(const KvAttnArgs& a) {
     if (a.Q > kKvPlanRows) return a.prefix;
-    // one round trip to memory, less than another launch
+    // A thread's rows one after another, two trips to memory each, the sequence and then the window: two where the batch
+    // has one row, up to eight with four waves and four rows or more. (One short sequence: 4,400 clocks with what follows here.)
     constexpr int kPer = kKvPlanRows / (64 * WAVES);
     const bool first = blockIdx.x == 0;
     int64_t n[kPer], sum = 0;

@@ -3,8 +3,9 @@
 //
 // Mathematics. y = x / sqrt(mean(x^2) + eps) * (w + offset); pair (a, b) of dims turns by
 // t = position * inv_freq: (a cos t - b sin t, b cos t + a sin t). t is taken in 64 bits as
-// turns of a circle, of which the fraction alone goes on in 32: a position of a million
-// times a frequency of one has lost 0.06 rad in 32 bits, here 2^-31.
+// turns of a circle, of which the fraction alone, 1/2 at most, goes on in 32: its rounding
+// is an angle of pi 2^-25 at most, and the product's own 2^-51 of t. (In 32 bits throughout, an
+// angle of a million has neighbours 0.06 rad away and is off by half of that.)
 //
 // Bound by memory: a head's numbers are read and written once. A lane holds 8 neighbouring
 // dims of a head (16 bytes), D / 8 lanes a head; sums go over them by lane permutes, and a
