@@ -93,6 +93,8 @@ typedef struct mqa_kv_new {
  * maps outside [0, P_phys) (MQA_STATUS_BAD_PAGE). The queries of such rows are
  * turned all the same. Rows must go to distinct slots: of two that share one,
  * what it holds afterwards is unspecified (no access leaves the cache).
+ * Overlaps of the queries' output are refused as above; the cache must lie apart
+ * from every other tensor, which is not looked at.
  */
 int32_t mqa_kv_append(const mqa_kv_new* rows, const mqa_kv_rows* q, const mqa_kv_cache* cache, void* stream);
 

@@ -89,6 +89,8 @@ const char* taken() {   // what was recorded since the last call of it
 def recorded(calls, where):
     """(return code, launches) of every call; the stand-in is built in `where`."""
     from fp4_mqa_scoring_amd import build
+    if not os.path.exists(build.LIB):
+        build.build()
     src, lib = os.path.join(str(where), "runtime.hip"), os.path.join(str(where), "runtime.so")
     if not os.path.exists(lib):
         with open(src, "w") as f:
